@@ -24,13 +24,34 @@ STATUS = {0: "FP4Q_OK", -1: "FP4Q_E_NULL", -2: "FP4Q_E_ARG", -3: "FP4Q_E_SHAPE",
 # every symbol include/fp4q.h declares
 EXPORTS = ("fp4q_workspace_bytes", "fp4q_quantize", "fp4q_quantize_noalloc",
            "fp4q_quantize_relaxed", "fp4q_dequantize", "fp4q_error", "fp4q_status_string",
-           "fp4q_abi_version")
+           "fp4q_abi_version", "fp4q_kv_write", "fp4q_kv_read", "fp4q_attend",
+           "fp4q_attend_workspace_bytes")
 
 
 class fp4q_spec(C.Structure):
     _fields_ = [("format", C.c_int32), ("block", C.c_int32), ("scale_rule", C.c_int32),
                 ("objective", C.c_int32), ("sweep_lo", C.c_int32), ("sweep_hi", C.c_int32),
                 ("rotate", C.c_int32), ("global_scale_given", C.c_int32)]
+
+
+class fp4q_kv_cache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("k_scales", C.c_void_p), ("k_global", C.c_void_p),
+                ("v_codes", C.c_void_p), ("v_scales", C.c_void_p), ("v_global", C.c_void_p),
+                ("num_pages", C.c_int64), ("kv_heads", C.c_int32), ("page_size", C.c_int32),
+                ("head_dim", C.c_int32), ("reserved", C.c_int32),
+                ("code_page", C.c_int64), ("code_head", C.c_int64), ("code_token", C.c_int64),
+                ("scale_page", C.c_int64), ("scale_head", C.c_int64), ("scale_token", C.c_int64)]
+
+
+class fp4q_attention(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_row_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("out", C.c_void_p), ("out_row_stride", C.c_int64), ("out_head_stride", C.c_int64),
+                ("lse", C.c_void_p), ("q_starts", C.c_void_p), ("kv_lens", C.c_void_p),
+                ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("total_q", C.c_int64),
+                ("table_len", C.c_int32), ("batch", C.c_int32), ("max_q", C.c_int32),
+                ("max_kv", C.c_int32), ("q_heads", C.c_int32), ("dtype", C.c_int32),
+                ("causal", C.c_int32), ("window", C.c_int32), ("scale", C.c_float),
+                ("reserved", C.c_int32)]
 
 
 class Fp4qError(RuntimeError):
@@ -66,6 +87,15 @@ def _lib_handle():
         L.fp4q_error.restype = C.c_int
         L.fp4q_error.argtypes = [sp, vp, i32, i64, i64, vp, vp, vp, vp, vp, sz,
                                  C.POINTER(C.c_double), vp]
+        kp, ap = C.POINTER(fp4q_kv_cache), C.POINTER(fp4q_attention)
+        L.fp4q_kv_write.restype = C.c_int
+        L.fp4q_kv_write.argtypes = [sp, kp, vp, vp, i32, i64, i64, i64, i64, i64, vp, vp]
+        L.fp4q_kv_read.restype = C.c_int
+        L.fp4q_kv_read.argtypes = [sp, kp, vp, i64, vp, vp, i32, vp]
+        L.fp4q_attend_workspace_bytes.restype = sz
+        L.fp4q_attend_workspace_bytes.argtypes = [sp, kp, ap]
+        L.fp4q_attend.restype = C.c_int
+        L.fp4q_attend.argtypes = [sp, kp, ap, vp, sz, vp]
         L.fp4q_status_string.restype = C.c_char_p
         L.fp4q_status_string.argtypes = [C.c_int]
         L.fp4q_abi_version.restype = C.c_int
@@ -385,3 +415,263 @@ def error(x, codes, scales, global_scale, format=FP4Q_NVFP4, rotate=0, importanc
     rows, cols = x2.shape
     ws = workspace if workspace is not None else alloc_workspace(spec, rows, cols, x.device)
     return fp4q_error(spec, x2, importance, codes, scales, global_scale, ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit KV cache
+# ---------------------------------------------------------------------------
+
+def _cache_tensor(name, t, shape, device, require_cuda):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    _check_device(name, t, device, require_cuda)
+    if t.dtype != torch.uint8:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected torch.uint8")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {shape}")
+    if t.stride(3) != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+class KvCache:
+    """A 4-bit KV cache: K and V as codes uint8 [pages, kv_heads, page_size,
+    head_dim / 2] and scales uint8 [pages, kv_heads, page_size, head_dim /
+    block] (any strides, the last dimension contiguous, K's and V's alike) and
+    one global scale float32 [1] each (None for MXFP4).  The tensors are the
+    caller's; this handle checks them once, keeps references to them and passes
+    their addresses on.  A contiguous cache [B, H, T, D] is one of B pages of T
+    tokens.  `scale_rule`, `window` and `rotate` say how rows are written (and
+    `rotate` how they are read)."""
+
+    def __init__(self, k_codes, k_scales, k_global, v_codes, v_scales, v_global,
+                 format=FP4Q_NVFP4, scale_rule=FP4Q_SCALE_ABSMAX, window=None, rotate=0,
+                 require_cuda=True):
+        if format not in (FP4Q_NVFP4, FP4Q_MXFP4):
+            raise ValueError("a KV cache is NVFP4 or MXFP4")
+        self.spec = make_spec(format, scale_rule, FP4Q_OBJ_MSE, window, rotate,
+                              global_scale_given=format != FP4Q_MXFP4)
+        if not isinstance(k_codes, torch.Tensor):
+            raise TypeError("k_codes must be a torch tensor")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, kv_heads, page_size, head_dim / 2]")
+        pages, heads, page, half = k_codes.shape
+        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page, 2 * half
+        if self.head_dim not in (64, 128, 256):
+            raise ValueError(f"head_dim {self.head_dim} is not supported; use 64, 128 or 256")
+        if heads < 1 or page < 1:
+            raise ValueError("a KV cache needs at least one head and one token per page")
+        self.device = k_codes.device
+        _check_device("k_codes", k_codes, None, require_cuda)
+        small = (pages, heads, page, self.head_dim // self.spec.block)
+        for name, t, shape in (("k_codes", k_codes, (pages, heads, page, half)),
+                               ("v_codes", v_codes, (pages, heads, page, half)),
+                               ("k_scales", k_scales, small), ("v_scales", v_scales, small)):
+            _cache_tensor(name, t, shape, self.device, require_cuda)
+        for name, t in (("k_global", k_global), ("v_global", v_global)):
+            _check_tensor(name, t, _F32, 1, self.device, require_cuda,
+                          optional=format == FP4Q_MXFP4)
+        if k_codes.stride() != v_codes.stride() or k_scales.stride() != v_scales.stride():
+            raise ValueError("K and V of a cache must have the same strides")
+        self.tensors = (k_codes, k_scales, k_global, v_codes, v_scales, v_global)
+        ptr = [None if t is None else t.data_ptr() for t in self.tensors]
+        self.struct = fp4q_kv_cache(*ptr, pages, heads, page, self.head_dim, 0,
+                                    *k_codes.stride()[:3], *k_scales.stride()[:3])
+        self._spec, self._struct = C.byref(self.spec), C.byref(self.struct)
+
+
+def alloc_kv_cache(pages, kv_heads, page_size, head_dim, k_global=None, v_global=None,
+                   format=FP4Q_NVFP4, scale_rule=FP4Q_SCALE_ABSMAX, window=None, rotate=0,
+                   device="cuda"):
+    """A zeroed cache.  The global scales (numbers or tensors, NVFP4 only) are
+    those of the tensors that will be written, max|x| / 1536 for instance."""
+    block = 32 if format == FP4Q_MXFP4 else 16
+    t = []
+    for g in (k_global, v_global):
+        if format == FP4Q_MXFP4:
+            g = None
+        elif g is None:
+            raise ValueError("an NVFP4 cache needs both global scales")
+        else:
+            g = torch.as_tensor(g, dtype=torch.float32, device=device).reshape(1).clone()
+        t += [torch.zeros(pages, kv_heads, page_size, head_dim // 2, dtype=torch.uint8, device=device),
+              torch.zeros(pages, kv_heads, page_size, head_dim // block, dtype=torch.uint8, device=device),
+              g]
+    return KvCache(*t, format=format, scale_rule=scale_rule, window=window, rotate=rotate)
+
+
+def _rows(name, t, rows, heads, dim, device, dtypes=_X):
+    """A [rows, heads, dim] tensor whose last dimension is contiguous; returns
+    its row and head strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, but the cache is on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected " + " or ".join(map(str, dtypes)))
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected "
+                         f"[{'rows' if rows is None else rows}, {heads}, {dim}]")
+    st = t.stride()
+    if st[2] != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return st[0], st[1]
+
+
+def _ints(name, t, dtype, device, dim=1):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, but the cache is on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    if t.dim() != dim or (t.numel() > 0 and t.stride(dim - 1) != 1):
+        raise ValueError(f"{name} must have {dim} dimension(s), the last one contiguous")
+    return t.data_ptr()
+
+
+class _on:
+    """The device of the cache as the current one, and the stream of the call
+    (torch's current one there unless given) as torch's current one, so that
+    what is allocated for the call belongs to that stream."""
+
+    def __init__(self, device, stream):
+        self.device, self.given = device, stream
+        self.inner = []
+
+    def __enter__(self):
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            self.inner.append(torch.cuda.device(self.device))
+            self.inner[-1].__enter__()
+        if self.given is not None:
+            self.inner.append(torch.cuda.stream(self.given))
+            self.inner[-1].__enter__()
+            return self.given.cuda_stream
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        while self.inner:
+            self.inner.pop().__exit__(*exc)
+
+
+def kv_write(cache, k, v, slots, stream=None):
+    """Quantize k and v, float32 or bfloat16 [tokens, kv_heads, head_dim] (last
+    dimension contiguous), into the cache at `slots` (int64 [tokens]; a
+    negative or too large slot skips its token)."""
+    dev = cache.device
+    p = _ints("slots", slots, torch.int64, dev)
+    n = slots.shape[0]
+    ks = _rows("k", k, n, cache.heads, cache.head_dim, dev)
+    vs = _rows("v", v, n, cache.heads, cache.head_dim, dev)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    with _on(dev, stream) as st:
+        _check("fp4q_kv_write", _lib_handle().fp4q_kv_write(
+            cache._spec, cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k), n, *ks, *vs, p, st))
+
+
+def kv_read(cache, slots, dtype=torch.float32, stream=None):
+    """The values of the rows at `slots` (int64 [tokens]): (k, v), each
+    [tokens, kv_heads, head_dim] of `dtype`, un-rotated."""
+    dev = cache.device
+    p = _ints("slots", slots, torch.int64, dev)
+    if dtype not in _X:
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    with _on(dev, stream) as st:
+        k = torch.empty(slots.shape[0], cache.heads, cache.head_dim, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        _check("fp4q_kv_read", _lib_handle().fp4q_kv_read(
+            cache._spec, cache._struct, p, slots.shape[0], k.data_ptr(), v.data_ptr(),
+            _dtype_code(k), st))
+    return k, v
+
+
+def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, scale, out, lse):
+    """The call's fp4q_attention, from checked tensors."""
+    dev = cache.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a torch tensor [total_q, q_heads, head_dim]")
+    total, heads = q.shape[0], q.shape[1]
+    if heads < 1 or heads % cache.heads:
+        raise ValueError(f"q has {heads} heads; expected a multiple of the cache's {cache.heads}")
+    qs = _rows("q", q, total, heads, cache.head_dim, dev)
+    lens = _ints("kv_lens", kv_lens, torch.int32, dev)
+    batch = kv_lens.shape[0]
+    starts = None
+    if q_starts is not None:
+        starts = _ints("q_starts", q_starts, torch.int32, dev)
+        if q_starts.shape[0] != batch + 1:
+            raise ValueError(f"q_starts has {q_starts.shape[0]} entries; expected batch + 1 = {batch + 1}")
+        if max_q is None:
+            max_q = total
+    else:
+        each = total // batch if batch else 0
+        if each * batch != total or (max_q is not None and max_q != each):
+            raise ValueError("without q_starts, q must hold max_q rows for each sequence")
+        max_q = each
+    table, stride, entries = None, 0, 0
+    if block_table is not None:
+        table = _ints("block_table", block_table, torch.int32, dev, 2)
+        if block_table.shape[0] != batch:
+            raise ValueError(f"block_table has {block_table.shape[0]} rows; expected {batch}")
+        if cache.page_size % 16:
+            raise ValueError("with a block_table the page size must be a multiple of 16")
+        stride, entries = block_table.stride(0), block_table.shape[1]
+    if max_kv is None:
+        max_kv = cache.page_size * (entries if table is not None else 1)
+    os = _rows("out", out, total, heads, cache.head_dim, dev, (q.dtype,))
+    if lse is not None:
+        _check_tensor("lse", lse, _F32, total * heads, dev, require_cuda=False)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    return fp4q_attention(q.data_ptr(), *qs, out.data_ptr(), *os,
+                          None if lse is None else lse.data_ptr(), starts, lens, table, stride,
+                          total, entries, batch, max_q, max_kv, heads, _dtype_code(q), int(causal),
+                          window, scale, 0)
+
+
+def attend_workspace_bytes(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None,
+                           max_q=None, causal=True, window=0):
+    """Bytes that `attend` of these arguments needs as its workspace (only
+    their shapes and types matter)."""
+    call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, None, q, None)
+    return int(_lib_handle().fp4q_attend_workspace_bytes(cache._spec, cache._struct, C.byref(call)))
+
+
+def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_q=None,
+           causal=True, window=0, scale=None, return_lse=False, out=None, workspace=None, stream=None):
+    """Attention of the queries q, float32 or bfloat16 [total_q, q_heads,
+    head_dim], over the cache; query head h reads KV head h // (q_heads //
+    kv_heads).  Returns out like q, or (out, lse float32 [total_q, q_heads])
+    with return_lse.
+
+    kv_lens      int32 [batch]: keys of each sequence, its new ones among them.
+    max_kv       a bound on kv_lens (default: what a sequence's pages hold).
+    block_table  int32 [batch, entries]: the pages of each sequence; None:
+                 sequence b is page b (a contiguous cache).
+    q_starts     int32 [batch + 1]: the queries of sequence b are the rows
+                 q_starts[b] : q_starts[b+1]; None: the same number for each.
+    max_q        a bound on the queries of a sequence.
+    causal       the last query of a sequence sees all of its keys, each one
+                 before it one less; False: every query sees all.
+    window       with causal, only the last `window` of those (0: all).
+    scale        of the logits (default head_dim ** -0.5).
+    A query without keys gives zeros and lse -inf.  Rows of no sequence are not
+    written: they stay what they are in `out`, unspecified where it is
+    allocated here.  A given workspace (uint8, attend_workspace_bytes) must
+    not be shared by calls that may run at the same time."""
+    dev = cache.device
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
+        call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window,
+                          scale, out, lse)
+        lib, ref = _lib_handle(), C.byref(call)
+        need = lib.fp4q_attend_workspace_bytes(cache._spec, cache._struct, ref)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif need:
+            _check_tensor("workspace", workspace, _U8, need, dev, require_cuda=False)
+        _check("fp4q_attend", lib.fp4q_attend(
+            cache._spec, cache._struct, ref, workspace.data_ptr() if need else None, need, st))
+    return (out, lse) if return_lse else out

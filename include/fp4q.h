@@ -252,6 +252,137 @@ fp4q_status fp4q_error(const fp4q_spec* spec, const void* x, int32_t x_dtype,
                        const float* global_scale, void* workspace, size_t ws_bytes,
                        double out_host[2], void* stream);
 
+/* ---- the 4-bit KV cache ---------------------------------------------------
+ *
+ * K and V of a cache are two sets of NVFP4 or MXFP4 codes and scales under one
+ * fixed global scale each (MXFP4 has none).  A cache is `num_pages` pages of
+ * `page_size` tokens of `kv_heads` rows of `head_dim` values; slot s is token
+ * s % page_size of page s / page_size.  A contiguous cache [B, H, T, D] is
+ * one of B pages of T tokens.
+ *   k_codes ...  the four byte arrays; row (page, head, token) of the codes is
+ *                head_dim / 2 bytes at page*code_page + head*code_head +
+ *                token*code_token, of the scales head_dim / block bytes at
+ *                page*scale_page + ..., laid out inside a row as
+ *                fp4q_quantize lays out one row.  K and V share the strides.
+ *   k_global, v_global  one fp32 each, the global scale S (NVFP4; may be NULL
+ *                for MXFP4): read at each call, never written.
+ *   head_dim     64, 128 or 256.
+ *   strides      in bytes, non-negative; code strides and bases multiples of
+ *                16, scale strides and bases of 4 (2 for MXFP4 with head_dim
+ *                64); code_token at most 2^20 and scale_token at most 2^20.
+ * spec of the calls below: format NVFP4 or MXFP4 (others:
+ * FP4Q_E_UNSUPPORTED), block, and rotate = 0, or = block for rows that are
+ * stored rotated.  fp4q_kv_write also takes the scale rule and its window;
+ * its objective has to be MSE and global_scale_given 1 (NVFP4).
+ *
+ * What lies on the device is checked there: a slot, a page or a length out of
+ * range is never followed (each entry point says what it gives instead).
+ * Scale bytes of live rows are finite patterns, as the quantizers write them;
+ * rows that no query sees may hold anything. */
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    const float* k_global;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    const float* v_global;
+    int64_t num_pages;
+    int32_t kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+    int32_t reserved; /* 0 */
+    int64_t code_page, code_head, code_token;
+    int64_t scale_page, scale_head, scale_token;
+} fp4q_kv_cache;
+
+/* Quantize the keys and values of `tokens` tokens into the cache.
+ *   k, v     [tokens, kv_heads, head_dim] (dtype FP4Q_F32 or FP4Q_BF16), the
+ *            head_dim values contiguous, token and head strides in elements;
+ *            bases and strides 16-byte aligned.
+ *   slots    int64 [tokens] on the device; a token whose slot is negative or
+ *            not below num_pages * page_size is skipped.  A slot named twice
+ *            in one call ends with blocks of either token.
+ * Every block gets the codes and the scale that fp4q_quantize gives it under
+ * the same spec with the global scale given: ABSMAX, SWEEP and, for NVFP4,
+ * FOUR_OVER_SIX.
+ * Launches one kernel and takes no workspace. */
+fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, const void* k,
+                          const void* v, int32_t dtype, int64_t tokens, int64_t k_token_stride,
+                          int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                          const int64_t* slots, void* stream);
+
+/* Dequantize the rows of `tokens` slots into k and v, each contiguous
+ * [tokens, kv_heads, head_dim] of `dtype` (16-byte aligned), un-rotated when
+ * spec->rotate is set: the values fp4q_dequantize gives.  A slot out of range
+ * reads as zeros. */
+fp4q_status fp4q_kv_read(const fp4q_spec* spec, const fp4q_kv_cache* cache, const int64_t* slots,
+                         int64_t tokens, void* k, void* v, int32_t dtype, void* stream);
+
+/* Attention of packed queries over the cache:
+ *   out_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i),
+ *   lse_i = log sum_j exp(scale q_i.k_j),
+ * over the keys j that query i sees.  Query head h reads KV head
+ * h / (q_heads / kv_heads).
+ *   q, out   [total_q, q_heads, head_dim] of `dtype`, the head_dim values
+ *            contiguous, row and head strides in elements; bases and strides
+ *            16-byte aligned.
+ *   lse      fp32 [total_q, q_heads] contiguous, or NULL.
+ *   q_starts int32 [batch + 1] on the device: the queries of sequence b are
+ *            rows q_starts[b] .. q_starts[b+1] - 1.  NULL: every sequence has
+ *            max_q of them, and total_q = batch * max_q.  Rows of no sequence
+ *            are left as they are, and so are those of a sequence whose starts
+ *            run backwards or past total_q.
+ *   kv_lens  int32 [batch] on the device: keys of each sequence, its own new
+ *            ones among them.
+ *   block_table  int32 [batch, table_len] on the device, row stride
+ *            table_stride: the page of each page_size keys of a sequence (the
+ *            page size then a multiple of 16).  NULL: sequence b is page b.
+ *            Pages of keys that no query sees are not looked at.
+ *   max_q, max_kv  bounds of the query and key counts of a sequence; queries
+ *            of a sequence past max_q are left as they are.
+ *   causal   1: the last query sees every key, each one before it one key
+ *            less (query i of n sees keys 0 .. kv_len - n + i).  0: all keys.
+ *   window   with causal: only the last `window` of those keys; 0: all.
+ *   scale    the factor of the logits, finite.
+ * A query that sees no key gives zeros and lse = -inf.  A sequence whose
+ * kv_len is negative or above max_kv, or above what its pages hold, or that
+ * reads through a page number out of range, gives NaN in the rows concerned.
+ * Logits, softmax statistics and sums are binary32.  Dequantized values enter
+ * the matrix products exactly; queries and probabilities as up to three
+ * 16-bit parts, so that binary32 calls keep about binary32's precision.
+ *   workspace  fp4q_attend_workspace_bytes() bytes, 256-byte aligned (NULL
+ *            where that is 0): partial results of keys split over workgroups. */
+typedef struct {
+    const void* q;
+    int64_t q_row_stride, q_head_stride;
+    void* out;
+    int64_t out_row_stride, out_head_stride;
+    float* lse;
+    const int32_t* q_starts;
+    const int32_t* kv_lens;
+    const int32_t* block_table;
+    int64_t table_stride;
+    int64_t total_q;
+    int32_t table_len;
+    int32_t batch;
+    int32_t max_q;
+    int32_t max_kv;
+    int32_t q_heads;
+    int32_t dtype;
+    int32_t causal;
+    int32_t window;
+    float scale;
+    int32_t reserved; /* 0 */
+} fp4q_attention;
+
+/* Bytes of workspace of this call (sizes, window and formats alone decide;
+ * pointers and device contents do not); 0 also for arguments that fp4q_attend
+ * refuses. */
+size_t fp4q_attend_workspace_bytes(const fp4q_spec* spec, const fp4q_kv_cache* cache,
+                                   const fp4q_attention* call);
+fp4q_status fp4q_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
+                        const fp4q_attention* call, void* workspace, size_t ws_bytes, void* stream);
+
 const char* fp4q_status_string(fp4q_status status);
 int fp4q_abi_version(void);
 

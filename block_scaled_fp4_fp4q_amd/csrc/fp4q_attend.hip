@@ -36,6 +36,7 @@ typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 
+constexpr uint32_t kNanScales = 0xFFFFFFFFu; // bytes that are NaN in E4M3 and in E8M0
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -177,9 +178,10 @@ __device__ __forceinline__ int64_t uniform64(int64_t x)
 
 // The granules of keys [k0, k1) of sequence b (k0 a multiple of 16) into LDS,
 // by the whole workgroup.
+template <int THREADS>
 __device__ __forceinline__ void find_granules(const AttendArgs& a, int b, int head, int k0, int k1, Granule* g)
 {
-    for (int j = threadIdx.x; j * 16 < k1 - k0; j += kThreads)
+    for (int j = threadIdx.x; j * 16 < k1 - k0; j += THREADS)
         g[j] = granule_at(a, b, head, k0 + j * 16);
 }
 
@@ -209,7 +211,7 @@ struct Tile {
     static constexpr int VW = VB < 4 ? 1 : VB / 4;
     uint32_t k[2][KW], ks[2];
     uint32_t v[2][4][VW], vs[2][4];
-    bool lost[2]; // 16 keys whose page does not exist (uniform)
+    uint32_t lost[2]; // all ones where the 16 keys' page does not exist (uniform)
 };
 
 // a lane's fixed byte offsets within 16 rows
@@ -247,7 +249,7 @@ __device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g,
         rows = rows < 0 ? 0 : (rows > 16 ? 16 : rows);
         const Granule at = g[rows > 0 ? h : 0];
         const int64_t co = uniform64(at.codes), so = uniform64(at.scales);
-        t.lost[h] = rows > 0 && co < 0;
+        const bool lost = rows > 0 && co < 0;
         if (co < 0)
             rows = 0; // read nothing
         const int cb = rows > 0 ? (rows - 1) * (int)a.kv.c_token + D / 2 : 0;
@@ -274,6 +276,7 @@ __device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g,
             t.ks[h] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ks, o.ks, 0, 0);
         else
             t.ks[h] = __builtin_amdgcn_raw_buffer_load_b32(ks, o.ks, 0, 0);
+        t.lost[h] = lost ? kNanScales : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (D == 64) {
@@ -296,10 +299,11 @@ __device__ __forceinline__ u32x4 k_operand(const Tile<MX, D>& t, int h, int c)
 {
     constexpr int B = MX ? 32 : 16;
     const int s = (8 * c) / B; // scale of these eight values among the lane's
+    const uint32_t ks = t.ks[h] | t.lost[h]; // lost: K, and the logits that see it, are NaN
     if constexpr (MX) {
-        return expand_bf16(t.k[h][c], e8m0_step((t.ks[h] >> (8 * s)) & 0xFFu));
+        return expand_bf16(t.k[h][c], e8m0_step((ks >> (8 * s)) & 0xFFu));
     } else {
-        const f16x2 two = s < 2 ? e4m3_pair<false>(t.ks[h]) : e4m3_pair<true>(t.ks[h]);
+        const f16x2 two = s < 2 ? e4m3_pair<false>(ks) : e4m3_pair<true>(ks);
         const _Float16 one = two[s & 1];
         return expand_f16(t.k[h][c], f16x2{one, one});
     }
@@ -439,7 +443,7 @@ __global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const
         return; // the joining kernel does not read it
     const int k0 = lo + chunk * p.chunk;
     const int k1 = hi - k0 < p.chunk ? hi : k0 + p.chunk;
-    find_granules(a, b, head, k0, k1, granule);
+    find_granules<kThreads>(a, b, head, k0, k1, granule);
 
     // this wave's 16 rows and its share of the keys
     const int tiles16 = p.rows_per_tile / 16; // 1, 2 or 4
@@ -544,8 +548,7 @@ __global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const
         }
         float x[8];
         float top = -__builtin_huge_valf();
-        const bool whole = key >= all_lo && key + kTileKeys <= all_hi && key + kTileKeys <= k1 &&
-                           !now.lost[0] && !now.lost[1];
+        const bool whole = key >= all_lo && key + kTileKeys <= all_hi && key + kTileKeys <= k1;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -553,7 +556,6 @@ __global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const
                 float t = s[h][i] * factor;
                 if (!whole) {
                     const int k = key + 16 * h + 4 * i + g;
-                    t = now.lost[h] ? __builtin_nanf("") : t;
                     t = (k >= row_lo && k < row_hi) ? t : -__builtin_huge_valf();
                 }
                 x[4 * h + i] = t;
@@ -659,6 +661,513 @@ __global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const
     }
 }
 
+// ---- many queries: workgroups of 32 rows a wave, keys through LDS ---------------------
+//
+// S^T = K Q^T and O^T = V^T P^T by 32x32x16 products.  A workgroup's waves
+// each own 32 query rows (queries of one sequence and KV head, all heads of
+// the group) and share 64 keys at a time, which they expand together from
+// 4 bits to the 16-bit operands in LDS: each code is expanded once for all
+// rows of the workgroup.  Two buffers: while one is multiplied, the other is
+// filled from codes loaded a step earlier; one barrier per step.
+// Places of an operand (lane = n + 32 h, n a row or column, h a half):
+//   - K: row m of a 32-key tile is key m with bits 2 and 3 exchanged, so that
+//     accumulator 8 x + j of half h is key 16 x + 8 h + j: eight consecutive
+//     keys, one operand of the second product.  Half h holds values
+//     h D/2 + 8 c ... of a row at step c, so a lane's part of a query row is
+//     contiguous.
+//   - V^T: row 32 t + i is value (D/32) i + t, so that the thread that expands
+//     D/32 adjacent values writes rows 32 apart (no bank conflict), and a lane
+//     ends with D/8 contiguous values of the result for each a of
+//     value = (D/32) (4 h + 8 a) + ...
+//   - 16-byte units of a row are exchanged by an XOR with the row, so that 16
+//     lanes that read or write one unit of 16 rows meet all 64 banks.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kManyKeys = 64;      // keys of one step
+constexpr int kManySegment = 4096; // keys whose places are looked up at once
+
+template <bool MX>
+__device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
+{
+    if constexpr (MX)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+}
+
+// the 16-byte unit `u` of K's row m, of V^T's row d
+template <int D>
+__device__ __forceinline__ int k_unit(int m, int u)
+{
+    return D == 64 ? m * 8 + (u ^ ((m >> 1) & 7)) : m * (D / 8) + (u ^ (m & 15));
+}
+__device__ __forceinline__ int v_unit(int d, int u) { return d * 8 + (u ^ ((d >> 1) & 7)); }
+
+// codes and scales of one wave's 16 keys of a step, as loaded
+template <int D>
+struct StageK {
+    uint32_t w[D / 32], s;
+    uint32_t lost; // all ones where the keys' page does not exist (uniform)
+};
+template <int D>
+struct StageV {
+    uint32_t w[8], s[8]; // by key; D/64 code bytes of D/32 values
+};
+
+struct ManyBuffers {
+    __amdgpu_buffer_rsrc_t codes, scales;
+    bool lost;
+};
+
+// resources over the rows of 16 keys from `key` that lie before `end`
+template <int B, int D>
+__device__ __forceinline__ ManyBuffers many_buffers(const AttendArgs& a, const Granule* g, int side, int key, int end)
+{
+    int rows = end - key;
+    rows = __builtin_amdgcn_readfirstlane(rows < 0 ? 0 : (rows > 16 ? 16 : rows));
+    const int64_t co = rows > 0 ? uniform64(g->codes) : 0, so = rows > 0 ? uniform64(g->scales) : 0;
+    const bool lost = co < 0;
+    if (lost)
+        rows = 0; // read nothing
+    const int cb = rows > 0 ? (rows - 1) * (int)a.kv.c_token + D / 2 : 0;
+    const int sb = rows > 0 ? (rows - 1) * (int)a.kv.s_token + D / B : 0;
+    return ManyBuffers{buffer_of(a.kv.codes[side] + co, cb), buffer_of(a.kv.scales[side] + so, sb), lost};
+}
+
+template <bool MX, int D>
+__device__ __forceinline__ void stage_k(const AttendArgs& a, const Granule* g, int key, int end, int lane, StageK<D>& t)
+{
+    constexpr int B = MX ? 32 : 16;
+    constexpr int QS = D / 4 >= B ? D / 4 / B : 1;
+    const ManyBuffers m = many_buffers<B, D>(a, g, 0, key, end);
+    const int row = lane >> 2, quarter = lane & 3;
+    const int o = row * (int)a.kv.c_token + quarter * (D / 8);
+    const int os = row * (int)a.kv.s_token + (quarter * (D / 4)) / B;
+    if constexpr (D == 64) {
+        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(m.codes, o, 0, 0);
+        t.w[0] = w.x;
+        t.w[1] = w.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < D / 128; ++j) {
+            const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(m.codes, o + 16 * j, 0, 0);
+            t.w[4 * j + 0] = w.x;
+            t.w[4 * j + 1] = w.y;
+            t.w[4 * j + 2] = w.z;
+            t.w[4 * j + 3] = w.w;
+        }
+    }
+    if constexpr (QS == 1)
+        t.s = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(m.scales, os, 0, 0);
+    else if constexpr (QS == 2)
+        t.s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(m.scales, os, 0, 0);
+    else
+        t.s = __builtin_amdgcn_raw_buffer_load_b32(m.scales, os, 0, 0);
+    t.lost = m.lost ? kNanScales : 0u;
+}
+
+template <bool MX, int D>
+__device__ __forceinline__ void stage_v(const AttendArgs& a, const Granule* g, int key, int end, int lane, StageV<D>& t)
+{
+    constexpr int B = MX ? 32 : 16;
+    const ManyBuffers m = many_buffers<B, D>(a, g, 1, key, end);
+    const int unit = lane >> 5, i = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int row = 8 * unit + j;
+        const int o = row * (int)a.kv.c_token + i * (D / 64);
+        if constexpr (D == 64)
+            t.w[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(m.codes, o, 0, 0);
+        else if constexpr (D == 128)
+            t.w[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(m.codes, o, 0, 0);
+        else
+            t.w[j] = __builtin_amdgcn_raw_buffer_load_b32(m.codes, o, 0, 0);
+        t.s[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(m.scales, row * (int)a.kv.s_token + (i * (D / 32)) / B, 0, 0);
+    }
+}
+
+// expand granule `w` (0..3) of a step into K's buffer
+template <bool MX, int D>
+__device__ __forceinline__ void expand_k(const StageK<D>& t, int w, int lane, u32x4* buf)
+{
+    constexpr int B = MX ? 32 : 16;
+    const int key = 16 * w + (lane >> 2), quarter = lane & 3;
+    const int m = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const int s = (8 * c) / B;
+        const uint32_t ks = t.s | t.lost; // lost: K, and the logits that see it, are NaN
+        u32x4 x;
+        if constexpr (MX) {
+            x = expand_bf16(t.w[c], e8m0_step((ks >> (8 * s)) & 0xFFu));
+        } else {
+            const f16x2 two = s < 2 ? e4m3_pair<false>(ks) : e4m3_pair<true>(ks);
+            const _Float16 one = two[s & 1];
+            x = expand_f16(t.w[c], f16x2{one, one});
+        }
+        buf[k_unit<D>(m, quarter * (D / 32) + c)] = x;
+    }
+}
+
+template <bool MX, int D>
+__device__ __forceinline__ void expand_v(const StageV<D>& t, int w, int lane, u32x4* buf)
+{
+    const int unit = 2 * w + (lane >> 5), i = lane & 31;
+#pragma unroll
+    for (int m = 0; m < D / 64; ++m) { // values 2m and 2m + 1 of the thread's
+        uint32_t e[4], o[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t x = t.w[2 * p] >> (8 * m), y = t.w[2 * p + 1] >> (8 * m);
+            if constexpr (MX) {
+                const uint32_t cx = fp4_pair_bf16<0>(x, e8m0_step(t.s[2 * p]));
+                const uint32_t cy = fp4_pair_bf16<0>(y, e8m0_step(t.s[2 * p + 1]));
+                e[p] = __builtin_amdgcn_perm(cy, cx, 0x05040100u);
+                o[p] = __builtin_amdgcn_perm(cy, cx, 0x07060302u);
+            } else {
+                const f16x2 s = e4m3_pair<false>(t.s[2 * p] | (t.s[2 * p + 1] << 8));
+                const uint32_t lo = (x & 0x0Fu) | ((y << 4) & 0xF0u);
+                const uint32_t hi = ((x >> 4) & 0x0Fu) | (y & 0xF0u);
+                e[p] = __builtin_bit_cast(uint32_t, fp4_pair_f16<0>(lo) * s);
+                o[p] = __builtin_bit_cast(uint32_t, fp4_pair_f16<0>(hi) * s);
+            }
+        }
+        buf[v_unit(32 * (2 * m) + i, unit)] = u32x4{e[0], e[1], e[2], e[3]};
+        buf[v_unit(32 * (2 * m + 1) + i, unit)] = u32x4{o[0], o[1], o[2], o[3]};
+    }
+}
+
+// Orthonormal Hadamard of blocks of B among the first N values of a lane, the
+// block's other half in lane ^ 32 where N < B
+template <int B, int N>
+__device__ __forceinline__ void rotate_half(float* v, int h)
+{
+    constexpr int W = N < B ? N : B;
+#pragma unroll
+    for (int s = 1; s < W; s *= 2)
+#pragma unroll
+        for (int i = 0; i < N; i += 2 * s)
+#pragma unroll
+            for (int j = i; j < i + s; ++j) {
+                const float p = v[j], q = v[j + s];
+                v[j] = p + q;
+                v[j + s] = p - q;
+            }
+    if constexpr (N < B) {
+        const float sign = h ? -1.0f : 1.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] = __builtin_fmaf(sign, v[j], __shfl_xor(v[j], 32, 64));
+    }
+}
+
+template <bool MX, int D, int NQ, int NP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, const AttendPlan p)
+{
+    constexpr int B = MX ? 32 : 16;
+    constexpr int C = D / 16;  // steps of the first product
+    constexpr int T = D / 32;  // row tiles of V^T
+    constexpr int KU = kManyKeys * D / 8; // 16-byte units of a buffer
+    __shared__ u32x4 kbuf[2][KU];
+    __shared__ u32x4 vbuf[2][KU];
+    __shared__ Granule granule[kManySegment / 16];
+
+    // blocks: (sequence, KV head) fastest, so that with a multiple of eight of
+    // them the row tiles that read one head's keys share an XCD's L2; then the
+    // chunk; the row tiles with the most keys (the last ones) first
+    const int heads = a.batch * a.kv.heads;
+    int id = blockIdx.x;
+    const int bh = id % heads;
+    id /= heads;
+    const int chunk = id % p.chunks;
+    const int tile = p.tiles - 1 - id / p.chunks;
+    const int head = bh % a.kv.heads, b = bh / a.kv.heads;
+
+    const Extent e = extent_of(a, b);
+    const int rows = e.qn * a.group;
+    const int r0 = tile * p.rows_per_tile;
+    if (r0 >= rows)
+        return;
+    const int r1 = r0 + p.rows_per_tile < rows ? r0 + p.rows_per_tile : rows;
+    int lo, hi;
+    tile_keys(a, e, r0, r1, lo, hi);
+    if (chunk >= chunks_of(p, lo, hi))
+        return;
+    const int k0 = lo + chunk * p.chunk;
+    const int k1 = hi - k0 < p.chunk ? hi : k0 + p.chunk;
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int n = lane & 31, h = lane >> 5;
+    const int w0 = r0 + wave * 32;            // the wave's first row
+    const int r = w0 + n;
+    const bool live = r < r1;
+    int row_lo = 0, row_hi = 0;
+
+    u32x4 q[NQ][C];
+    float factor; // of the row's logits, to log2 units; positive
+    {
+        float v[D / 2];
+#pragma unroll
+        for (int j = 0; j < D / 2; ++j)
+            v[j] = 0.0f;
+        if (live) {
+            const int i = r / a.group, j = r - i * a.group;
+            seen_by(a, e, i, row_lo, row_hi);
+            const int64_t at = (e.q0 + i) * a.q_row + (head * a.group + j) * a.q_head + h * (D / 2);
+            if (a.bf16) {
+                const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at);
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) {
+                    const u32x4 w = x[t];
+                    v[8 * t + 0] = bf16_lo(w.x); v[8 * t + 1] = bf16_hi(w.x);
+                    v[8 * t + 2] = bf16_lo(w.y); v[8 * t + 3] = bf16_hi(w.y);
+                    v[8 * t + 4] = bf16_lo(w.z); v[8 * t + 5] = bf16_hi(w.z);
+                    v[8 * t + 6] = bf16_lo(w.w); v[8 * t + 7] = bf16_hi(w.w);
+                }
+            } else {
+                const f32x4* x = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at);
+#pragma unroll
+                for (int t = 0; t < D / 8; ++t) {
+                    const f32x4 w = x[t];
+                    v[4 * t + 0] = w.x; v[4 * t + 1] = w.y; v[4 * t + 2] = w.z; v[4 * t + 3] = w.w;
+                }
+            }
+        }
+        const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+        const float turn = a.rotate ? (B == 16 ? 0.25f : __uint_as_float(0x3E3504F3u)) * sign : sign;
+        if (a.rotate)
+            rotate_half<B, D / 2>(v, h);
+#pragma unroll
+        for (int j = 0; j < D / 2; ++j)
+            v[j] *= turn;
+        factor = a.scale * sign * kLog2e;
+        if constexpr (!MX) {
+            factor *= *a.kv.global[0];
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 2; ++j)
+                top = __builtin_fmaxf(top, __builtin_fabsf(v[j]));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+            const int up = (top > 0.0f && top < __builtin_huge_valf())
+                               ? 141 - (int)(__float_as_uint(top) >> 23) : 0;
+#pragma unroll
+            for (int j = 0; j < D / 2; ++j)
+                v[j] = __builtin_ldexpf(v[j], up);
+            factor = __builtin_ldexpf(factor, -up);
+        }
+        factor = __builtin_fmaxf(factor, 0x1p-126f);
+#pragma unroll
+        for (int s = 0; s < NQ; ++s)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                q[s][c].x = take_part<MX>(v[8 * c + 0], v[8 * c + 1]);
+                q[s][c].y = take_part<MX>(v[8 * c + 2], v[8 * c + 3]);
+                q[s][c].z = take_part<MX>(v[8 * c + 4], v[8 * c + 5]);
+                q[s][c].w = take_part<MX>(v[8 * c + 6], v[8 * c + 7]);
+            }
+    }
+    // keys that any row, and that every row, of the wave sees (uniform)
+    int wave_lo = 0, wave_hi = 0, all_lo = 0x7FFFFFFF, all_hi = 0;
+    if (w0 < r1) {
+        const int last = (w0 + 32 < r1 ? w0 + 32 : r1) - 1;
+        int t;
+        seen_by(a, e, w0 / a.group, wave_lo, all_hi);
+        seen_by(a, e, last / a.group, all_lo, wave_hi);
+        (void)t;
+    }
+
+    f32x16 o[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            o[t][j] = 0.0f;
+    float m = -__builtin_huge_valf(), l = 0.0f;
+
+    // waves 0-3 expand K and, of eight waves, 4-7 V
+    const bool does_k = wave < 4, does_v = WAVES == 4 || wave >= 4;
+    const int w = wave & 3;
+    StageK<D> sk;
+    StageV<D> sv;
+    for (int s0 = k0; s0 < k1; s0 += kManySegment) {
+        const int s1 = k1 - s0 < kManySegment ? k1 : s0 + kManySegment;
+        __syncthreads(); // the last segment's places and buffers are done with
+        find_granules<64 * WAVES>(a, b, head, s0, s1, granule);
+        __syncthreads();
+        auto load = [&](int key) {
+            const int mine = key + 16 * w;
+            const Granule* g = granule + (mine < s1 ? (mine - s0) / 16 : 0);
+            if (does_k)
+                stage_k<MX, D>(a, g, mine, s1, lane, sk);
+            if (does_v)
+                stage_v<MX, D>(a, g, mine, s1, lane, sv);
+        };
+        auto expand = [&](int to) {
+            if (does_k)
+                expand_k<MX, D>(sk, w, lane, kbuf[to]);
+            if (does_v)
+                expand_v<MX, D>(sv, w, lane, vbuf[to]);
+        };
+        load(s0);
+        expand(0);
+        if (s0 + kManyKeys < s1)
+            load(s0 + kManyKeys);
+        __syncthreads();
+        int at = 0;
+        for (int key = s0; key < s1; key += kManyKeys, at ^= 1) {
+            if (key + kManyKeys < s1) {
+                expand(at ^ 1);
+                if (key + 2 * kManyKeys < s1)
+                    load(key + 2 * kManyKeys);
+            }
+            if (key < wave_hi && key + kManyKeys > wave_lo) {
+                f32x16 s[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        s[x][j] = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const u32x4 k = kbuf[at][k_unit<D>(32 * x + n, h * C + c)];
+#pragma unroll
+                        for (int t = NQ - 1; t >= 0; --t)
+                            s[x] = mfma32<MX>(k, q[t][c], s[x]);
+                    }
+                }
+                if (!(key >= all_lo && key + kManyKeys <= all_hi)) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int k = key + 32 * x + 16 * (j >> 3) + 8 * h + (j & 7);
+                            s[x][j] = (k >= row_lo && k < row_hi) ? s[x][j] : -__builtin_huge_valf();
+                        }
+                }
+                float top = s[0][0];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        top = __builtin_fmaxf(top, s[x][j]);
+                top *= factor;
+                if (__builtin_amdgcn_ballot_w64(top > m + kLazy) != 0) {
+                    const float raised = __builtin_fmaxf(m, __builtin_fmaxf(top, __shfl_xor(top, 32, 64)));
+                    const float f = m == raised ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
+                    m = raised;
+                    l *= f;
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+                        o[t] *= f;
+                }
+                const float base = m == -__builtin_huge_valf() ? 0.0f : m - kUp;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        s[x][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][j], factor, -base));
+                        l += s[x][j];
+                    }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    u32x4 pr[NP];
+                    float y[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y[j] = s[u >> 1][8 * (u & 1) + j];
+#pragma unroll
+                    for (int t = 0; t < NP; ++t) {
+                        pr[t].x = take_part<MX>(y[0], y[1]);
+                        pr[t].y = take_part<MX>(y[2], y[3]);
+                        pr[t].z = take_part<MX>(y[4], y[5]);
+                        pr[t].w = take_part<MX>(y[6], y[7]);
+                    }
+#pragma unroll
+                    for (int d = 0; d < T; ++d) {
+                        const u32x4 v = vbuf[at][v_unit(32 * d + n, 2 * u + h)];
+#pragma unroll
+                        for (int t = NP - 1; t >= 0; --t)
+                            o[d] = mfma32<MX>(v, pr[t], o[d]);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (e.bad)
+        l = __builtin_nanf("");
+    m -= kUp;
+
+    // the lane's values: D/8 contiguous ones for each a, in order
+    if (p.chunks == 1) {
+        const float inv = l == 0.0f ? 0.0f : (MX ? 1.0f : *a.kv.global[1]) / l;
+        const float turn = inv * (a.rotate ? (B == 16 ? 0.25f : __uint_as_float(0x3E3504F3u)) : 1.0f);
+        const int i = live ? r / a.group : 0, j = r - i * a.group;
+        const int64_t row = e.q0 + i;
+        const int qh = head * a.group + j;
+        if (live && a.lse && h == 0)
+            a.lse[row * a.q_heads + qh] = l == 0.0f ? -__builtin_huge_valf() : (m + __builtin_log2f(l)) * kLn2;
+        float y[4][4 * T];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    y[x][T * k + t] = o[t][4 * x + k] * turn;
+        if (a.rotate) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                rotate_half<B, 4 * T>(y[x], h);
+            if constexpr (8 * T < B) { // D = 64 in blocks of 32: two of them make one
+#pragma unroll
+                for (int x = 0; x < 4; x += 2)
+#pragma unroll
+                    for (int k = 0; k < 4 * T; ++k) {
+                        const float u = y[x][k], v = y[x + 1][k];
+                        y[x][k] = u + v;
+                        y[x + 1][k] = u - v;
+                    }
+            }
+        }
+        if (!live)
+            return;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int at = T * (4 * h + 8 * x);
+            if (a.bf16) {
+                uint16_t* to = static_cast<uint16_t*>(a.out) + row * a.o_row + qh * a.o_head + at;
+#pragma unroll
+                for (int k = 0; k < T / 2; ++k)
+                    reinterpret_cast<u32x4*>(to)[k] =
+                        u32x4{bf16_pair(y[x][8 * k], y[x][8 * k + 1]), bf16_pair(y[x][8 * k + 2], y[x][8 * k + 3]),
+                              bf16_pair(y[x][8 * k + 4], y[x][8 * k + 5]), bf16_pair(y[x][8 * k + 6], y[x][8 * k + 7])};
+            } else {
+                float* to = static_cast<float*>(a.out) + row * a.o_row + qh * a.o_head + at;
+#pragma unroll
+                for (int k = 0; k < T; ++k)
+                    reinterpret_cast<f32x4*>(to)[k] = f32x4{y[x][4 * k], y[x][4 * k + 1], y[x][4 * k + 2], y[x][4 * k + 3]};
+            }
+        }
+    } else if (live) {
+        const Partial out = partials_of(a, p);
+        const int64_t at_row = (((int64_t)b * a.kv.heads + head) * a.max_q * a.group + r) * p.chunks + chunk;
+        if (h == 0)
+            out.stat[at_row] = float2{m, l};
+        float* to = out.o + at_row * D;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int t = 0; t < T; t += 2)
+                    *reinterpret_cast<float2*>(to + T * (4 * h + 8 * x + k) + t) =
+                        float2{o[t][4 * x + k], o[t + 1][4 * x + k]};
+    }
+}
+
 // ---- joining the chunks of a row ---------------------------------------------------
 //
 // One workgroup per query row: D/4 lanes hold four values each, and the
@@ -756,16 +1265,25 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
 }
 
 template <bool MX, int D>
-hipError_t launch_few(const AttendArgs& a, const AttendPlan& p)
+hipError_t launch_parts(const AttendArgs& a, const AttendPlan& p)
 {
     const int64_t groups = (int64_t)a.batch * a.kv.heads * p.tiles * p.chunks;
     const dim3 grid((uint32_t)groups);
-    if (!a.bf16)
+    if (p.many) {
+        constexpr int WAVES = D == 256 ? 4 : 8;
+        if (!a.bf16)
+            attend_many<MX, D, MX ? 3 : 2, MX ? 3 : 2, 4><<<grid, 256, 0, a.stream>>>(a, p);
+        else if (a.rotate)
+            attend_many<MX, D, MX ? 3 : 2, MX ? 2 : 1, WAVES><<<grid, 64 * WAVES, 0, a.stream>>>(a, p);
+        else
+            attend_many<MX, D, 1, MX ? 2 : 1, WAVES><<<grid, 64 * WAVES, 0, a.stream>>>(a, p);
+    } else if (!a.bf16) {
         attend_few<MX, D, MX ? 3 : 2, MX ? 3 : 2><<<grid, kThreads, 0, a.stream>>>(a, p);
-    else if (a.rotate)
+    } else if (a.rotate) {
         attend_few<MX, D, MX ? 3 : 2, MX ? 2 : 1><<<grid, kThreads, 0, a.stream>>>(a, p);
-    else
+    } else {
         attend_few<MX, D, 1, MX ? 2 : 1><<<grid, kThreads, 0, a.stream>>>(a, p);
+    }
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || p.chunks == 1)
         return err;
@@ -777,9 +1295,9 @@ template <bool MX>
 hipError_t launch_dim(const AttendArgs& a, const AttendPlan& p)
 {
     switch (a.kv.head_dim) {
-    case 64: return launch_few<MX, 64>(a, p);
-    case 128: return launch_few<MX, 128>(a, p);
-    default: return launch_few<MX, 256>(a, p);
+    case 64: return launch_parts<MX, 64>(a, p);
+    case 128: return launch_parts<MX, 128>(a, p);
+    default: return launch_parts<MX, 256>(a, p);
     }
 }
 

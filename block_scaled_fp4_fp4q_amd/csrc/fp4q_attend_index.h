@@ -13,7 +13,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTileKeys = 32;                     // keys of one wave's step
 constexpr int kStepKeys = kWaves * kTileKeys;     // a chunk is a multiple of this
-constexpr int kMaxChunk = 4096;                   // keys of one workgroup at most
+constexpr int kMaxChunk = 4096;                   // keys of one workgroup of the kernel for few queries at most
 
 // what a row tile of one sequence sees
 struct Extent {
@@ -101,18 +101,25 @@ inline AttendPlan plan_of(const AttendArgs& a)
 {
     AttendPlan p{};
     const int64_t rows = (int64_t)a.max_q * a.group;
-    p.rows_per_tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    p.many = rows > 64;
+    if (p.many)
+        p.rows_per_tile = (a.bf16 && a.kv.head_dim < 256) ? 256 : 128; // 32 rows a wave
+    else
+        p.rows_per_tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
     p.tiles = (int)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
     const int64_t units = (int64_t)a.batch * a.kv.heads * p.tiles;
     const int64_t span = attend_span(a);
-    int64_t want = (1024 + units - 1) / units;
+    int64_t want = ((p.many ? 512 : 1024) + units - 1) / units;
     int64_t chunk = (span + want - 1) / want;
-    chunk = (chunk + kStepKeys - 1) / kStepKeys * kStepKeys;
-    chunk = chunk < kStepKeys ? kStepKeys : (chunk > kMaxChunk ? kMaxChunk : chunk);
+    const int64_t step = p.many ? 2 * kStepKeys : kStepKeys;
+    chunk = (chunk + step - 1) / step * step;
+    chunk = chunk < step ? step : chunk;
+    if (!p.many && chunk > kMaxChunk)
+        chunk = kMaxChunk;
     p.chunk = (int)chunk;
     const int64_t chunks = span <= chunk ? 1 : (span + chunk - 1) / chunk;
     // a launch holds fewer than 2^32 threads
-    const int64_t most = (((int64_t)1 << 32) - 1) / kThreads;
+    const int64_t most = (((int64_t)1 << 32) - 1) / 512;
     if (units > most / chunks || (chunks > 1 && (int64_t)a.batch * a.kv.heads > most / rows)) {
         p.chunks = 0;
         return p;

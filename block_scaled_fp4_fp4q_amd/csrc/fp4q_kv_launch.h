@@ -63,9 +63,10 @@ struct AttendArgs {
 
 // How one attention call is cut into workgroups, from its sizes alone.
 struct AttendPlan {
+    bool many;         // the kernel for many queries (else the one for few)
     int rows_per_tile; // query rows of one workgroup
     int tiles;         // row tiles per sequence and KV head
-    int chunk;         // keys of one workgroup (a multiple of 128)
+    int chunk;         // keys of one workgroup
     int chunks;        // key chunks per row tile
     size_t workspace;  // bytes of partial results (0 where chunks == 1)
 };

@@ -34,6 +34,7 @@ int main()
         a.window = a.causal && pick(0, 1) ? pick(1, 300) : 0;
         a.max_kv = paged ? pick(0, 900) : pick(0, a.kv.page_size);
         a.max_q = pick(1, 40);
+        a.bf16 = pick(0, 1);
         const int tokens = a.kv.page_size, dim = a.kv.head_dim, block = a.kv.mx ? 32 : 16;
         a.kv.num_pages = paged ? pick(1, 60) : a.batch - (odd ? pick(0, 1) : 0);
         // heads inside tokens or tokens inside heads
@@ -65,7 +66,7 @@ int main()
         a.q_starts = starts.data();
 
         const AttendPlan p = plan_of(a);
-        CHECK(p.chunks >= 1 && p.chunk % kStepKeys == 0 && p.chunk <= kMaxChunk);
+        CHECK(p.chunks >= 1 && p.chunk % kStepKeys == 0 && (p.many || p.chunk <= kMaxChunk));
         CHECK((int64_t)p.tiles * p.rows_per_tile >= (int64_t)a.max_q * a.group);
         const int64_t all = (int64_t)a.batch * a.kv.heads * a.max_q * a.group * p.chunks;
         if (p.chunks > 1)
@@ -89,7 +90,7 @@ int main()
                 for (int c = 0; c < chunks; ++c) {
                     const int k0 = lo + c * p.chunk;
                     const int k1 = hi - k0 < p.chunk ? hi : k0 + p.chunk;
-                    CHECK(k0 % 32 == 0 && k1 - k0 <= kMaxChunk);
+                    CHECK(k0 % 32 == 0 && (p.many || k1 - k0 <= kMaxChunk));
                     for (int key = k0; key < k1; key += 16) {
                         const Granule g = granule_at(a, b, head, key);
                         const int n = std::min(16, k1 - key);

@@ -114,6 +114,14 @@ __device__ __forceinline__ u32x4 expand_bf16(uint32_t w, float step)
     return r;
 }
 
+// the last digit of `id` to base `n`, which leaves it
+__device__ __forceinline__ uint32_t take_digit(uint32_t& id, int n)
+{
+    const uint32_t q = id / (uint32_t)n, r = id - q * (uint32_t)n;
+    id = q;
+    return r;
+}
+
 // ---- lanes -----------------------------------------------------------------
 
 // the maximum (sum) over the four lanes n, n+16, n+32, n+48, in all of them
@@ -163,10 +171,12 @@ __device__ __forceinline__ void rotate_quarter(float* v, int g)
 
 // Raw buffer resource over `bytes` bytes from p (uniform): a load past the end
 // gives zeros, so rows behind the last key read as zero codes with zero
-// scales, whatever the memory holds.
+// scales, whatever the memory holds.  (A size that the compiler holds in a
+// vector register would turn every load into a loop over the lanes.)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, int bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00027000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t x)
@@ -204,6 +214,13 @@ __device__ __forceinline__ void find_granules(const AttendArgs& a, int b, int he
 // Nothing passes through LDS in the loop, and the codes of the next 32 keys
 // are loaded while these are computed.
 
+// waves per SIMD that the registers are cut for: three for D = 128, where four
+// would spill
+constexpr int few_waves(int D, int NQ, int QT)
+{
+    return D == 64 ? (QT == 1 ? 4 : 3) : D == 128 ? (QT == 1 ? 3 : 2) : (NQ == 3 ? 1 : 2);
+}
+
 template <bool MX, int D>
 struct Tile {
     static constexpr int KW = D / 32;            // code words of a lane's quarter row
@@ -236,9 +253,9 @@ __device__ __forceinline__ Lane lane_offsets(const AttendArgs& a, int n, int g)
 }
 
 // the codes and scales of keys [key, key + 32), of which those from `end` on
-// are not read
+// are not read; granule 0 is that of key k0
 template <bool MX, int D>
-__device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g, int key, int end,
+__device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g, int k0, int key, int end,
                                           const Lane& o, Tile<MX, D>& t)
 {
     constexpr int B = MX ? 32 : 16;
@@ -247,7 +264,7 @@ __device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g,
     for (int h = 0; h < 2; ++h) {
         int rows = end - key - 16 * h;
         rows = rows < 0 ? 0 : (rows > 16 ? 16 : rows);
-        const Granule at = g[rows > 0 ? h : 0];
+        const Granule at = g[rows > 0 ? (key - k0) / 16 + h : 0];
         const int64_t co = uniform64(at.codes), so = uniform64(at.scales);
         const bool lost = rows > 0 && co < 0;
         if (co < 0)
@@ -369,40 +386,52 @@ __device__ __forceinline__ Partial partials_of(const AttendArgs& a, const Attend
     return r;
 }
 
-// one row's quarter of the result, from its sums, their total and maximum
-template <int B, int D>
-__device__ __forceinline__ void finish_quarter(const AttendArgs& a, const Extent& e, int head, int r, int g,
-                                               float* o, float m, float l, float Sv)
+// One query row's result from its sums: eight of the D values (those from
+// 8 j on) in each of D/8 lanes, which are lanes of one wave in order.
+template <bool MX, int D, bool F32>
+__device__ __forceinline__ void finish_row(const AttendArgs& a, const Extent& e, int head, int r, int j,
+                                           float* o, float m, float l)
 {
-    const float inv = l == 0.0f ? 0.0f : Sv / l; // nothing seen: zeros
+    constexpr int B = MX ? 32 : 16;
+    const float inv = l == 0.0f ? 0.0f : (MX ? 1.0f : *a.kv.global[1]) / l; // nothing seen: zeros
 #pragma unroll
-    for (int j = 0; j < D / 4; ++j)
-        o[j] *= inv;
-    if (a.rotate)
-        rotate_quarter<B, D>(o, g);
-    const int i = r / a.group, j = r - i * a.group;
-    if (i >= e.qn)
-        return;
-    const int64_t row = e.q0 + i;
-    const int qh = head * a.group + j;
-    if (a.lse && g == 0)
-        a.lse[row * a.q_heads + qh] = l == 0.0f ? -__builtin_huge_valf() : (m + __builtin_log2f(l)) * kLn2;
-    if (a.bf16) {
-        uint16_t* y = static_cast<uint16_t*>(a.out) + row * a.o_row + qh * a.o_head + g * (D / 4);
+    for (int k = 0; k < 8; ++k)
+        o[k] *= inv;
+    if (a.rotate) {
 #pragma unroll
-        for (int t = 0; t < D / 32; ++t) {
-            u32x4 w;
-            w.x = bf16_pair(o[8 * t + 0], o[8 * t + 1]);
-            w.y = bf16_pair(o[8 * t + 2], o[8 * t + 3]);
-            w.z = bf16_pair(o[8 * t + 4], o[8 * t + 5]);
-            w.w = bf16_pair(o[8 * t + 6], o[8 * t + 7]);
-            reinterpret_cast<u32x4*>(y)[t] = w;
+        for (int s = 1; s < 8; s *= 2)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2 * s)
+#pragma unroll
+                for (int k = i; k < i + s; ++k) {
+                    const float p = o[k], q = o[k + s];
+                    o[k] = p + q;
+                    o[k + s] = p - q;
+                }
+#pragma unroll
+        for (int s = 1; s < B / 8; s *= 2) {
+            const float sign = (j & s) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                o[k] = __builtin_fmaf(sign, o[k], __shfl_xor(o[k], s, 64));
         }
-    } else {
-        float* y = static_cast<float*>(a.out) + row * a.o_row + qh * a.o_head + g * (D / 4);
+        const float c = B == 16 ? 0.25f : __uint_as_float(0x3E3504F3u); // fl32(1/sqrt(B))
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t)
-            reinterpret_cast<f32x4*>(y)[t] = f32x4{o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]};
+        for (int k = 0; k < 8; ++k)
+            o[k] *= c;
+    }
+    const int i = r / a.group;
+    const int64_t row = e.q0 + i;
+    const int qh = head * a.group + (r - i * a.group);
+    if (a.lse && j == 0)
+        a.lse[row * a.q_heads + qh] = l == 0.0f ? -__builtin_huge_valf() : (m + __builtin_log2f(l)) * kLn2;
+    if constexpr (F32) {
+        f32x4* y = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + row * a.o_row + qh * a.o_head + 8 * j);
+        y[0] = f32x4{o[0], o[1], o[2], o[3]};
+        y[1] = f32x4{o[4], o[5], o[6], o[7]};
+    } else {
+        u32x4* y = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + row * a.o_row + qh * a.o_head + 8 * j);
+        *y = u32x4{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]), bf16_pair(o[4], o[5]), bf16_pair(o[6], o[7])};
     }
 }
 
@@ -412,24 +441,27 @@ __device__ __forceinline__ void finish_quarter(const AttendArgs& a, const Extent
 // are still told from zero.
 constexpr float kLazy = 6.0f, kUp = 9.0f;
 
-template <bool MX, int D, int NQ, int NP>
-__global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const AttendPlan p)
+// QT: 16-row tiles of one wave, which share the expanded codes.  With QT = 2
+// half the expansions are saved; at D = 256 the registers do not hold it.
+template <bool MX, int D, int NQ, int NP, int QT>
+__global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(const AttendArgs a, const AttendPlan p)
 {
     constexpr int B = MX ? 32 : 16;
+    constexpr bool F32 = NP == (MX ? 3 : 2);
     constexpr int KW = D / 32;
     constexpr int N = D / 4;
+    constexpr int RW = F32 ? D / 16 : D / 32; // 16-byte words of a row's quarter
+    constexpr int R = 16 * QT;
     __shared__ Granule granule[kMaxChunk / 16 + 2];
-    __shared__ float merge_o[2][16][D + 4];
-    __shared__ float2 merge_s[2][16];
+    __shared__ float merge_o[kWaves][R][D + 4]; // by wave
+    __shared__ float2 merge_s[kWaves][R];
 
     // blocks: chunk fastest, then row tile, KV head, sequence
-    int64_t id = blockIdx.x;
-    const int chunk = (int)(id % p.chunks);
-    id /= p.chunks;
-    const int tile = (int)(id % p.tiles);
-    id /= p.tiles;
-    const int head = (int)(id % a.kv.heads);
-    const int b = (int)(id / a.kv.heads);
+    uint32_t id = blockIdx.x;
+    const int chunk = (int)take_digit(id, p.chunks);
+    const int tile = (int)take_digit(id, p.tiles);
+    const int head = (int)take_digit(id, a.kv.heads);
+    const int b = (int)id;
 
     const Extent e = extent_of(a, b);
     const int rows = e.qn * a.group;
@@ -443,53 +475,73 @@ __global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const
         return; // the joining kernel does not read it
     const int k0 = lo + chunk * p.chunk;
     const int k1 = hi - k0 < p.chunk ? hi : k0 + p.chunk;
-    find_granules<kThreads>(a, b, head, k0, k1, granule);
 
-    // this wave's 16 rows and its share of the keys
-    const int tiles16 = p.rows_per_tile / 16; // 1, 2 or 4
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    // this wave's rows and its share of the keys
+    const int parts = p.rows_per_tile / R; // 1, 2 or 4
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 15, g = lane >> 4;
-    const int part = wave % tiles16, turn = wave / tiles16, turns = kWaves / tiles16;
-    const int r = r0 + part * 16 + n;
-    const bool live = r < r1;
-    int row_lo = 0, row_hi = 0;
+    const int part = wave % parts, turn = wave / parts, turns = kWaves / parts;
 
-    // the row's quarter, rotated, as parts
-    u32x4 q[NQ][KW];
-    float factor; // of the row's logits, to log2 units
-    {
+    // the rows' quarters are under way while the keys are looked up and the
+    // first codes loaded
+    u32x4 raw[QT][RW];
+    int row_lo[QT], row_hi[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int r = r0 + part * R + 16 * t + n;
+        row_lo[t] = row_hi[t] = 0;
+#pragma unroll
+        for (int c = 0; c < RW; ++c)
+            raw[t][c] = u32x4{0u, 0u, 0u, 0u};
+        if (r < r1) {
+            const int i = r / a.group, j = r - i * a.group;
+            seen_by(a, e, i, row_lo[t], row_hi[t]);
+            const int64_t at = (e.q0 + i) * a.q_row + (head * a.group + j) * a.q_head + g * N;
+            const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + at * (F32 ? 4 : 2));
+#pragma unroll
+            for (int c = 0; c < RW; ++c)
+                raw[t][c] = x[c];
+        }
+    }
+    find_granules<kThreads>(a, b, head, k0, k1, granule);
+    __syncthreads();
+
+    const Lane at = lane_offsets<MX, D>(a, n, g);
+    const int step = turns * kTileKeys;
+    Tile<MX, D> now, next;
+    int key = k0 + turn * kTileKeys;
+    load_tile<MX, D>(a, granule, k0, key, k1, at, now);
+
+    // the quarters, rotated, as parts
+    u32x4 q[QT][NQ][KW];
+    float factor[QT]; // of the row's logits, to log2 units; positive
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
         float v[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            v[j] = 0.0f;
-        if (live) {
-            const int i = r / a.group, j = r - i * a.group;
-            seen_by(a, e, i, row_lo, row_hi);
-            const int64_t at = (e.q0 + i) * a.q_row + (head * a.group + j) * a.q_head + g * N;
-            if (a.bf16) {
-                const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at);
-#pragma unroll
-                for (int t = 0; t < N / 8; ++t) {
-                    const u32x4 w = x[t];
-                    v[8 * t + 0] = bf16_lo(w.x); v[8 * t + 1] = bf16_hi(w.x);
-                    v[8 * t + 2] = bf16_lo(w.y); v[8 * t + 3] = bf16_hi(w.y);
-                    v[8 * t + 4] = bf16_lo(w.z); v[8 * t + 5] = bf16_hi(w.z);
-                    v[8 * t + 6] = bf16_lo(w.w); v[8 * t + 7] = bf16_hi(w.w);
-                }
+        for (int c = 0; c < RW; ++c) {
+            const u32x4 w = raw[t][c];
+            if constexpr (F32) {
+                v[4 * c + 0] = __uint_as_float(w.x); v[4 * c + 1] = __uint_as_float(w.y);
+                v[4 * c + 2] = __uint_as_float(w.z); v[4 * c + 3] = __uint_as_float(w.w);
             } else {
-                const f32x4* x = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at);
-#pragma unroll
-                for (int t = 0; t < N / 4; ++t) {
-                    const f32x4 w = x[t];
-                    v[4 * t + 0] = w.x; v[4 * t + 1] = w.y; v[4 * t + 2] = w.z; v[4 * t + 3] = w.w;
-                }
+                v[8 * c + 0] = bf16_lo(w.x); v[8 * c + 1] = bf16_hi(w.x);
+                v[8 * c + 2] = bf16_lo(w.y); v[8 * c + 3] = bf16_hi(w.y);
+                v[8 * c + 4] = bf16_lo(w.z); v[8 * c + 5] = bf16_hi(w.z);
+                v[8 * c + 6] = bf16_lo(w.w); v[8 * c + 7] = bf16_hi(w.w);
             }
         }
         if (a.rotate)
             rotate_quarter<B, D>(v, g);
-        factor = a.scale * kLog2e;
+        // a negative factor goes to the query, so that the largest product is
+        // the largest logit
+        const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] *= sign;
+        factor[t] = a.scale * sign * kLog2e;
         if constexpr (!MX) {
-            factor *= *a.kv.global[0];
+            factor[t] *= *a.kv.global[0];
             float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -501,163 +553,166 @@ __global__ __launch_bounds__(kThreads) void attend_few(const AttendArgs a, const
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 v[j] = __builtin_ldexpf(v[j], up);
-            factor = __builtin_ldexpf(factor, -up);
+            factor[t] = __builtin_ldexpf(factor[t], -up);
         }
+        factor[t] = __builtin_fmaxf(factor[t], 0x1p-126f); // not zero: it meets infinities
 #pragma unroll
         for (int s = 0; s < NQ; ++s)
 #pragma unroll
             for (int c = 0; c < KW; ++c) {
-                q[s][c].x = take_part<MX>(v[8 * c + 0], v[8 * c + 1]);
-                q[s][c].y = take_part<MX>(v[8 * c + 2], v[8 * c + 3]);
-                q[s][c].z = take_part<MX>(v[8 * c + 4], v[8 * c + 5]);
-                q[s][c].w = take_part<MX>(v[8 * c + 6], v[8 * c + 7]);
+                q[t][s][c].x = take_part<MX>(v[8 * c + 0], v[8 * c + 1]);
+                q[t][s][c].y = take_part<MX>(v[8 * c + 2], v[8 * c + 3]);
+                q[t][s][c].z = take_part<MX>(v[8 * c + 4], v[8 * c + 5]);
+                q[t][s][c].w = take_part<MX>(v[8 * c + 6], v[8 * c + 7]);
             }
     }
-    __syncthreads(); // granules
 
-    f32x4 o[D / 16];
+    f32x4 o[QT][D / 16];
+    float m[QT], l[QT];
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-        o[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -__builtin_huge_valf(), l = 0.0f;
-    const Lane at = lane_offsets<MX, D>(a, n, g);
-    const int step = turns * kTileKeys;
+    for (int t = 0; t < QT; ++t) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+            o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        m[t] = -__builtin_huge_valf();
+        l[t] = 0.0f;
+    }
     // keys that every row of the workgroup sees need no mask
     int all_lo, all_hi, unused;
     seen_by(a, e, (r1 - 1) / a.group, all_lo, unused);
     seen_by(a, e, r0 / a.group, unused, all_hi);
+    all_hi = all_hi < k1 ? all_hi : k1;
 
-    Tile<MX, D> now, next;
-    int key = k0 + turn * kTileKeys;
-    if (key < k1)
-        load_tile<MX, D>(a, granule + (key - k0) / 16, key, k1, at, now);
     for (; key < k1; key += step) {
-        if (key + step < k1)
-            load_tile<MX, D>(a, granule + (key + step - k0) / 16, key + step, k1, at, next);
-        f32x4 s[2];
+        load_tile<MX, D>(a, granule, k0, key + step, k1, at, next); // past the end: nothing
+        f32x4 s[QT][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+                s[t][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < KW; ++c) {
                 const u32x4 k = k_operand<MX, D>(now, h, c);
 #pragma unroll
-                for (int t = NQ - 1; t >= 0; --t) // small parts first
-                    s[h] = mfma16<MX>(k, q[t][c], s[h]);
+                for (int t = 0; t < QT; ++t)
+#pragma unroll
+                    for (int x = NQ - 1; x >= 0; --x) // small parts first
+                        s[t][h] = mfma16<MX>(k, q[t][x][c], s[t][h]);
             }
         }
-        float x[8];
-        float top = -__builtin_huge_valf();
-        const bool whole = key >= all_lo && key + kTileKeys <= all_hi && key + kTileKeys <= k1;
+        u32x4 pr[QT][NP];
+        const bool whole = key >= all_lo && key + kTileKeys <= all_hi;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int t = 0; t < QT; ++t) {
+            if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float t = s[h][i] * factor;
-                if (!whole) {
-                    const int k = key + 16 * h + 4 * i + g;
-                    t = (k >= row_lo && k < row_hi) ? t : -__builtin_huge_valf();
-                }
-                x[4 * h + i] = t;
-                top = __builtin_fmaxf(top, t);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = key + 16 * h + 4 * i + g;
+                        s[t][h][i] = (k >= row_lo[t] && k < row_hi[t]) ? s[t][h][i] : -__builtin_huge_valf();
+                    }
             }
-        top = column_max(top);
-        if (__builtin_amdgcn_ballot_w64(top > m + kLazy) != 0) {
-            const float raised = __builtin_fmaxf(m, top);
-            const float f = m == raised ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
-            m = raised;
-            l *= f;
+            float top = -__builtin_huge_valf();
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-                o[c] *= f;
-        }
-        const float base = m == -__builtin_huge_valf() ? 0.0f : m - kUp;
-        u32x4 pr[NP];
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = __builtin_amdgcn_exp2f(x[j] - base);
-            l += x[j];
-        }
+                for (int i = 0; i < 4; ++i)
+                    top = __builtin_fmaxf(top, s[t][h][i]);
+            top *= factor[t];
+            if (__builtin_amdgcn_ballot_w64(top > m[t] + kLazy) != 0) {
+                const float raised = __builtin_fmaxf(m[t], column_max(top));
+                const float f = m[t] == raised ? 1.0f : __builtin_amdgcn_exp2f(m[t] - raised);
+                m[t] = raised;
+                l[t] *= f;
 #pragma unroll
-        for (int t = 0; t < NP; ++t) {
-            pr[t].x = take_part<MX>(x[0], x[1]);
-            pr[t].y = take_part<MX>(x[2], x[3]);
-            pr[t].z = take_part<MX>(x[4], x[5]);
-            pr[t].w = take_part<MX>(x[6], x[7]);
+                for (int c = 0; c < D / 16; ++c)
+                    o[t][c] *= f;
+            }
+            const float base = m[t] == -__builtin_huge_valf() ? 0.0f : m[t] - kUp;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j >> 2][j & 3], factor[t], -base));
+                l[t] += x[j];
+            }
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                pr[t][y].x = take_part<MX>(x[0], x[1]);
+                pr[t][y].y = take_part<MX>(x[2], x[3]);
+                pr[t][y].z = take_part<MX>(x[4], x[5]);
+                pr[t][y].w = take_part<MX>(x[6], x[7]);
+            }
         }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             u32x4 even, odd;
             v_operands<MX, D>(now, c, even, odd);
 #pragma unroll
-            for (int t = NP - 1; t >= 0; --t) {
-                o[2 * c] = mfma16<MX>(even, pr[t], o[2 * c]);
-                o[2 * c + 1] = mfma16<MX>(odd, pr[t], o[2 * c + 1]);
-            }
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int y = NP - 1; y >= 0; --y) {
+                    o[t][2 * c] = mfma16<MX>(even, pr[t][y], o[t][2 * c]);
+                    o[t][2 * c + 1] = mfma16<MX>(odd, pr[t][y], o[t][2 * c + 1]);
+                }
         }
         now = next;
     }
-    l = column_sum(l);
-    if (e.bad)
-        l = __builtin_nanf("");
 
-    // join the waves that share these rows: half of them hand over, in turn
-    // (kUp cancels: l and o carry it alike until the end)
-    for (int half = turns / 2; half >= 1; half /= 2) {
-        __syncthreads();
-        const int slot = part + (turn - half) * tiles16;
-        if (turn >= half && turn < 2 * half) {
+    // join the waves that share rows, through LDS: D/8 lanes take a row
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const float sum = column_sum(l[t]);
+        if (r0 + part * R + 16 * t + n < r1) {
             if (g == 0)
-                merge_s[slot][n] = float2{m, l};
+                merge_s[wave][16 * t + n] = float2{m[t], sum};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int c = 0; c < D / 16; c += 4)
-                    *reinterpret_cast<f32x4*>(&merge_o[slot][n][g * N + i * (D / 16) + c]) =
-                        f32x4{o[c][i], o[c + 1][i], o[c + 2][i], o[c + 3][i]};
-        }
-        __syncthreads();
-        if (turn < half) {
-            const int from = part + turn * tiles16;
-            const float2 other = merge_s[from][n];
-            const float raised = __builtin_fmaxf(m, other.x);
-            const float f0 = m == raised ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
-            const float f1 = other.x == raised ? 1.0f : __builtin_amdgcn_exp2f(other.x - raised);
-            m = raised;
-            l = l * f0 + other.y * f1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < D / 16; c += 4) {
-                    const f32x4 t = *reinterpret_cast<const f32x4*>(&merge_o[from][n][g * N + i * (D / 16) + c]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[c + j][i] = o[c + j][i] * f0 + t[j] * f1;
-                }
+                    *reinterpret_cast<f32x4*>(&merge_o[wave][16 * t + n][g * N + i * (D / 16) + c]) =
+                        f32x4{o[t][c][i], o[t][c + 1][i], o[t][c + 2][i], o[t][c + 3][i]};
         }
     }
-    if (turn != 0)
-        return;
-    float y[N];
+    __syncthreads();
+    const int j = threadIdx.x % (D / 8);
+    for (int x = threadIdx.x / (D / 8); x < r1 - r0; x += kThreads / (D / 8)) {
+        const int from = x / R, at_row = x % R; // the row's part, and its place there
+        float top = -__builtin_huge_valf(), sum = 0.0f;
+        for (int t = 0; t < turns; ++t)
+            top = __builtin_fmaxf(top, merge_s[from + t * parts][at_row].x);
+        float y[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int k = 0; k < 8; ++k)
+            y[k] = 0.0f;
+        for (int t = 0; t < turns; ++t) {
+            const float2 st = merge_s[from + t * parts][at_row];
+            const float f = st.x == top ? 1.0f : __builtin_amdgcn_exp2f(st.x - top);
+            const f32x4* src = reinterpret_cast<const f32x4*>(&merge_o[from + t * parts][at_row][8 * j]);
+            const f32x4 u = src[0], w = src[1];
+            sum += st.y * f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-            y[i * (D / 16) + c] = o[c][i];
-    // back from 2^kUp: as the maximum's unit, exactly
-    m = m - kUp;
-    if (p.chunks == 1) {
-        // (rows past the last one take part in the rotation's exchanges)
-        finish_quarter<B, D>(a, e, head, live ? r : 0x7FFFFFFF, g, y, m, l, MX ? 1.0f : *a.kv.global[1]);
-    } else if (live) {
-        const Partial w = partials_of(a, p);
-        const int64_t at_row = (((int64_t)b * a.kv.heads + head) * a.max_q * a.group + r) * p.chunks + chunk;
-        if (g == 0)
-            w.stat[at_row] = float2{m, l};
-        float* to = w.o + at_row * D + g * N;
-#pragma unroll
-        for (int j = 0; j < N; j += 4)
-            *reinterpret_cast<f32x4*>(to + j) = f32x4{y[j], y[j + 1], y[j + 2], y[j + 3]};
+            for (int k = 0; k < 4; ++k) {
+                y[k] += u[k] * f;
+                y[4 + k] += w[k] * f;
+            }
+        }
+        if (e.bad)
+            sum = __builtin_nanf("");
+        top -= kUp; // the sums' unit
+        const int r = r0 + x;
+        if (p.chunks == 1) {
+            finish_row<MX, D, F32>(a, e, head, r, j, y, top, sum);
+        } else {
+            const Partial w = partials_of(a, p);
+            const int64_t to = (((int64_t)b * a.kv.heads + head) * a.max_q * a.group + r) * p.chunks + chunk;
+            if (j == 0)
+                w.stat[to] = float2{top, sum};
+            f32x4* out = reinterpret_cast<f32x4*>(w.o + to * D + 8 * j);
+            out[0] = f32x4{y[0], y[1], y[2], y[3]};
+            out[1] = f32x4{y[4], y[5], y[6], y[7]};
+        }
     }
 }
 
@@ -876,13 +931,11 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     // blocks: (sequence, KV head) fastest, so that with a multiple of eight of
     // them the row tiles that read one head's keys share an XCD's L2; then the
     // chunk; the row tiles with the most keys (the last ones) first
-    const int heads = a.batch * a.kv.heads;
-    int id = blockIdx.x;
-    const int bh = id % heads;
-    id /= heads;
-    const int chunk = id % p.chunks;
-    const int tile = p.tiles - 1 - id / p.chunks;
-    const int head = bh % a.kv.heads, b = bh / a.kv.heads;
+    uint32_t id = blockIdx.x;
+    const int head = (int)take_digit(id, a.kv.heads);
+    const int b = (int)take_digit(id, a.batch);
+    const int chunk = (int)take_digit(id, p.chunks);
+    const int tile = p.tiles - 1 - (int)id;
 
     const Extent e = extent_of(a, b);
     const int rows = e.qn * a.group;
@@ -1180,11 +1233,11 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
     constexpr int L = D / 4, T = kThreads / L;
     __shared__ f32x4 sum[T][L];
     __shared__ float red[kWaves];
-    const int rows_seq = a.max_q * a.group;
     const int64_t id = blockIdx.x;
-    const int r = (int)(id % rows_seq);
-    const int head = (int)(id / rows_seq % a.kv.heads);
-    const int b = (int)(id / rows_seq / a.kv.heads);
+    uint32_t rest = blockIdx.x;
+    const int r = (int)take_digit(rest, a.max_q * a.group);
+    const int head = (int)take_digit(rest, a.kv.heads);
+    const int b = (int)rest;
     const Extent e = extent_of(a, b);
     const int rows = e.qn * a.group;
     if (r >= rows)
@@ -1264,6 +1317,17 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
     }
 }
 
+template <bool MX, int D, int QT>
+void launch_few(const AttendArgs& a, const AttendPlan& p, dim3 grid)
+{
+    if (!a.bf16)
+        attend_few<MX, D, MX ? 3 : 2, MX ? 3 : 2, QT><<<grid, kThreads, 0, a.stream>>>(a, p);
+    else if (a.rotate)
+        attend_few<MX, D, MX ? 3 : 2, MX ? 2 : 1, QT><<<grid, kThreads, 0, a.stream>>>(a, p);
+    else
+        attend_few<MX, D, 1, MX ? 2 : 1, QT><<<grid, kThreads, 0, a.stream>>>(a, p);
+}
+
 template <bool MX, int D>
 hipError_t launch_parts(const AttendArgs& a, const AttendPlan& p)
 {
@@ -1277,12 +1341,10 @@ hipError_t launch_parts(const AttendArgs& a, const AttendPlan& p)
             attend_many<MX, D, MX ? 3 : 2, MX ? 2 : 1, WAVES><<<grid, 64 * WAVES, 0, a.stream>>>(a, p);
         else
             attend_many<MX, D, 1, MX ? 2 : 1, WAVES><<<grid, 64 * WAVES, 0, a.stream>>>(a, p);
-    } else if (!a.bf16) {
-        attend_few<MX, D, MX ? 3 : 2, MX ? 3 : 2><<<grid, kThreads, 0, a.stream>>>(a, p);
-    } else if (a.rotate) {
-        attend_few<MX, D, MX ? 3 : 2, MX ? 2 : 1><<<grid, kThreads, 0, a.stream>>>(a, p);
+    } else if (p.rows_per_tile == 16 || D == 256) {
+        launch_few<MX, D, 1>(a, p, grid);
     } else {
-        attend_few<MX, D, 1, MX ? 2 : 1><<<grid, kThreads, 0, a.stream>>>(a, p);
+        launch_few<MX, D, D == 256 ? 1 : 2>(a, p, grid);
     }
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || p.chunks == 1)

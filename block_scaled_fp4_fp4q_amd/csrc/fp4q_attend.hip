@@ -214,13 +214,6 @@ __device__ __forceinline__ void find_granules(const AttendArgs& a, int b, int he
 // Nothing passes through LDS in the loop, and the codes of the next 32 keys
 // are loaded while these are computed.
 
-// waves per SIMD that the registers are cut for: three for D = 128, where four
-// would spill
-constexpr int few_waves(int D, int NQ, int QT)
-{
-    return D == 64 ? (QT == 1 ? 4 : 3) : D == 128 ? (QT == 1 ? 3 : 2) : (NQ == 3 ? 1 : 2);
-}
-
 template <bool MX, int D>
 struct Tile {
     static constexpr int KW = D / 32;            // code words of a lane's quarter row
@@ -370,19 +363,25 @@ __device__ __forceinline__ void v_operands(const Tile<MX, D>& t, int m, u32x4& e
     odd = u32x4{o[0], o[1], o[2], o[3]};
 }
 
-// where a workgroup's partial result for one query row goes
+// Partial results in the workspace, by place: many queries, (row, chunk); few,
+// (slot, row of the tile).
 struct Partial {
-    float* o;     // [rows, chunks, D] sums of p v, in units of V's global scale
-    float2* stat; // [rows, chunks] (maximum in log2 units, sum)
+    float* o;     // [places, D] sums of p v, in units of V's global scale
+    float2* stat; // [places] (maximum in log2 units, sum)
+    int2* pairs;  // few: (first slot, number) of each sequence and KV head
 };
 
 __device__ __forceinline__ Partial partials_of(const AttendArgs& a, const AttendPlan& p)
 {
-    const int64_t rows = (int64_t)a.batch * a.kv.heads * a.max_q * a.group;
     Partial r;
-    r.stat = static_cast<float2*>(a.workspace);
-    const size_t stat = (size_t)rows * p.chunks * sizeof(float2);
-    r.o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + ((stat + 255) & ~(size_t)255));
+    char* at = static_cast<char*>(a.workspace);
+    const size_t pairs = (size_t)a.batch * a.kv.heads;
+    r.pairs = reinterpret_cast<int2*>(at);
+    if (!p.many)
+        at += (pairs * sizeof(int2) + 255) & ~(size_t)255;
+    const size_t places = p.many ? pairs * a.max_q * a.group * p.chunks : (size_t)2 * p.parts * p.rows_per_tile;
+    r.stat = reinterpret_cast<float2*>(at);
+    r.o = reinterpret_cast<float*>(at + ((places * sizeof(float2) + 255) & ~(size_t)255));
     return r;
 }
 
@@ -441,10 +440,93 @@ __device__ __forceinline__ void finish_row(const AttendArgs& a, const Extent& e,
 // are still told from zero.
 constexpr float kLazy = 6.0f, kUp = 9.0f;
 
+// the pair of workgroup `blockIdx.x` and its part of it: steps [from, to), the
+// number of parts, and the slots of its and of the first part's results
+struct FewWhere {
+    int b, head;
+    int from, to, parts, slot, first_slot;
+};
+
+// By the whole workgroup: the steps of all sequences (a lane each) are summed,
+// then their parts and slots up to the sequence that holds this workgroup's.
+// Returns an empty part where there is none.
+__device__ __forceinline__ FewWhere find_part(const AttendArgs& a, const AttendPlan& p)
+{
+    __shared__ uint64_t sums[kWaves];
+    __shared__ uint32_t found[4]; // sequence, its first part and slot, steps per head
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t heads = a.kv.heads, id = blockIdx.x;
+    auto steps_of = [&](int b) -> uint32_t { return b < a.batch ? (uint32_t)few_steps(a, extent_of(a, b)) : 0u; };
+    // inclusive sum over the workgroup's threads, and the sum of all
+    auto scan = [&](uint64_t v, uint64_t& all) {
+#pragma unroll
+        for (int off = 1; off < 64; off *= 2) {
+            const uint64_t t = __shfl_up(v, off, 64);
+            v += lane >= (uint32_t)off ? t : 0u;
+        }
+        __syncthreads();
+        if (lane == 63)
+            sums[wave] = v;
+        __syncthreads();
+        all = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < kWaves; ++w) {
+            v += w < wave ? sums[w] : 0u;
+            all += sums[w];
+        }
+        return v;
+    };
+    uint32_t steps = steps_of(threadIdx.x), total = 0;
+    const uint32_t first_steps = steps;
+    uint64_t all;
+    for (int b0 = 0;;) {
+        scan(steps, all);
+        total += (uint32_t)all;
+        b0 += kThreads;
+        if (b0 >= a.batch)
+            break;
+        steps = steps_of(b0 + threadIdx.x);
+    }
+    const uint32_t most = few_most(p, total * heads);
+    steps = first_steps;
+    uint64_t before = 0; // parts in the low half, slots in the high one
+    for (int b0 = 0;;) {
+        const uint32_t parts = few_parts(steps, most);
+        const uint64_t mine = (uint64_t)(parts * heads) | (uint64_t)(parts > 1 ? parts * heads : 0u) << 32;
+        const uint64_t upto = before + scan(mine, all);
+        if ((uint32_t)upto > id && (uint32_t)(upto - mine) <= id) { // one thread, once
+            found[0] = b0 + threadIdx.x;
+            found[1] = (uint32_t)(upto - mine);
+            found[2] = (uint32_t)((upto - mine) >> 32);
+            found[3] = steps;
+        }
+        before += all;
+        if ((uint32_t)before > id)
+            break;
+        b0 += kThreads;
+        if (b0 >= a.batch)
+            return FewWhere{};
+        steps = steps_of(b0 + threadIdx.x);
+    }
+    __syncthreads();
+    FewWhere r;
+    steps = __builtin_amdgcn_readfirstlane(found[3]);
+    const uint32_t parts = few_parts(steps, most), at = id - __builtin_amdgcn_readfirstlane(found[1]);
+    const uint32_t head = at / parts, i = at - head * parts;
+    r.b = (int)__builtin_amdgcn_readfirstlane(found[0]);
+    r.head = (int)head;
+    r.from = few_from(steps, parts, i);
+    r.to = few_from(steps, parts, i + 1);
+    r.parts = (int)parts;
+    r.first_slot = (int)(__builtin_amdgcn_readfirstlane(found[2]) + head * parts);
+    r.slot = r.first_slot + (int)i;
+    return r;
+}
+
 // QT: 16-row tiles of one wave, which share the expanded codes.  With QT = 2
 // half the expansions are saved; at D = 256 the registers do not hold it.
 template <bool MX, int D, int NQ, int NP, int QT>
-__global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(const AttendArgs a, const AttendPlan p)
+__global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(const AttendArgs a, const AttendPlan p)
 {
     constexpr int B = MX ? 32 : 16;
     constexpr bool F32 = NP == (MX ? 3 : 2);
@@ -452,30 +534,33 @@ __global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(con
     constexpr int N = D / 4;
     constexpr int RW = F32 ? D / 16 : D / 32; // 16-byte words of a row's quarter
     constexpr int R = 16 * QT;
-    __shared__ Granule granule[kMaxChunk / 16 + 2];
+    __shared__ Granule granule[kSegment / 16];
     __shared__ float merge_o[kWaves][R][D + 4]; // by wave
     __shared__ float2 merge_s[kWaves][R];
 
-    // blocks: chunk fastest, then row tile, KV head, sequence
-    uint32_t id = blockIdx.x;
-    const int chunk = (int)take_digit(id, p.chunks);
-    const int tile = (int)take_digit(id, p.tiles);
-    const int head = (int)take_digit(id, a.kv.heads);
-    const int b = (int)id;
-
+    FewWhere piece{0, 0, 0, 0, 1, 0, 0};
+    if (p.chunks == 1) { // one pair per workgroup
+        uint32_t id = blockIdx.x;
+        piece.head = (int)take_digit(id, a.kv.heads);
+        piece.b = (int)id;
+    } else {
+        piece = find_part(a, p);
+        if (piece.from == piece.to)
+            return;
+    }
+    const int b = piece.b, head = piece.head;
     const Extent e = extent_of(a, b);
     const int rows = e.qn * a.group;
-    const int r0 = tile * p.rows_per_tile;
-    if (r0 >= rows)
+    if (rows == 0)
         return;
-    const int r1 = r0 + p.rows_per_tile < rows ? r0 + p.rows_per_tile : rows;
+    const int steps = few_steps(a, e);
+    if (p.chunks == 1)
+        piece.to = steps;
+    const int r0 = 0, r1 = rows;
     int lo, hi;
     tile_keys(a, e, r0, r1, lo, hi);
-    if (chunk >= chunks_of(p, lo, hi))
-        return; // the joining kernel does not read it
-    const int k0 = lo + chunk * p.chunk;
-    const int k1 = hi - k0 < p.chunk ? hi : k0 + p.chunk;
-
+    const int k0 = lo + piece.from * kStepKeys;
+    const int k1 = piece.to == steps ? hi : lo + piece.to * kStepKeys;
     // this wave's rows and its share of the keys
     const int parts = p.rows_per_tile / R; // 1, 2 or 4
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -503,14 +588,14 @@ __global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(con
                 raw[t][c] = x[c];
         }
     }
-    find_granules<kThreads>(a, b, head, k0, k1, granule);
-    __syncthreads();
-
     const Lane at = lane_offsets<MX, D>(a, n, g);
     const int step = turns * kTileKeys;
     Tile<MX, D> now, next;
-    int key = k0 + turn * kTileKeys;
-    load_tile<MX, D>(a, granule, k0, key, k1, at, now);
+    int s0 = k0, s1 = k1 - k0 < kSegment ? k1 : k0 + kSegment;
+    find_granules<kThreads>(a, b, head, s0, s1, granule);
+    __syncthreads();
+    int key = s0 + turn * kTileKeys;
+    load_tile<MX, D>(a, granule, s0, key, s1, at, now);
 
     // the quarters, rotated, as parts
     u32x4 q[QT][NQ][KW];
@@ -583,8 +668,9 @@ __global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(con
     seen_by(a, e, r0 / a.group, unused, all_hi);
     all_hi = all_hi < k1 ? all_hi : k1;
 
-    for (; key < k1; key += step) {
-        load_tile<MX, D>(a, granule, k0, key + step, k1, at, next); // past the end: nothing
+    for (;;) {
+    for (; key < s1; key += step) {
+        load_tile<MX, D>(a, granule, s0, key + step, s1, at, next); // past the end: nothing
         f32x4 s[QT][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -659,6 +745,16 @@ __global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(con
         }
         now = next;
     }
+    if (s1 >= k1)
+        break;
+    s0 = s1; // the places of the next keys
+    s1 = k1 - s0 < kSegment ? k1 : s0 + kSegment;
+    __syncthreads();
+    find_granules<kThreads>(a, b, head, s0, s1, granule);
+    __syncthreads();
+    key = s0 + turn * kTileKeys;
+    load_tile<MX, D>(a, granule, s0, key, s1, at, now);
+    }
 
     // join the waves that share rows, through LDS: D/8 lanes take a row
 #pragma unroll
@@ -702,11 +798,11 @@ __global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(con
             sum = __builtin_nanf("");
         top -= kUp; // the sums' unit
         const int r = r0 + x;
-        if (p.chunks == 1) {
+        if (piece.parts == 1) {
             finish_row<MX, D, F32>(a, e, head, r, j, y, top, sum);
         } else {
             const Partial w = partials_of(a, p);
-            const int64_t to = (((int64_t)b * a.kv.heads + head) * a.max_q * a.group + r) * p.chunks + chunk;
+            const int64_t to = (int64_t)piece.slot * p.rows_per_tile + r;
             if (j == 0)
                 w.stat[to] = float2{top, sum};
             f32x4* out = reinterpret_cast<f32x4*>(w.o + to * D + 8 * j);
@@ -714,6 +810,8 @@ __global__ __launch_bounds__(kThreads, few_waves(D, NQ, QT)) void attend_few(con
             out[1] = f32x4{y[4], y[5], y[6], y[7]};
         }
     }
+    if (p.chunks != 1 && piece.from == 0 && threadIdx.x == 0)
+        partials_of(a, p).pairs[(int64_t)b * a.kv.heads + head] = int2{piece.first_slot, piece.parts};
 }
 
 // ---- many queries: workgroups of 32 rows a wave, keys through LDS ---------------------
@@ -1233,8 +1331,8 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
     constexpr int L = D / 4, T = kThreads / L;
     __shared__ f32x4 sum[T][L];
     __shared__ float red[kWaves];
-    const int64_t id = blockIdx.x;
-    uint32_t rest = blockIdx.x;
+    const uint32_t id = blockIdx.x;
+    uint32_t rest = id;
     const int r = (int)take_digit(rest, a.max_q * a.group);
     const int head = (int)take_digit(rest, a.kv.heads);
     const int b = (int)rest;
@@ -1242,18 +1340,31 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
     const int rows = e.qn * a.group;
     if (r >= rows)
         return;
-    const int r0 = r - r % p.rows_per_tile;
-    int lo, hi;
-    tile_keys(a, e, r0, r0 + p.rows_per_tile < rows ? r0 + p.rows_per_tile : rows, lo, hi);
-    const int chunks = chunks_of(p, lo, hi);
     const Partial w = partials_of(a, p);
-    const float2* stat = w.stat + id * p.chunks;
-    const float* part = w.o + id * p.chunks * D;
+    // places of the row's partial results: base + c * stride
+    int chunks;
+    int64_t base, stride;
+    if (p.many) {
+        const int r0 = r - r % p.rows_per_tile;
+        int lo, hi;
+        tile_keys(a, e, r0, r0 + p.rows_per_tile < rows ? r0 + p.rows_per_tile : rows, lo, hi);
+        chunks = chunks_of(p, lo, hi);
+        base = (int64_t)id * p.chunks;
+        stride = 1;
+    } else {
+        const int2 pair = w.pairs[id / (uint32_t)(a.max_q * a.group)];
+        chunks = pair.y;
+        if (chunks == 1)
+            return; // done by the one workgroup that had it all
+        base = (int64_t)pair.x * p.rows_per_tile + r;
+        stride = p.rows_per_tile;
+    }
+    auto place = [&](int c) { return base + c * stride; };
 
     // the maximum over the chunks (a NaN is in the sums, never in a maximum)
     float m = -__builtin_huge_valf();
     for (int c = threadIdx.x; c < chunks; c += kThreads)
-        m = __builtin_fmaxf(m, stat[c].x);
+        m = __builtin_fmaxf(m, w.stat[place(c)].x);
     m = wave_max(m);
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = m;
@@ -1266,9 +1377,9 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float l = 0.0f;
     for (int c = turn; c < chunks; c += T) {
-        const float2 s = stat[c];
+        const float2 s = w.stat[place(c)];
         const float f = s.x == m ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
-        const f32x4 t = *reinterpret_cast<const f32x4*>(part + (int64_t)c * D + 4 * j);
+        const f32x4 t = *reinterpret_cast<const f32x4*>(w.o + place(c) * D + 4 * j);
         l += s.y * f;
         o += t * f;
     }
@@ -1331,8 +1442,7 @@ void launch_few(const AttendArgs& a, const AttendPlan& p, dim3 grid)
 template <bool MX, int D>
 hipError_t launch_parts(const AttendArgs& a, const AttendPlan& p)
 {
-    const int64_t groups = (int64_t)a.batch * a.kv.heads * p.tiles * p.chunks;
-    const dim3 grid((uint32_t)groups);
+    const dim3 grid((uint32_t)p.groups);
     if (p.many) {
         constexpr int WAVES = D == 256 ? 4 : 8;
         if (!a.bf16)

@@ -12,8 +12,26 @@ namespace fp4q {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTileKeys = 32;                     // keys of one wave's step
-constexpr int kStepKeys = kWaves * kTileKeys;     // a chunk is a multiple of this
-constexpr int kMaxChunk = 4096;                   // keys of one workgroup of the kernel for few queries at most
+constexpr int kStepKeys = kWaves * kTileKeys;     // keys of a workgroup's step at most
+constexpr int kMinPart = 2;                       // steps that are not cut further
+constexpr int kCus = 256;
+constexpr int kSegment = 4096;                    // keys whose places are looked up at once
+
+inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// waves per SIMD that the kernel for few queries is built for: what its
+// registers allow without spilling (rows16: 16-row tiles of a wave; parts: 16-bit
+// parts of a query)
+constexpr int few_waves_of(int dim, int parts, int rows16)
+{
+    return dim == 64 ? (rows16 == 1 ? 4 : 3) : dim == 128 ? (rows16 == 1 ? 3 : 2) : (parts == 3 ? 1 : 2);
+}
+
+inline int few_waves(const AttendArgs& a)
+{
+    const int parts = a.bf16 && !a.rotate ? 1 : (a.kv.mx ? 3 : 2);
+    return few_waves_of(a.kv.head_dim, parts, (int64_t)a.max_q * a.group > 16 && a.kv.head_dim < 256 ? 2 : 1);
+}
 
 // what a row tile of one sequence sees
 struct Extent {
@@ -95,39 +113,81 @@ FP4Q_INDEX Granule granule_at(const AttendArgs& a, int b, int head, int key)
                    page * a.kv.s_page + head * a.kv.s_head + off * a.kv.s_token};
 }
 
-// Row tiles and key chunks from the sizes that the host knows.  Chunks are cut
-// so that about four workgroups per CU (256 CUs) exist where the keys allow.
+// ---- few queries: equal shares of the work -----------------------------------------
+//
+// A pair (a sequence and a KV head) of n steps of kStepKeys keys is computed by
+// ceil(n / most) workgroups, in equal parts; `most` follows from the sum of all
+// lengths, which lie on the device, so that the parts about fill the
+// chip once whatever the lengths are.  A pair in more than one part has
+// partial results, each in a slot of its own.  Steps count in 31 bits.
+
+// steps of each KV head of a sequence; a sequence with queries has at least
+// one, which says that there is nothing where there is nothing
+FP4Q_INDEX int few_steps(const AttendArgs& a, const Extent& e)
+{
+    if (e.qn == 0)
+        return 0;
+    int lo, hi;
+    tile_keys(a, e, 0, e.qn * a.group, lo, hi);
+    const int n = (int)(((int64_t)hi - lo + kStepKeys - 1) / kStepKeys);
+    return n < 1 ? 1 : n;
+}
+
+// steps of a part at most, where all pairs together have `total`
+FP4Q_INDEX uint32_t few_most(const AttendPlan& p, uint32_t total)
+{
+    const uint32_t n = (total + p.parts - 1) / p.parts;
+    return n < kMinPart ? kMinPart : n;
+}
+
+FP4Q_INDEX uint32_t few_parts(uint32_t steps, uint32_t most) { return (steps + most - 1) / most; }
+
+// first step of part i of `parts`
+FP4Q_INDEX int few_from(uint32_t steps, uint32_t parts, uint32_t i) { return (int)((uint64_t)steps * i / parts); }
+
+// Row tiles, and key chunks or parts, from the sizes that the host knows.
 inline AttendPlan plan_of(const AttendArgs& a)
 {
     AttendPlan p{};
-    const int64_t rows = (int64_t)a.max_q * a.group;
-    p.many = rows > 64;
-    if (p.many)
-        p.rows_per_tile = (a.bf16 && a.kv.head_dim < 256) ? 256 : 128; // 32 rows a wave
-    else
-        p.rows_per_tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    p.tiles = (int)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
-    const int64_t units = (int64_t)a.batch * a.kv.heads * p.tiles;
+    const int64_t rows = (int64_t)a.max_q * a.group, pairs = (int64_t)a.batch * a.kv.heads;
     const int64_t span = attend_span(a);
-    int64_t want = ((p.many ? 512 : 1024) + units - 1) / units;
-    int64_t chunk = (span + want - 1) / want;
-    const int64_t step = p.many ? 2 * kStepKeys : kStepKeys;
-    chunk = (chunk + step - 1) / step * step;
-    chunk = chunk < step ? step : chunk;
-    if (!p.many && chunk > kMaxChunk)
-        chunk = kMaxChunk;
-    p.chunk = (int)chunk;
-    const int64_t chunks = span <= chunk ? 1 : (span + chunk - 1) / chunk;
-    // a launch holds fewer than 2^32 threads
-    const int64_t most = (((int64_t)1 << 32) - 1) / 512;
-    if (units > most / chunks || (chunks > 1 && (int64_t)a.batch * a.kv.heads > most / rows)) {
-        p.chunks = 0;
+    const int64_t most = (((int64_t)1 << 32) - 1) / 512; // a launch holds fewer than 2^32 threads
+    p.chunks = 1;
+    p.many = rows > 64;
+    if (!p.many) {
+        p.rows_per_tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+        p.tiles = 1;
+        const int64_t steps = (span + kStepKeys - 1) / kStepKeys;
+        if (pairs > most / (steps > rows ? steps : rows))
+            return p; // groups == 0: refused
+        p.groups = (int)pairs;
+        if (steps > kMinPart) {
+            // workgroups that are resident at once: 256 CUs, one wave of each
+            // on every SIMD.  ceil() adds half a part for each pair.
+            const int64_t all = (int64_t)kCus * few_waves(a);
+            p.parts = (int)(2 * all - pairs > all ? all - pairs / 2 : all / 2);
+            p.groups += p.parts;
+            p.chunks = 2; // partial results
+            const size_t places = (size_t)2 * p.parts * p.rows_per_tile;
+            p.workspace = round256((size_t)pairs * 8) + round256(places * 8) + places * a.kv.head_dim * 4;
+        }
         return p;
     }
+    p.rows_per_tile = (a.bf16 && a.kv.head_dim < 256) ? 256 : 128; // 32 rows a wave
+    p.tiles = (int)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
+    const int64_t units = pairs * p.tiles;
+    const int64_t want = (512 + units - 1) / units;
+    int64_t chunk = (span + want - 1) / want;
+    chunk = (chunk + 255) / 256 * 256;
+    p.chunk = (int)(chunk < 256 ? 256 : chunk);
+    const int64_t chunks = span <= chunk ? 1 : (span + chunk - 1) / chunk;
+    if (units > most / chunks || (chunks > 1 && pairs > most / rows))
+        return p; // groups == 0: refused
+    p.groups = (int)(units * chunks);
     p.chunks = (int)chunks;
     if (chunks > 1) {
-        const size_t all = (size_t)a.batch * a.kv.heads * rows * chunks;
-        p.workspace = ((all * 8 + 255) & ~(size_t)255) + all * a.kv.head_dim * 4;
+        const size_t all = (size_t)pairs * rows * chunks;
+        p.workspace = round256(all * 8) + all * a.kv.head_dim * 4;
     }
     return p;
 }

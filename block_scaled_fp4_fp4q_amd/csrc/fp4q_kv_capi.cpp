@@ -281,7 +281,7 @@ fp4q_status fp4q_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
     if (a.batch == 0)
         return FP4Q_OK;
     const fp4q::AttendPlan p = fp4q::plan_attend(a);
-    if (p.chunks == 0)
+    if (p.groups == 0)
         return FP4Q_E_SHAPE; // more workgroups than a launch holds
     if (p.workspace != 0) {
         if (!workspace)

@@ -477,6 +477,7 @@ class KvCache:
         self.struct = fp4q_kv_cache(*ptr, pages, heads, page, self.head_dim, 0,
                                     *k_codes.stride()[:3], *k_scales.stride()[:3])
         self._spec, self._struct = C.byref(self.spec), C.byref(self.struct)
+        self._calls = {}  # attend's checked argument shapes
 
 
 def alloc_kv_cache(pages, kv_heads, page_size, head_dim, k_global=None, v_global=None,
@@ -501,20 +502,19 @@ def alloc_kv_cache(pages, kv_heads, page_size, head_dim, k_global=None, v_global
 
 def _rows(name, t, rows, heads, dim, device, dtypes=_X):
     """A [rows, heads, dim] tensor whose last dimension is contiguous; returns
-    its row and head strides."""
+    its strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, but the cache is on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}; expected " + " or ".join(map(str, dtypes)))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected "
-                         f"[{'rows' if rows is None else rows}, {heads}, {dim}]")
+    if tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected [{rows}, {heads}, {dim}]")
     st = t.stride()
     if st[2] != 1 and t.numel() > 0:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return st[0], st[1]
+    return st
 
 
 def _ints(name, t, dtype, device, dim=1):
@@ -524,33 +524,40 @@ def _ints(name, t, dtype, device, dim=1):
         raise ValueError(f"{name} is on {t.device}, but the cache is on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
-    if t.dim() != dim or (t.numel() > 0 and t.stride(dim - 1) != 1):
+    if t.dim() != dim or (t.numel() > 0 and t.stride()[-1] != 1):
         raise ValueError(f"{name} must have {dim} dimension(s), the last one contiguous")
-    return t.data_ptr()
+
+
+def _here(device, stream):
+    """Whether a call on `device` runs as it is: no stream given, and the
+    device current."""
+    return stream is None and (device.type != "cuda" or device.index == _current_device())
 
 
 class _on:
-    """The device of the cache as the current one, and the stream of the call
-    (torch's current one there unless given) as torch's current one, so that
-    what is allocated for the call belongs to that stream."""
+    """The device as the current one, and a given stream as torch's current
+    one there, so that what a call allocates belongs to its stream."""
 
     def __init__(self, device, stream):
-        self.device, self.given = device, stream
-        self.inner = []
+        self.inner = [torch.cuda.device(device)]
+        if stream is not None:
+            self.inner.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
-            self.inner.append(torch.cuda.device(self.device))
-            self.inner[-1].__enter__()
-        if self.given is not None:
-            self.inner.append(torch.cuda.stream(self.given))
-            self.inner[-1].__enter__()
-            return self.given.cuda_stream
-        return torch.cuda.current_stream(self.device).cuda_stream
+        for c in self.inner:
+            c.__enter__()
 
     def __exit__(self, *exc):
-        while self.inner:
-            self.inner.pop().__exit__(*exc)
+        for c in reversed(self.inner):
+            c.__exit__(*exc)
+
+
+# the current device's index and a device's current stream as an integer,
+# without the objects that the public functions make (these calls take a few
+# microseconds in all)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def kv_write(cache, k, v, slots, stream=None):
@@ -558,35 +565,41 @@ def kv_write(cache, k, v, slots, stream=None):
     dimension contiguous), into the cache at `slots` (int64 [tokens]; a
     negative or too large slot skips its token)."""
     dev = cache.device
-    p = _ints("slots", slots, torch.int64, dev)
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return kv_write(cache, k, v, slots)
+    _ints("slots", slots, torch.int64, dev)
     n = slots.shape[0]
     ks = _rows("k", k, n, cache.heads, cache.head_dim, dev)
     vs = _rows("v", v, n, cache.heads, cache.head_dim, dev)
     if k.dtype != v.dtype:
         raise ValueError("k and v must have the same dtype")
-    with _on(dev, stream) as st:
-        _check("fp4q_kv_write", _lib_handle().fp4q_kv_write(
-            cache._spec, cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k), n, *ks, *vs, p, st))
+    _check("fp4q_kv_write", _lib_handle().fp4q_kv_write(
+        cache._spec, cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k), n, ks[0], ks[1],
+        vs[0], vs[1], slots.data_ptr(), _current_stream(dev.index)))
 
 
 def kv_read(cache, slots, dtype=torch.float32, stream=None):
     """The values of the rows at `slots` (int64 [tokens]): (k, v), each
     [tokens, kv_heads, head_dim] of `dtype`, un-rotated."""
     dev = cache.device
-    p = _ints("slots", slots, torch.int64, dev)
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return kv_read(cache, slots, dtype)
+    _ints("slots", slots, torch.int64, dev)
     if dtype not in _X:
         raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
-    with _on(dev, stream) as st:
-        k = torch.empty(slots.shape[0], cache.heads, cache.head_dim, dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        _check("fp4q_kv_read", _lib_handle().fp4q_kv_read(
-            cache._spec, cache._struct, p, slots.shape[0], k.data_ptr(), v.data_ptr(),
-            _dtype_code(k), st))
+    n = slots.shape[0]
+    k = torch.empty((n, cache.heads, cache.head_dim), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    _check("fp4q_kv_read", _lib_handle().fp4q_kv_read(
+        cache._spec, cache._struct, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+        _dtype_code(k), _current_stream(dev.index)))
     return k, v
 
 
-def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, scale, out, lse):
-    """The call's fp4q_attention, from checked tensors."""
+def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, scale, out):
+    """The call's fp4q_attention without its pointers, from checked tensors."""
     dev = cache.device
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise TypeError("q must be a torch tensor [total_q, q_heads, head_dim]")
@@ -594,11 +607,10 @@ def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, 
     if heads < 1 or heads % cache.heads:
         raise ValueError(f"q has {heads} heads; expected a multiple of the cache's {cache.heads}")
     qs = _rows("q", q, total, heads, cache.head_dim, dev)
-    lens = _ints("kv_lens", kv_lens, torch.int32, dev)
+    _ints("kv_lens", kv_lens, torch.int32, dev)
     batch = kv_lens.shape[0]
-    starts = None
     if q_starts is not None:
-        starts = _ints("q_starts", q_starts, torch.int32, dev)
+        _ints("q_starts", q_starts, torch.int32, dev)
         if q_starts.shape[0] != batch + 1:
             raise ValueError(f"q_starts has {q_starts.shape[0]} entries; expected batch + 1 = {batch + 1}")
         if max_q is None:
@@ -608,33 +620,50 @@ def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, 
         if each * batch != total or (max_q is not None and max_q != each):
             raise ValueError("without q_starts, q must hold max_q rows for each sequence")
         max_q = each
-    table, stride, entries = None, 0, 0
+    stride, entries = 0, 0
     if block_table is not None:
-        table = _ints("block_table", block_table, torch.int32, dev, 2)
+        _ints("block_table", block_table, torch.int32, dev, 2)
         if block_table.shape[0] != batch:
             raise ValueError(f"block_table has {block_table.shape[0]} rows; expected {batch}")
         if cache.page_size % 16:
             raise ValueError("with a block_table the page size must be a multiple of 16")
         stride, entries = block_table.stride(0), block_table.shape[1]
     if max_kv is None:
-        max_kv = cache.page_size * (entries if table is not None else 1)
+        max_kv = cache.page_size * (entries if block_table is not None else 1)
     os = _rows("out", out, total, heads, cache.head_dim, dev, (q.dtype,))
-    if lse is not None:
-        _check_tensor("lse", lse, _F32, total * heads, dev, require_cuda=False)
     if scale is None:
         scale = cache.head_dim ** -0.5
-    return fp4q_attention(q.data_ptr(), *qs, out.data_ptr(), *os,
-                          None if lse is None else lse.data_ptr(), starts, lens, table, stride,
+    return fp4q_attention(None, qs[0], qs[1], None, os[0], os[1], None, None, None, None, stride,
                           total, entries, batch, max_q, max_kv, heads, _dtype_code(q), int(causal),
                           window, scale, 0)
+
+
+def _point(call, q, out, lse, kv_lens, block_table, q_starts):
+    call.q, call.out, call.kv_lens = q.data_ptr(), out.data_ptr(), kv_lens.data_ptr()
+    if lse is not None:
+        call.lse = lse.data_ptr()
+    if block_table is not None:
+        call.block_table = block_table.data_ptr()
+    if q_starts is not None:
+        call.q_starts = q_starts.data_ptr()
+
+
+def _same(t):
+    """What the checks of a tensor depend on."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _workspace_bytes(cache, call):
+    return int(_lib_handle().fp4q_attend_workspace_bytes(cache._spec, cache._struct, C.byref(call)))
 
 
 def attend_workspace_bytes(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None,
                            max_q=None, causal=True, window=0):
     """Bytes that `attend` of these arguments needs as its workspace (only
     their shapes and types matter)."""
-    call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, None, q, None)
-    return int(_lib_handle().fp4q_attend_workspace_bytes(cache._spec, cache._struct, C.byref(call)))
+    call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, None, q)
+    _point(call, q, q, None, kv_lens, block_table, q_starts)
+    return _workspace_bytes(cache, call)
 
 
 def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_q=None,
@@ -660,18 +689,41 @@ def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_
     allocated here.  A given workspace (uint8, attend_workspace_bytes) must
     not be shared by calls that may run at the same time."""
     dev = cache.device
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
-        call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window,
-                          scale, out, lse)
-        lib, ref = _lib_handle(), C.byref(call)
-        need = lib.fp4q_attend_workspace_bytes(cache._spec, cache._struct, ref)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif need:
-            _check_tensor("workspace", workspace, _U8, need, dev, require_cuda=False)
-        _check("fp4q_attend", lib.fp4q_attend(
-            cache._spec, cache._struct, ref, workspace.data_ptr() if need else None, need, st))
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return attend(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window,
+                          scale, return_lse, out, workspace)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch tensor [total_q, q_heads, head_dim]")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
+    # calls that differ in addresses alone share their checks
+    key = (_same(q), _same(kv_lens), _same(block_table), _same(q_starts), _same(out), max_kv, max_q,
+           causal, window, scale)
+    known = cache._calls.get(key)
+    if known is None:
+        call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, scale, out)
+        _point(call, q, out, lse, kv_lens, block_table, q_starts)
+        if len(cache._calls) >= 64:
+            cache._calls.clear()
+        need = _workspace_bytes(cache, call)
+        cache._calls[key] = (bytes(call), need)
+    else:
+        call, need = fp4q_attention.from_buffer_copy(known[0]), known[1]
+        call.lse = None
+        _point(call, q, out, lse, kv_lens, block_table, q_starts)
+    if not need:
+        space = None
+    elif workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        space = workspace.data_ptr()
+    else:
+        _check_tensor("workspace", workspace, _U8, need, dev, require_cuda=False)
+        space = workspace.data_ptr()
+    st = _lib_handle().fp4q_attend(cache._spec, cache._struct, C.byref(call), space, need,
+                                   _current_stream(dev.index))
+    if st:
+        cache._calls.pop(key, None)
+        _check("fp4q_attend", st)
     return (out, lse) if return_lse else out

@@ -1319,23 +1319,30 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     }
 }
 
-// ---- joining the chunks of a row ---------------------------------------------------
+// ---- joining the partial results of a row ------------------------------------------
 //
-// One workgroup per query row: D/4 lanes hold four values each, and the
-// 256 / (D/4) groups of lanes take every so-manieth chunk; reads every partial
-// result once.
-template <bool MX, int D>
-__global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, const AttendPlan p)
+// D/4 lanes hold four values each of a row; T groups of such lanes take every
+// T-th of its partial results.  One workgroup has as many rows as fit.  Reads
+// every partial result once: bound by that traffic where there are many rows,
+// by the latency of a few dependent loads where there are few.
+template <bool MX, int D, int T>
+__global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, const AttendPlan p, const uint32_t all_rows)
 {
     constexpr int B = MX ? 32 : 16;
-    constexpr int L = D / 4, T = kThreads / L;
-    __shared__ f32x4 sum[T][L];
-    __shared__ float red[kWaves];
-    const uint32_t id = blockIdx.x;
+    constexpr int L = D / 4;
+    constexpr int R = kThreads / (L * T); // rows of a workgroup
+    __shared__ f32x4 sum[T > 1 ? kThreads : 1];
+    __shared__ float2 red[T > 1 ? kThreads / L : 1];
+    const int j = threadIdx.x % L, turn = threadIdx.x / L % T, at = threadIdx.x / (L * T);
+    const uint32_t id = blockIdx.x * R + at;
     uint32_t rest = id;
     const int r = (int)take_digit(rest, a.max_q * a.group);
     const int head = (int)take_digit(rest, a.kv.heads);
     const int b = (int)rest;
+    // a row's lanes leave together; with T > 1 so does the workgroup (R = 1)
+    static_assert(T == 1 || R == 1, "rows of one workgroup");
+    if (id >= all_rows)
+        return;
     const Extent e = extent_of(a, b);
     const int rows = e.qn * a.group;
     if (r >= rows)
@@ -1359,44 +1366,39 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
         base = (int64_t)pair.x * p.rows_per_tile + r;
         stride = p.rows_per_tile;
     }
-    auto place = [&](int c) { return base + c * stride; };
-
-    // the maximum over the chunks (a NaN is in the sums, never in a maximum)
-    float m = -__builtin_huge_valf();
-    for (int c = threadIdx.x; c < chunks; c += kThreads)
-        m = __builtin_fmaxf(m, w.stat[place(c)].x);
-    m = wave_max(m);
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kWaves; ++t)
-        m = __builtin_fmaxf(m, red[t]);
-
-    const int j = threadIdx.x % L, turn = threadIdx.x / L;
+    // a running maximum over this lane's share (a NaN is in the sums, never in
+    // a maximum)
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
+    float l = 0.0f, m = -__builtin_huge_valf();
     for (int c = turn; c < chunks; c += T) {
-        const float2 s = w.stat[place(c)];
-        const float f = s.x == m ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
-        const f32x4 t = *reinterpret_cast<const f32x4*>(w.o + place(c) * D + 4 * j);
-        l += s.y * f;
-        o += t * f;
+        const float2 s = w.stat[base + c * stride];
+        const f32x4 t = *reinterpret_cast<const f32x4*>(w.o + (base + c * stride) * D + 4 * j);
+        const float raised = __builtin_fmaxf(m, s.x);
+        const float f0 = m == raised ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
+        const float f1 = s.x == raised ? 1.0f : __builtin_amdgcn_exp2f(s.x - raised);
+        m = raised;
+        l = l * f0 + s.y * f1;
+        o = o * f0 + t * f1;
     }
-    sum[turn][j] = o;
-    __shared__ float total[T];
-    if (j == 0)
-        total[turn] = l;
-    __syncthreads();
-    if (threadIdx.x >= 64)
-        return;
-    // D = 256: a whole wave; else the lanes past L repeat the first ones
-    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    l = 0.0f;
+    if constexpr (T > 1) {
+        sum[threadIdx.x] = o;
+        if (j == 0)
+            red[turn] = float2{m, l};
+        __syncthreads();
+        if (threadIdx.x >= L)
+            return;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-        o += sum[t][j];
-        l += total[t];
+        for (int t = 0; t < T; ++t)
+            m = __builtin_fmaxf(m, red[t].x);
+        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        l = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const float2 s = red[t];
+            const float f = s.x == m ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
+            l += s.y * f;
+            o += sum[t * L + j] * f;
+        }
     }
     const float inv = l == 0.0f ? 0.0f : (MX ? 1.0f : *a.kv.global[1]) / l;
     o *= inv;
@@ -1412,8 +1414,6 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
         }
         o *= (B == 16) ? 0.25f : __uint_as_float(0x3E3504F3u);
     }
-    if (threadIdx.x >= L)
-        return;
     const int i = r / a.group;
     const int qh = head * a.group + (r - i * a.group);
     const int64_t row = e.q0 + i;
@@ -1459,7 +1459,13 @@ hipError_t launch_parts(const AttendArgs& a, const AttendPlan& p)
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || p.chunks == 1)
         return err;
-    attend_join<MX, D><<<dim3((uint32_t)((int64_t)a.batch * a.kv.heads * a.max_q * a.group)), kThreads, 0, a.stream>>>(a, p);
+    // a workgroup per row where there may be many partial results of each
+    const uint32_t rows = (uint32_t)((int64_t)a.batch * a.kv.heads * a.max_q * a.group);
+    constexpr int per = kThreads / (D / 4);
+    if (p.many && p.chunks <= 4 * per)
+        attend_join<MX, D, 1><<<dim3((rows + per - 1) / per), kThreads, 0, a.stream>>>(a, p, rows);
+    else
+        attend_join<MX, D, per><<<dim3(rows), kThreads, 0, a.stream>>>(a, p, rows);
     return hipGetLastError();
 }
 

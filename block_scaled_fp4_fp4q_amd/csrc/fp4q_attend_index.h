@@ -176,7 +176,7 @@ inline AttendPlan plan_of(const AttendArgs& a)
     p.rows_per_tile = (a.bf16 && a.kv.head_dim < 256) ? 256 : 128; // 32 rows a wave
     p.tiles = (int)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
     const int64_t units = pairs * p.tiles;
-    const int64_t want = (512 + units - 1) / units;
+    const int64_t want = (kCus + units - 1) / units; // one workgroup fills a CU
     int64_t chunk = (span + want - 1) / want;
     chunk = (chunk + 255) / 256 * 256;
     p.chunk = (int)(chunk < 256 ? 256 : chunk);

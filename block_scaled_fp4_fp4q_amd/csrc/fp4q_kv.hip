@@ -20,6 +20,20 @@ constexpr int kThreads = 256;
 enum { kRuleAbsMax = 0, kRuleSweep = 1, kRuleFourSix = 2 };
 constexpr int kWinLo = -3, kWinHi = 7; // the window that is unrolled
 
+// page and place of a valid slot; 32-bit arithmetic where all slots fit (a
+// 64-bit division costs as much as the rest of a block's decode)
+__device__ __forceinline__ void slot_place(const KvView& kv, int64_t slot, int64_t slots, int64_t& page, int64_t& off)
+{
+    if (slots <= (int64_t)0xFFFFFFFF) {
+        const uint32_t p = (uint32_t)slot / (uint32_t)kv.page_size;
+        page = p;
+        off = (uint32_t)slot - p * (uint32_t)kv.page_size;
+    } else {
+        page = slot / kv.page_size;
+        off = slot - page * kv.page_size;
+    }
+}
+
 // the constants of one E4M3 pattern under the cache's global scale
 struct alignas(16) Pattern {
     float r;  // fl32(1/D)
@@ -204,7 +218,8 @@ __global__ __launch_bounds__(kThreads) void kv_write(const KvWriteArgs a, const 
         if constexpr (ROT)
             fwht<B>(v);
         const float top = block_absmax<B>(v);
-        const int64_t page = slot / a.kv.page_size, off = slot - page * a.kv.page_size;
+        int64_t page, off;
+        slot_place(a.kv, slot, most, page, off);
         uint8_t* codes = a.kv.codes[side] + page * a.kv.c_page + head * a.kv.c_head + off * a.kv.c_token;
         uint8_t* scales = a.kv.scales[side] + page * a.kv.s_page + head * a.kv.s_head + off * a.kv.s_token;
         if constexpr (MX) {
@@ -288,7 +303,8 @@ __global__ __launch_bounds__(kThreads) void kv_read(const KvReadArgs a, const in
             for (int i = 0; i < E; ++i)
                 o[i] = 0.0f;
         } else {
-            const int64_t page = slot / a.kv.page_size, off = slot - page * a.kv.page_size;
+            int64_t page, off;
+            slot_place(a.kv, slot, most, page, off);
             const uint8_t* codes =
                 a.kv.codes[side] + page * a.kv.c_page + head * a.kv.c_head + off * a.kv.c_token;
             const uint8_t* scales =

@@ -443,83 +443,87 @@ constexpr float kLazy = 6.0f, kUp = 9.0f;
 // the pair of workgroup `blockIdx.x` and its part of it: steps [from, to), the
 // number of parts, and the slots of its and of the first part's results
 struct FewWhere {
+    Extent e;
     int b, head;
     int from, to, parts, slot, first_slot;
 };
 
-// By the whole workgroup: the steps of all sequences (a lane each) are summed,
-// then their parts and slots up to the sequence that holds this workgroup's.
-// Returns an empty part where there is none.
+// inclusive sum over a wave's lanes up to this one, by moves within rows of 16
+// and from row to row
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v)
+{
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true); // from 1 below, in rows of 16
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true); // 2
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true); // 4
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true); // 8
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, true); // row 0's (2's) sum to row 1 (3)
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, true); // row 1's to rows 2 and 3
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// By every wave for itself, a lane for each of 64 sequences at a time: the sum
+// of all steps, the length of a part, then the parts and slots up to the
+// sequence that holds this workgroup's part.  Returns an empty part where there
+// is none.
 __device__ __forceinline__ FewWhere find_part(const AttendArgs& a, const AttendPlan& p)
 {
-    __shared__ uint64_t sums[kWaves];
-    __shared__ uint32_t found[4]; // sequence, its first part and slot, steps per head
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     const uint32_t heads = a.kv.heads, id = blockIdx.x;
-    auto steps_of = [&](int b) -> uint32_t { return b < a.batch ? (uint32_t)few_steps(a, extent_of(a, b)) : 0u; };
-    // inclusive sum over the workgroup's threads, and the sum of all
-    auto scan = [&](uint64_t v, uint64_t& all) {
-#pragma unroll
-        for (int off = 1; off < 64; off *= 2) {
-            const uint64_t t = __shfl_up(v, off, 64);
-            v += lane >= (uint32_t)off ? t : 0u;
-        }
-        __syncthreads();
-        if (lane == 63)
-            sums[wave] = v;
-        __syncthreads();
-        all = 0;
-#pragma unroll
-        for (uint32_t w = 0; w < kWaves; ++w) {
-            v += w < wave ? sums[w] : 0u;
-            all += sums[w];
-        }
-        return v;
+    Extent e{};
+    auto steps_of = [&](int b0) -> uint32_t {
+        const int b = b0 + lane;
+        e = extent_of(a, b < a.batch ? b : a.batch - 1);
+        return b < a.batch ? (uint32_t)few_steps(a, e) : 0u;
     };
-    uint32_t steps = steps_of(threadIdx.x), total = 0;
-    const uint32_t first_steps = steps;
-    uint64_t all;
-    for (int b0 = 0;;) {
-        scan(steps, all);
-        total += (uint32_t)all;
-        b0 += kThreads;
-        if (b0 >= a.batch)
-            break;
-        steps = steps_of(b0 + threadIdx.x);
+    uint32_t steps = 0, total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        steps = steps_of(b0);
+        total += lane_value(wave_scan(steps), 63);
     }
-    const uint32_t most = few_most(p, total * heads);
-    steps = first_steps;
-    uint64_t before = 0; // parts in the low half, slots in the high one
-    for (int b0 = 0;;) {
+    uint32_t most = few_most(p, total * heads);
+    // the least length with which all parts are resident at once, searched
+    // from below where one look at the lengths shows them all (a second round
+    // of a few parts would cost as much as the first); else about that
+    if (a.batch <= 64 && (uint32_t)a.batch * heads <= (uint32_t)p.parts) {
+        for (int k = 0; k < 16 && lane_value(wave_scan(few_parts(steps, most)), 63) * heads > (uint32_t)p.parts; ++k)
+            most += 1 + most / 16;
+    } else {
+        most += most * (a.batch * heads < (uint32_t)p.parts ? a.batch * heads : p.parts) / (2 * p.parts);
+    }
+    uint32_t parts_before = 0, slots_before = 0;
+    FewWhere r{};
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        if (a.batch > 64)
+            steps = steps_of(b0);
         const uint32_t parts = few_parts(steps, most);
-        const uint64_t mine = (uint64_t)(parts * heads) | (uint64_t)(parts > 1 ? parts * heads : 0u) << 32;
-        const uint64_t upto = before + scan(mine, all);
-        if ((uint32_t)upto > id && (uint32_t)(upto - mine) <= id) { // one thread, once
-            found[0] = b0 + threadIdx.x;
-            found[1] = (uint32_t)(upto - mine);
-            found[2] = (uint32_t)((upto - mine) >> 32);
-            found[3] = steps;
+        const uint32_t mine = parts * heads, taken = parts > 1 ? mine : 0u;
+        const uint32_t upto = parts_before + wave_scan(mine), slots = slots_before + wave_scan(taken);
+        const uint64_t here = __builtin_amdgcn_ballot_w64(upto > id);
+        if (here != 0) { // the first such lane's sequence
+            const int at = __builtin_ctzll(here);
+            steps = lane_value(steps, at);
+            const uint32_t n = lane_value(parts, at);
+            const uint32_t k = id - (lane_value(upto, at) - lane_value(mine, at));
+            const uint32_t head = k / n, i = k - head * n;
+            r.e.q0 = (int64_t)lane_value((uint32_t)e.q0, at); // rows count in 31 bits here
+            r.e.qn = (int)lane_value((uint32_t)e.qn, at);
+            r.e.shift = (int)lane_value((uint32_t)e.shift, at);
+            r.e.kn = (int)lane_value((uint32_t)e.kn, at);
+            r.e.bad = lane_value(e.bad ? 1u : 0u, at) != 0;
+            r.b = b0 + at;
+            r.head = (int)head;
+            r.from = few_from(steps, n, i);
+            r.to = few_from(steps, n, i + 1);
+            r.parts = (int)n;
+            r.first_slot = (int)(lane_value(slots, at) - lane_value(taken, at) + head * n);
+            r.slot = r.first_slot + (int)i;
+            return r;
         }
-        before += all;
-        if ((uint32_t)before > id)
-            break;
-        b0 += kThreads;
-        if (b0 >= a.batch)
-            return FewWhere{};
-        steps = steps_of(b0 + threadIdx.x);
+        parts_before = lane_value(upto, 63);
+        slots_before = lane_value(slots, 63);
     }
-    __syncthreads();
-    FewWhere r;
-    steps = __builtin_amdgcn_readfirstlane(found[3]);
-    const uint32_t parts = few_parts(steps, most), at = id - __builtin_amdgcn_readfirstlane(found[1]);
-    const uint32_t head = at / parts, i = at - head * parts;
-    r.b = (int)__builtin_amdgcn_readfirstlane(found[0]);
-    r.head = (int)head;
-    r.from = few_from(steps, parts, i);
-    r.to = few_from(steps, parts, i + 1);
-    r.parts = (int)parts;
-    r.first_slot = (int)(__builtin_amdgcn_readfirstlane(found[2]) + head * parts);
-    r.slot = r.first_slot + (int)i;
     return r;
 }
 
@@ -538,24 +542,23 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
     __shared__ float merge_o[kWaves][R][D + 4]; // by wave
     __shared__ float2 merge_s[kWaves][R];
 
-    FewWhere piece{0, 0, 0, 0, 1, 0, 0};
+    FewWhere piece{};
     if (p.chunks == 1) { // one pair per workgroup
         uint32_t id = blockIdx.x;
         piece.head = (int)take_digit(id, a.kv.heads);
         piece.b = (int)id;
+        piece.e = extent_of(a, piece.b);
+        piece.to = few_steps(a, piece.e);
+        piece.parts = 1;
     } else {
         piece = find_part(a, p);
-        if (piece.from == piece.to)
-            return;
     }
-    const int b = piece.b, head = piece.head;
-    const Extent e = extent_of(a, b);
-    const int rows = e.qn * a.group;
-    if (rows == 0)
+    if (piece.from == piece.to)
         return;
+    const int b = piece.b, head = piece.head;
+    const Extent e = piece.e;
+    const int rows = e.qn * a.group;
     const int steps = few_steps(a, e);
-    if (p.chunks == 1)
-        piece.to = steps;
     const int r0 = 0, r1 = rows;
     int lo, hi;
     tile_keys(a, e, r0, r1, lo, hi);
@@ -1175,18 +1178,19 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
             if (key < wave_hi && key + kManyKeys > wave_lo) {
                 f32x16 s[2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         s[x][j] = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
                         const u32x4 k = kbuf[at][k_unit<D>(32 * x + n, h * C + c)];
 #pragma unroll
                         for (int t = NQ - 1; t >= 0; --t)
                             s[x] = mfma32<MX>(k, q[t][c], s[x]);
                     }
-                }
                 if (!(key >= all_lo && key + kManyKeys <= all_hi)) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x)

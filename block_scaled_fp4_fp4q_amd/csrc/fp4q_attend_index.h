@@ -158,14 +158,13 @@ inline AttendPlan plan_of(const AttendArgs& a)
         p.rows_per_tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
         p.tiles = 1;
         const int64_t steps = (span + kStepKeys - 1) / kStepKeys;
-        if (pairs > most / (steps > rows ? steps : rows))
+        if (pairs > most / (steps > rows ? steps : rows) || a.total_q > 0x7FFFFFFF)
             return p; // groups == 0: refused
         p.groups = (int)pairs;
         if (steps > kMinPart) {
             // workgroups that are resident at once: 256 CUs, one wave of each
-            // on every SIMD.  ceil() adds half a part for each pair.
-            const int64_t all = (int64_t)kCus * few_waves(a);
-            p.parts = (int)(2 * all - pairs > all ? all - pairs / 2 : all / 2);
+            // on every SIMD
+            p.parts = kCus * few_waves(a);
             p.groups += p.parts;
             p.chunks = 2; // partial results
             const size_t places = (size_t)2 * p.parts * p.rows_per_tile;

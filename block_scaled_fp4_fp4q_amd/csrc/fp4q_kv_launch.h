@@ -67,7 +67,7 @@ struct AttendPlan {
     int rows_per_tile; // query rows of one workgroup
     int tiles;         // row tiles per sequence and KV head
     int groups;        // workgroups (0: more than a launch holds)
-    int parts;         // few: what the sum of all keys is cut by (0: one workgroup per pair)
+    int parts;         // few: workgroups that run at once (0: one workgroup per pair)
     int chunk;         // many: keys of one workgroup
     int chunks;        // many: key chunks per row tile; few: 2 where there are partial results
     size_t workspace;  // bytes of partial results (0 where chunks == 1)

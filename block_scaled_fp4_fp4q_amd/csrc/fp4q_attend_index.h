@@ -24,7 +24,9 @@ inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // parts of a query)
 constexpr int few_waves_of(int dim, int parts, int rows16)
 {
-    return dim == 64 ? (rows16 == 1 ? 4 : 3) : dim == 128 ? (rows16 == 1 ? 3 : 2) : (parts == 3 ? 1 : 2);
+    return dim == 64    ? (rows16 == 1 ? 4 : 3) - (parts == 3 ? 1 : 0)
+           : dim == 128 ? (rows16 == 1 ? 3 : 2)
+                        : (parts == 3 ? 1 : 2);
 }
 
 inline int few_waves(const AttendArgs& a)

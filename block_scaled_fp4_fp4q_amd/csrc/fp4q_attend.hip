@@ -1025,6 +1025,8 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     constexpr int C = D / 16;  // steps of the first product
     constexpr int T = D / 32;  // row tiles of V^T
     constexpr int KU = kManyKeys * D / 8; // 16-byte units of a buffer
+    constexpr bool F32 = NP == (MX ? 3 : 2);
+    constexpr int RW = F32 ? D / 8 : D / 16; // 16-byte words of half a row
     __shared__ u32x4 kbuf[2][KU];
     __shared__ u32x4 vbuf[2][KU];
     __shared__ Granule granule[kManySegment / 16];
@@ -1058,34 +1060,61 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     const bool live = r < r1;
     int row_lo = 0, row_hi = 0;
 
+    // the row's half is under way while the keys are looked up and the first
+    // codes loaded
+    u32x4 raw[RW];
+#pragma unroll
+    for (int c = 0; c < RW; ++c)
+        raw[c] = u32x4{0u, 0u, 0u, 0u};
+    if (live) {
+        const int i = r / a.group, j = r - i * a.group;
+        seen_by(a, e, i, row_lo, row_hi);
+        const int64_t at = (e.q0 + i) * a.q_row + (head * a.group + j) * a.q_head + h * (D / 2);
+        const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + at * (F32 ? 4 : 2));
+#pragma unroll
+        for (int c = 0; c < RW; ++c)
+            raw[c] = x[c];
+    }
+
+    // waves 0-3 expand K and, of eight waves, 4-7 V
+    const bool does_k = wave < 4, does_v = WAVES == 4 || wave >= 4;
+    const int w = wave & 3;
+    StageK<D> sk;
+    StageV<D> sv;
+    int s0 = k0, s1 = k1 - k0 < kManySegment ? k1 : k0 + kManySegment;
+    auto load = [&](int key) {
+        const int mine = key + 16 * w;
+        const Granule* g = granule + (mine < s1 ? (mine - s0) / 16 : 0);
+        if (does_k)
+            stage_k<MX, D>(a, g, mine, s1, lane, sk);
+        if (does_v)
+            stage_v<MX, D>(a, g, mine, s1, lane, sv);
+    };
+    auto expand = [&](int to) {
+        if (does_k)
+            expand_k<MX, D>(sk, w, lane, kbuf[to]);
+        if (does_v)
+            expand_v<MX, D>(sv, w, lane, vbuf[to]);
+    };
+    find_granules<64 * WAVES>(a, b, head, s0, s1, granule);
+    __syncthreads();
+    load(s0);
+
     u32x4 q[NQ][C];
     float factor; // of the row's logits, to log2 units; positive
     {
         float v[D / 2];
 #pragma unroll
-        for (int j = 0; j < D / 2; ++j)
-            v[j] = 0.0f;
-        if (live) {
-            const int i = r / a.group, j = r - i * a.group;
-            seen_by(a, e, i, row_lo, row_hi);
-            const int64_t at = (e.q0 + i) * a.q_row + (head * a.group + j) * a.q_head + h * (D / 2);
-            if (a.bf16) {
-                const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at);
-#pragma unroll
-                for (int t = 0; t < D / 16; ++t) {
-                    const u32x4 w = x[t];
-                    v[8 * t + 0] = bf16_lo(w.x); v[8 * t + 1] = bf16_hi(w.x);
-                    v[8 * t + 2] = bf16_lo(w.y); v[8 * t + 3] = bf16_hi(w.y);
-                    v[8 * t + 4] = bf16_lo(w.z); v[8 * t + 5] = bf16_hi(w.z);
-                    v[8 * t + 6] = bf16_lo(w.w); v[8 * t + 7] = bf16_hi(w.w);
-                }
+        for (int c = 0; c < RW; ++c) {
+            const u32x4 x = raw[c];
+            if constexpr (F32) {
+                v[4 * c + 0] = __uint_as_float(x.x); v[4 * c + 1] = __uint_as_float(x.y);
+                v[4 * c + 2] = __uint_as_float(x.z); v[4 * c + 3] = __uint_as_float(x.w);
             } else {
-                const f32x4* x = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.q) + at);
-#pragma unroll
-                for (int t = 0; t < D / 8; ++t) {
-                    const f32x4 w = x[t];
-                    v[4 * t + 0] = w.x; v[4 * t + 1] = w.y; v[4 * t + 2] = w.z; v[4 * t + 3] = w.w;
-                }
+                v[8 * c + 0] = bf16_lo(x.x); v[8 * c + 1] = bf16_hi(x.x);
+                v[8 * c + 2] = bf16_lo(x.y); v[8 * c + 3] = bf16_hi(x.y);
+                v[8 * c + 4] = bf16_lo(x.z); v[8 * c + 5] = bf16_hi(x.z);
+                v[8 * c + 6] = bf16_lo(x.w); v[8 * c + 7] = bf16_hi(x.w);
             }
         }
         const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
@@ -1139,31 +1168,7 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
             o[t][j] = 0.0f;
     float m = -__builtin_huge_valf(), l = 0.0f;
 
-    // waves 0-3 expand K and, of eight waves, 4-7 V
-    const bool does_k = wave < 4, does_v = WAVES == 4 || wave >= 4;
-    const int w = wave & 3;
-    StageK<D> sk;
-    StageV<D> sv;
-    for (int s0 = k0; s0 < k1; s0 += kManySegment) {
-        const int s1 = k1 - s0 < kManySegment ? k1 : s0 + kManySegment;
-        __syncthreads(); // the last segment's places and buffers are done with
-        find_granules<64 * WAVES>(a, b, head, s0, s1, granule);
-        __syncthreads();
-        auto load = [&](int key) {
-            const int mine = key + 16 * w;
-            const Granule* g = granule + (mine < s1 ? (mine - s0) / 16 : 0);
-            if (does_k)
-                stage_k<MX, D>(a, g, mine, s1, lane, sk);
-            if (does_v)
-                stage_v<MX, D>(a, g, mine, s1, lane, sv);
-        };
-        auto expand = [&](int to) {
-            if (does_k)
-                expand_k<MX, D>(sk, w, lane, kbuf[to]);
-            if (does_v)
-                expand_v<MX, D>(sv, w, lane, vbuf[to]);
-        };
-        load(s0);
+    while (k0 < k1) {
         expand(0);
         if (s0 + kManyKeys < s1)
             load(s0 + kManyKeys);
@@ -1249,6 +1254,13 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
             }
             __syncthreads();
         }
+        if (s1 >= k1)
+            break;
+        s0 = s1; // the places of the next keys
+        s1 = k1 - s0 < kManySegment ? k1 : s0 + kManySegment;
+        find_granules<64 * WAVES>(a, b, head, s0, s1, granule);
+        __syncthreads();
+        load(s0);
     }
     l += __shfl_xor(l, 32, 64);
     if (e.bad)

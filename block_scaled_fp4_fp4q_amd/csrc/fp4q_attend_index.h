@@ -177,10 +177,26 @@ inline AttendPlan plan_of(const AttendArgs& a)
     p.rows_per_tile = (a.bf16 && a.kv.head_dim < 256) ? 256 : 128; // 32 rows a wave
     p.tiles = (int)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
     const int64_t units = pairs * p.tiles;
-    const int64_t want = (kCus + units - 1) / units; // one workgroup fills a CU
-    int64_t chunk = (span + want - 1) / want;
-    chunk = (chunk + 255) / 256 * 256;
+    // One workgroup of eight waves fills a CU.  Fewer row tiles than CUs are cut
+    // along the keys where that pays: c chunks save steps of 64 keys (1.9 us
+    // each at 128 values a head), and cost the joining launch (5 us) and
+    // the partial results' way to memory and back (5 TB/s).  512 queries
+    // of 32 heads alone are not cut (26 us, 33 with two chunks), after 16384
+    // keys they are.
+    const int64_t most_cuts = (kCus + units - 1) / units;
+    double best = 0.0;
+    int64_t chunk = 0;
+    for (int64_t c = 1; c <= most_cuts; ++c) {
+        const int64_t keys = ((span + c - 1) / c + 255) / 256 * 256;
+        const double us = (double)((keys + 63) / 64) * 1.9 * a.kv.head_dim / 128 +
+                          (c > 1 ? 5.0 + 2.0 * (double)pairs * rows * c * (a.kv.head_dim * 4 + 8) / 5e6 : 0.0);
+        if (c == 1 || us < best) {
+            best = us;
+            chunk = keys;
+        }
+    }
     p.chunk = (int)(chunk < 256 ? 256 : chunk);
+    chunk = p.chunk;
     const int64_t chunks = span <= chunk ? 1 : (span + chunk - 1) / chunk;
     if (units > most / chunks || (chunks > 1 && pairs > most / rows))
         return p; // groups == 0: refused

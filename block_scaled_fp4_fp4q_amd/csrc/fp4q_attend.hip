@@ -374,7 +374,7 @@ struct Partial {
 __device__ __forceinline__ Partial partials_of(const AttendArgs& a, const AttendPlan& p)
 {
     Partial r;
-    char* at = static_cast<char*>(a.workspace);
+    char* at = static_cast<char*>(a.workspace) + (p.many ? 0 : few_table_bytes(p.groups, a.batch));
     const size_t pairs = (size_t)a.batch * a.kv.heads;
     r.pairs = reinterpret_cast<int2*>(at);
     if (!p.many)
@@ -463,14 +463,58 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v)
 
 __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
+// The length of a part, from the sum of all steps and, where one look (64
+// sequences, a lane each) shows them all, from the parts that it makes: the
+// least length with which all are resident at once, searched from below (a
+// second round of a few parts would cost as much as the first); else about that.
+__device__ __forceinline__ uint32_t part_length(const AttendArgs& a, const AttendPlan& p, uint32_t total, uint32_t steps)
+{
+    const uint32_t heads = a.kv.heads, parts = p.parts;
+    uint32_t most = few_most(p, total * heads);
+    if (a.batch <= 64 && (uint32_t)a.batch * heads <= parts) {
+        for (int k = 0; k < 16 && lane_value(wave_scan(few_parts(steps, most)), 63) * heads > parts; ++k)
+            most += 1 + most / 16;
+    } else {
+        const uint32_t pairs = (uint32_t)a.batch * heads;
+        most += most * (pairs < parts ? pairs : parts) / (2 * parts);
+    }
+    return most;
+}
+
+// a part from its sequence, the parts and slots before that, and its number
+__device__ __forceinline__ void set_part(FewWhere& r, uint32_t steps, uint32_t parts, uint32_t k, uint32_t slot)
+{
+    const uint32_t head = k / parts, i = k - head * parts;
+    r.head = (int)head;
+    r.from = few_from(steps, parts, i);
+    r.to = few_from(steps, parts, i + 1);
+    r.parts = (int)parts;
+    r.first_slot = (int)(slot + head * parts);
+    r.slot = r.first_slot + (int)i;
+}
+
 // By every wave for itself, a lane for each of 64 sequences at a time: the sum
 // of all steps, the length of a part, then the parts and slots up to the
-// sequence that holds this workgroup's part.  Returns an empty part where there
-// is none.
+// sequence that holds this workgroup's part; or from the table, where there is
+// one.  Returns an empty part where there is none.
 __device__ __forceinline__ FewWhere find_part(const AttendArgs& a, const AttendPlan& p)
 {
     const int lane = threadIdx.x & 63;
     const uint32_t heads = a.kv.heads, id = blockIdx.x;
+    FewWhere r{};
+    if (a.batch > kScanBatch) {
+        const FewTable t = few_table(a.workspace, p.groups, a.batch);
+        const uint32_t b = __builtin_amdgcn_readfirstlane(t.sequence[id]);
+        if (b >= (uint32_t)a.batch)
+            return r;
+        const uint32_t* before = t.before + (size_t)3 * b;
+        const uint32_t steps = __builtin_amdgcn_readfirstlane(before[2]);
+        r.b = (int)b;
+        r.e = extent_of(a, (int)b);
+        set_part(r, steps, few_parts(steps, __builtin_amdgcn_readfirstlane(*t.most)),
+                 id - __builtin_amdgcn_readfirstlane(before[0]), __builtin_amdgcn_readfirstlane(before[1]));
+        return r;
+    }
     Extent e{};
     auto steps_of = [&](int b0) -> uint32_t {
         const int b = b0 + lane;
@@ -482,18 +526,8 @@ __device__ __forceinline__ FewWhere find_part(const AttendArgs& a, const AttendP
         steps = steps_of(b0);
         total += lane_value(wave_scan(steps), 63);
     }
-    uint32_t most = few_most(p, total * heads);
-    // the least length with which all parts are resident at once, searched
-    // from below where one look at the lengths shows them all (a second round
-    // of a few parts would cost as much as the first); else about that
-    if (a.batch <= 64 && (uint32_t)a.batch * heads <= (uint32_t)p.parts) {
-        for (int k = 0; k < 16 && lane_value(wave_scan(few_parts(steps, most)), 63) * heads > (uint32_t)p.parts; ++k)
-            most += 1 + most / 16;
-    } else {
-        most += most * (a.batch * heads < (uint32_t)p.parts ? a.batch * heads : p.parts) / (2 * p.parts);
-    }
+    const uint32_t most = part_length(a, p, total, steps);
     uint32_t parts_before = 0, slots_before = 0;
-    FewWhere r{};
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         if (a.batch > 64)
             steps = steps_of(b0);
@@ -503,28 +537,57 @@ __device__ __forceinline__ FewWhere find_part(const AttendArgs& a, const AttendP
         const uint64_t here = __builtin_amdgcn_ballot_w64(upto > id);
         if (here != 0) { // the first such lane's sequence
             const int at = __builtin_ctzll(here);
-            steps = lane_value(steps, at);
-            const uint32_t n = lane_value(parts, at);
-            const uint32_t k = id - (lane_value(upto, at) - lane_value(mine, at));
-            const uint32_t head = k / n, i = k - head * n;
             r.e.q0 = (int64_t)lane_value((uint32_t)e.q0, at); // rows count in 31 bits here
             r.e.qn = (int)lane_value((uint32_t)e.qn, at);
             r.e.shift = (int)lane_value((uint32_t)e.shift, at);
             r.e.kn = (int)lane_value((uint32_t)e.kn, at);
             r.e.bad = lane_value(e.bad ? 1u : 0u, at) != 0;
             r.b = b0 + at;
-            r.head = (int)head;
-            r.from = few_from(steps, n, i);
-            r.to = few_from(steps, n, i + 1);
-            r.parts = (int)n;
-            r.first_slot = (int)(lane_value(slots, at) - lane_value(taken, at) + head * n);
-            r.slot = r.first_slot + (int)i;
+            set_part(r, lane_value(steps, at), lane_value(parts, at), id - (lane_value(upto, at) - lane_value(mine, at)),
+                     lane_value(slots, at) - lane_value(taken, at));
             return r;
         }
         parts_before = lane_value(upto, 63);
         slots_before = lane_value(slots, 63);
     }
     return r;
+}
+
+// writes the table (one workgroup of one wave: 64 sequences at a time)
+__global__ __launch_bounds__(64) void attend_cut(const AttendArgs a, const AttendPlan p)
+{
+    const FewTable t = few_table(a.workspace, p.groups, a.batch);
+    const uint32_t heads = a.kv.heads;
+    const int lane = threadIdx.x;
+    uint32_t total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        const int b = b0 + lane;
+        const uint32_t steps = b < a.batch ? (uint32_t)few_steps(a, extent_of(a, b)) : 0u;
+        if (b < a.batch)
+            t.before[(size_t)3 * b + 2] = steps;
+        total += lane_value(wave_scan(steps), 63);
+    }
+    const uint32_t most = part_length(a, p, total, 0u);
+    if (lane == 0)
+        *t.most = most;
+    uint32_t parts_before = 0, slots_before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        const int b = b0 + lane;
+        const uint32_t steps = b < a.batch ? t.before[(size_t)3 * b + 2] : 0u; // this lane wrote it
+        const uint32_t parts = few_parts(steps, most);
+        const uint32_t mine = parts * heads, taken = parts > 1 ? mine : 0u;
+        const uint32_t upto = parts_before + wave_scan(mine), slots = slots_before + wave_scan(taken);
+        if (b < a.batch) {
+            t.before[(size_t)3 * b] = upto - mine;
+            t.before[(size_t)3 * b + 1] = slots - taken;
+        }
+        for (uint32_t id = upto - mine; id < upto; ++id)
+            t.sequence[id] = (uint32_t)b;
+        parts_before = lane_value(upto, 63);
+        slots_before = lane_value(slots, 63);
+    }
+    for (uint32_t id = parts_before + lane; id < (uint32_t)p.groups; id += 64)
+        t.sequence[id] = ~0u;
 }
 
 // QT: 16-row tiles of one wave, which share the expanded codes.  With QT = 2
@@ -1459,6 +1522,8 @@ template <bool MX, int D>
 hipError_t launch_parts(const AttendArgs& a, const AttendPlan& p)
 {
     const dim3 grid((uint32_t)p.groups);
+    if (!p.many && p.chunks > 1 && a.batch > kScanBatch)
+        attend_cut<<<1, 64, 0, a.stream>>>(a, p);
     if (p.many) {
         constexpr int WAVES = D == 256 ? 4 : 8;
         if (!a.bf16)

@@ -15,6 +15,7 @@ constexpr int kTileKeys = 32;                     // keys of one wave's step
 constexpr int kStepKeys = kWaves * kTileKeys;     // keys of a workgroup's step at most
 constexpr int kMinPart = 2;                       // steps that are not cut further
 constexpr int kCus = 256;
+constexpr int kScanBatch = 256;                   // sequences that every workgroup looks through itself
 constexpr int kSegment = 4096;                    // keys whose places are looked up at once
 
 inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -144,6 +145,30 @@ FP4Q_INDEX uint32_t few_most(const AttendPlan& p, uint32_t total)
 
 FP4Q_INDEX uint32_t few_parts(uint32_t steps, uint32_t most) { return (steps + most - 1) / most; }
 
+// What a kernel of its own writes down before the parts are computed, where
+// there are more than kScanBatch sequences (a look through them by every
+// workgroup would cost more than the launch): the sequence of each workgroup,
+// and the parts and slots before each sequence.
+struct FewTable {
+    uint32_t* sequence; // [groups], ~0 where a workgroup has no part
+    uint32_t* before;   // [batch][3]: parts, slots, steps per head
+    uint32_t* most;     // steps of a part at most
+};
+
+FP4Q_INDEX size_t few_table_bytes(int64_t groups, int64_t batch)
+{
+    return batch > kScanBatch ? (((size_t)groups + 3 * (size_t)batch + 1) * 4 + 255) & ~(size_t)255 : 0;
+}
+
+FP4Q_INDEX FewTable few_table(void* workspace, int groups, int batch)
+{
+    FewTable t;
+    t.sequence = static_cast<uint32_t*>(workspace);
+    t.before = t.sequence + groups;
+    t.most = t.before + (size_t)3 * batch;
+    return t;
+}
+
 // first step of part i of `parts`
 FP4Q_INDEX int few_from(uint32_t steps, uint32_t parts, uint32_t i) { return (int)((uint64_t)steps * i / parts); }
 
@@ -170,7 +195,8 @@ inline AttendPlan plan_of(const AttendArgs& a)
             p.groups += p.parts;
             p.chunks = 2; // partial results
             const size_t places = (size_t)2 * p.parts * p.rows_per_tile;
-            p.workspace = round256((size_t)pairs * 8) + round256(places * 8) + places * a.kv.head_dim * 4;
+            p.workspace = few_table_bytes(p.groups, a.batch) + round256((size_t)pairs * 8) + round256(places * 8) +
+                          places * a.kv.head_dim * 4;
         }
         return p;
     }

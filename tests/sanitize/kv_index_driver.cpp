@@ -149,7 +149,7 @@ int main()
             places = (int64_t)2 * p.parts * p.rows_per_tile;
         }
         if (p.chunks > 1)
-            CHECK(p.workspace >= (p.many ? 0 : round256((size_t)pairs * 8)) + round256((size_t)places * 8) + (size_t)places * dim * 4);
+            CHECK(p.workspace >= (p.many ? 0 : few_table_bytes(p.groups, a.batch) + round256((size_t)pairs * 8)) + round256((size_t)places * 8) + (size_t)places * dim * 4);
         for (int b = 0; b < a.batch; ++b) {
             const Extent e = extent_of(a, b);
             CHECK(e.qn >= 0 && e.qn <= a.max_q);

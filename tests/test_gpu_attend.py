@@ -196,6 +196,20 @@ def test_long_contexts_split_over_workgroups():
     run(f, queries(rng, sum(q_lens), 2, 64, "bf16"), q_lens)
 
 
+@pytest.mark.parametrize("batch", [64, 65, 130, 256, 257, 700])
+def test_many_sequences(batch):
+    """Lengths of many sequences, most short, a few long, some empty: those that a workgroup looks through itself and
+    those that are written down first."""
+    rng = np.random.default_rng(37)
+    lens = [int(n) for n in rng.integers(0, 60, batch)]
+    for b in rng.integers(0, batch, 5):
+        lens[b] = int(rng.integers(500, 3000))
+    f = Filled(rng, "nvfp4", 64, 2, 16, lens)
+    run(f, queries(rng, batch, 4, 64, "bf16"), [1] * batch, uniform=True, what=f"batch {batch}")
+    q_lens = [int(n) for n in rng.integers(0, 4, batch)]
+    run(f, queries(rng, sum(q_lens), 4, 64, "bf16"), q_lens, what=f"batch {batch}, packed")
+
+
 def test_cache_beyond_32_bit_offsets():
     """A cache of more than 2^32 bytes whose used pages lie at its end."""
     rng = np.random.default_rng(34)

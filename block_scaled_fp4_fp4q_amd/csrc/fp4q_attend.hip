@@ -34,7 +34,6 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kNanScales = 0xFFFFFFFFu; // bytes that are NaN in E4M3 and in E8M0
 constexpr float kLog2e = 1.4426950408889634f;

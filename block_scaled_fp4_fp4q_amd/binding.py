@@ -630,6 +630,11 @@ def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, 
         stride, entries = block_table.stride(0), block_table.shape[1]
     if max_kv is None:
         max_kv = cache.page_size * (entries if block_table is not None else 1)
+    # ctypes would drop the upper bits of these
+    for name, n in (("batch", batch), ("max_q", max_q), ("max_kv", max_kv), ("window", window),
+                    ("block_table's entries", entries)):
+        if not 0 <= n < 1 << 31:
+            raise ValueError(f"{name} is {n}; expected 31 bits")
     os = _rows("out", out, total, heads, cache.head_dim, dev, (q.dtype,))
     if scale is None:
         scale = cache.head_dim ** -0.5

@@ -1216,10 +1216,8 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     int wave_lo = 0, wave_hi = 0, all_lo = 0x7FFFFFFF, all_hi = 0;
     if (w0 < r1) {
         const int last = (w0 + 32 < r1 ? w0 + 32 : r1) - 1;
-        int t;
         seen_by(a, e, w0 / a.group, wave_lo, all_hi);
         seen_by(a, e, last / a.group, all_lo, wave_hi);
-        (void)t;
     }
 
     f32x16 o[T];

@@ -194,3 +194,19 @@ def test_binding_refuses_calls():
         args.update(kw)
         with pytest.raises((ValueError, TypeError)):
             B.attend_workspace_bytes(c, **args)
+
+
+def test_binding_refuses_sizes_past_31_bits():
+    c = host_cache()
+    q = torch.zeros(4, 8, 128)
+    lens = torch.zeros(4, dtype=torch.int32)
+    starts = torch.zeros(5, dtype=torch.int32)
+    for kw in (dict(max_kv=(1 << 32) + 16), dict(max_kv=1 << 31), dict(max_kv=-1), dict(window=1 << 32),
+               dict(window=-1), dict(max_q=(1 << 32) + 1, q_starts=starts), dict(max_q=-1, q_starts=starts)):
+        with pytest.raises(ValueError):
+            B.attend_workspace_bytes(c, q, lens, **kw)
+    # the default bound, what 2^27 pages of 16 tokens hold, does not fit
+    wide = torch.empty(1, 1 << 27, dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_kv"):
+        B.attend_workspace_bytes(c, q, lens[:1], block_table=wide)
+    B.attend_workspace_bytes(c, q, lens[:1], block_table=wide, max_kv=4096)

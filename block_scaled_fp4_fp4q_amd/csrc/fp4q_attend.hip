@@ -212,6 +212,18 @@ __device__ __forceinline__ void find_granules(const AttendArgs& a, int b, int he
 //     two keys of one value, the pair that the product wants.
 // Nothing passes through LDS in the loop, and the codes of the next 32 keys
 // are loaded while these are computed.
+//
+// Bound by HBM where there are many keys: 64 sequences of 4096 keys and 32 heads
+// of 128 values (1.2 GB of codes and scales) take 219 us with the joining, a
+// steady 6.0 TB/s.  Short of that by the fixed cost of a workgroup (about 8 us:
+// lengths, pages, the first loads, the waves' join), which is all that 131 keys
+// of 8 heads cost; 32 sequences of up to 8192 keys and 8 heads (170 MB, 28 us at
+// that rate) take 45 us with it and with the joining.  With two 16-row tiles of a wave and two parts of
+// the probabilities the issue of conversions and products joins in: 3 sequences
+// of 4 queries over up to 65521 keys, MXFP4, 39 us for 95 MB.
+// Measured and left: codes two tiles ahead (219 -> 245 us), two steps
+// unrolled (no change), a pair's workgroups spread by slices of the whole work
+// (half the engines idle, 345 us).
 
 template <bool MX, int D>
 struct Tile {
@@ -899,6 +911,19 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
 //     value = (D/32) (4 h + 8 a) + ...
 //   - 16-byte units of a row are exchanged by an XOR with the row, so that 16
 //     lanes that read or write one unit of 16 rows meet all 64 banks.
+//
+// Bound by issue: in a step the products take 37% of the cycles and the vector
+// ALU (exponentials, maxima, parts, expansion) 47%, on two waves per SIMD that
+// meet at the step's barrier.  8192 queries after themselves, 32 heads of
+// 128 over 8 KV heads, NVFP4, 562-595 us: 920-980 TFLOP/s of the pairs seen, where
+// a library's large f16 product reaches 1175.  Two times 509 queries after 16384
+// keys, MXFP4, 32 heads: 356 us with the joining (MXFP4's probabilities are two
+// products each).  Measured and left: waves 4-7 half a step behind 0-3 (a third
+// buffer of V and the logits kept over the barrier: 594 -> 630 us, and 361 ->
+// 413 with spilled registers), wave priorities around the products (no change),
+// workgroups of four waves (119 -> 109 us for 96 rows after 8192 keys, but 37 -> 45
+// for 128 rows of two short sequences), the causal end's tiles cut along the
+// keys (77 -> 107).
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -1399,8 +1424,9 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
 //
 // D/4 lanes hold four values each of a row; T groups of such lanes take every
 // T-th of its partial results.  One workgroup has as many rows as fit.  Reads
-// every partial result once: bound by that traffic where there are many rows,
-// by the latency of a few dependent loads where there are few.
+// every partial result once: bound by that traffic where there are many rows
+// (12 us for 32576 rows of 128 values of two partial results: 42 MB, 3.5 TB/s),
+// by the latency of a few dependent loads where there are few (5 us).
 template <bool MX, int D, int T>
 __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, const AttendPlan p, const uint32_t all_rows)
 {

@@ -5,6 +5,7 @@
 // fp4q_dequantize's on the row of a slot.  Both move every byte once: they are
 // bound by HBM where there are many tokens and by the launch where there are
 // few (the sweep's arithmetic, not the traffic, bounds a long swept write).
+// Times beside the kernels are of one call on an MI355X.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -183,9 +184,20 @@ __device__ __forceinline__ int sweep_pick(const float* v, float a, float S, int 
     return cb;
 }
 
-// one lane per block: load, rotate, choose the scale, encode, store at the slot
+// One lane per block: load, rotate, choose the scale, encode, store at the
+// slot; a block's 16 or 32 values stay in the lane's registers, so that neither
+// the transform nor the candidates move anything between lanes.  At 8 heads of
+// 128 bf16 values, K and V:
+//   AbsMax   bound by HBM: 262144 tokens 275 us, 1.4 GB, 5.0 TB/s;
+//   sweep    bound by the vector ALU, which every candidate asks for 8
+//            conversions each way: 8192 tokens 36 us, of which about 7 are the
+//            latency of a call; 262144 tokens 912 us, 590 Gelem/s;
+//   a step's 64 tokens take 7 us, whatever the rule: dependent loads (slot,
+//            scale, rows) and the launch.
+// The sweep's registers are held to six waves per SIMD (80, one value spilled;
+// with five waves and 94 registers 931 us for 262144 tokens).
 template <bool MX, int RULE, bool BF16, bool ROT>
-__global__ __launch_bounds__(kThreads) void kv_write(const KvWriteArgs a, const int blocks_shift,
+__global__ __launch_bounds__(kThreads, RULE == kRuleSweep && !MX ? 6 : 1) void kv_write(const KvWriteArgs a, const int blocks_shift,
                                                      const uint32_t items)
 {
     constexpr int B = MX ? 32 : 16;
@@ -279,7 +291,11 @@ __global__ __launch_bounds__(kThreads) void kv_write(const KvWriteArgs a, const 
 // Each lane decodes and stores 16 bytes of output (E = 8 bf16 or 4 binary32
 // values), so that a wave's stores are contiguous; the un-rotation's wide
 // stages cross the 2, 4 or 8 lanes that share a block, in the order and with
-// the roundings of the in-register transform.
+// the roundings of the in-register transform.  Bound by HBM: 65536 rows of 8
+// heads of 128 values, K and V, rotated, to bf16 move 345 MB in 67 us (5.1 TB/s)
+// from slots in order, in 75 us from slots in no order, where a row's 64 bytes
+// of codes and 8 of scales are parts of 128-byte lines.  (Plain instead of
+// nontemporal stores: 100 against 75 us.)
 template <bool MX, bool BF16, bool ROT>
 __global__ __launch_bounds__(kThreads) void kv_read(const KvReadArgs a, const int lane_shift,
                                                     const uint32_t items)
@@ -377,12 +393,17 @@ int log2_of(int n)
     return s;
 }
 
-// workgroups for `items` lanes: enough to cover them, and no more than keep
-// the chip full (the kernels stride over the rest)
-int groups_for(uint32_t items)
+// workgroups for `items` lanes: enough to cover them, at most `most` (the
+// kernels stride over the rest).  A write gets one block per lane up to 2^20
+// workgroups: 2^20 tokens of 8 heads of 128 values take 1075 us with AbsMax
+// and 3519 us swept, with at most 8192 workgroups 1289 and 3562.  A read is
+// faster with at most 8192: 65536 such rows to bf16 67 against 76 us.
+constexpr uint32_t kWriteGroups = 1u << 20, kReadGroups = 8192u;
+
+int groups_for(uint32_t items, uint32_t most)
 {
     const uint32_t g = (items + kThreads - 1) / kThreads;
-    return (int)(g < 8192u ? g : 8192u);
+    return (int)(g < most ? g : most);
 }
 
 // Tokens of one launch: item numbers, and a grid's stride past the last of
@@ -396,7 +417,7 @@ int64_t tokens_per_launch(int heads, int lanes_per_row)
 template <bool MX, int RULE, bool BF16>
 void launch_write(const KvWriteArgs& a, int shift, uint32_t items)
 {
-    const dim3 grid(groups_for(items), 2);
+    const dim3 grid(groups_for(items, kWriteGroups), 2);
     if (a.rotate)
         kv_write<MX, RULE, BF16, true><<<grid, kThreads, 0, a.stream>>>(a, shift, items);
     else
@@ -460,7 +481,7 @@ hipError_t launch_kv_read(const KvReadArgs& all)
         for (int side = 0; side < 2; ++side)
             a.y[side] = static_cast<char*>(all.y[side]) + t0 * a.kv.heads * a.kv.head_dim * (a.bf16 ? 2 : 4);
         const uint32_t items = (uint32_t)(a.tokens * a.kv.heads * lanes);
-        const dim3 grid(groups_for(items), 2);
+        const dim3 grid(groups_for(items, kReadGroups), 2);
         auto go = [&](auto mx, auto bf16) {
             if (a.rotate)
                 kv_read<mx.value, bf16.value, true><<<grid, kThreads, 0, a.stream>>>(a, shift, items);

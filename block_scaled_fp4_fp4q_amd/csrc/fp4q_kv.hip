@@ -184,22 +184,20 @@ __device__ __forceinline__ int sweep_pick(const float* v, float a, float S, int 
     return cb;
 }
 
-// One lane per block: load, rotate, choose the scale, encode, store at the
-// slot; a block's 16 or 32 values stay in the lane's registers, so that neither
-// the transform nor the candidates move anything between lanes.  At 8 heads of
-// 128 bf16 values, K and V:
-//   AbsMax   bound by HBM: 262144 tokens 275 us, 1.4 GB, 5.0 TB/s;
-//   sweep    bound by the vector ALU, which every candidate asks for 8
-//            conversions each way: 8192 tokens 36 us, of which about 7 are the
-//            latency of a call; 262144 tokens 912 us, 590 Gelem/s;
-//   a step's 64 tokens take 7 us, whatever the rule: dependent loads (slot,
-//            scale, rows) and the launch.
-// The sweep's registers are held to six waves per SIMD (80, one value spilled;
-// with five waves and 94 registers 931 us for 262144 tokens).
+// The searching rules, one lane per block: load, rotate, choose the scale,
+// encode, store at the slot; a block's 16 or 32 values stay in the lane's
+// registers, so that neither the transform nor the candidates move anything
+// between lanes.  The NVFP4 sweep is bound by the vector ALU, which every candidate
+// asks for 8 conversions each way: at 8 heads of 128 bf16 values, K and V, 8192
+// tokens take 36 us, of which about 7 are the latency of a call, 262144 tokens
+// 912 us, 590 Gelem/s; a step's 64 tokens take 7 us of dependent loads (slot,
+// scale, rows) and launch.  Its registers are held to six waves per SIMD (80,
+// one value spilled; with five waves and 94 registers 931 us for 262144 tokens).
 template <bool MX, int RULE, bool BF16, bool ROT>
 __global__ __launch_bounds__(kThreads, RULE == kRuleSweep && !MX ? 6 : 1) void kv_write(const KvWriteArgs a, const int blocks_shift,
                                                      const uint32_t items)
 {
+    static_assert(RULE == kRuleSweep || (RULE == kRuleFourSix && !MX), "the searching rules");
     constexpr int B = MX ? 32 : 16;
     __shared__ Pattern tab[RULE == kRuleSweep && !MX ? 128 : 1];
     const int side = blockIdx.y;
@@ -235,23 +233,20 @@ __global__ __launch_bounds__(kThreads, RULE == kRuleSweep && !MX ? 6 : 1) void k
         uint8_t* codes = a.kv.codes[side] + page * a.kv.c_page + head * a.kv.c_head + off * a.kv.c_token;
         uint8_t* scales = a.kv.scales[side] + page * a.kv.s_page + head * a.kv.s_head + off * a.kv.s_token;
         if constexpr (MX) {
-            int e = block_exponent(top);
-            if constexpr (RULE == kRuleSweep) {
-                const int e0 = e;
-                double best = 0.0;
-                int prev = 1000;
-                for (int k = a.lo; k <= a.hi; ++k) {
-                    int t = e0 + k;
-                    t = t < -127 ? -127 : (t > 127 ? 127 : t);
-                    if (t == prev)
-                        continue;
-                    const double E = exact_error<B>(v, exp2i(t), exp2i(-t));
-                    if (prev == 1000 || E < best) {
-                        best = E;
-                        e = t;
-                    }
-                    prev = t;
+            const int e0 = block_exponent(top);
+            int e = e0, prev = 1000;
+            double best = 0.0;
+            for (int k = a.lo; k <= a.hi; ++k) {
+                int t = e0 + k;
+                t = t < -127 ? -127 : (t > 127 ? 127 : t);
+                if (t == prev)
+                    continue;
+                const double E = exact_error<B>(v, exp2i(t), exp2i(-t));
+                if (prev == 1000 || E < best) {
+                    best = E;
+                    e = t;
                 }
+                prev = t;
             }
             const float r = exp2i(-e);
             const uint2 c0 = fp4_encode16(v, r), c1 = fp4_encode16(v + 16, r);
@@ -285,6 +280,99 @@ __global__ __launch_bounds__(kThreads, RULE == kRuleSweep && !MX ? 6 : 1) void k
             reinterpret_cast<uint2*>(codes)[b] = fp4_encode16(v, r);
             scales[b] = (uint8_t)sb;
         }
+    }
+}
+
+// AbsMax: each lane loads 32 bytes of a row (E = 16 bf16 or 8 binary32 values)
+// and writes their codes; the transform's wide stages and the maximum cross the
+// 1, 2 or 4 lanes that share a block, the sums in the order and with the
+// roundings of the in-register transform.  Bound by HBM: 65536 tokens of 8 heads
+// of 128 values, K and V, take 73 us from bf16 and 130 us from binary32 in either
+// format, 4.7 TB/s.  With a lane per block a wave's load instruction touches 16
+// bytes of each 64 or 128: 161 us for binary32 to NVFP4, 87 and 241 us for bf16
+// and binary32 to MXFP4.  With 16 bytes of a row in each lane its share of the
+// scale's arithmetic bounds: 97 to 177 us.
+template <bool MX, bool BF16, bool ROT>
+__global__ __launch_bounds__(kThreads) void kv_write_absmax(const KvWriteArgs a, const int lane_shift,
+                                                            const uint32_t items)
+{
+    constexpr int B = MX ? 32 : 16;
+    constexpr int E = BF16 ? 16 : 8;
+    const int side = blockIdx.y;
+    const float S = MX ? 1.0f : *a.kv.global[side];
+    const float S6 = 6.0f * S;
+    const uint32_t heads = (uint32_t)a.kv.heads;
+    const int64_t most = a.kv.num_pages * a.kv.page_size;
+    const uint32_t last = (uint32_t)(1 << lane_shift) - 1u;
+    for (uint32_t item = blockIdx.x * kThreads + threadIdx.x; item < items; item += gridDim.x * kThreads) {
+        const uint32_t part = item & last;
+        const uint32_t row = item >> lane_shift;
+        const uint32_t token = row / heads, head = row - token * heads;
+        const int64_t slot = a.slots[token];
+        if (slot < 0 || slot >= most)
+            continue; // with all lanes of its row
+        const char* x = static_cast<const char*>(a.x[side]) +
+                        (token * a.x_token[side] + head * a.x_head[side]) * (BF16 ? 2 : 4);
+        float v[E];
+        load_block<E, BF16>(x, part, v);
+        if constexpr (ROT) {
+#pragma unroll
+            for (int h = 1; h < E; h *= 2)
+#pragma unroll
+                for (int i = 0; i < E; i += 2 * h)
+#pragma unroll
+                    for (int j = i; j < i + h; ++j) {
+                        const float p = v[j], q = v[j + h];
+                        v[j] = p + q;
+                        v[j + h] = p - q;
+                    }
+#pragma unroll
+            for (int h = 1; h < B / E; h *= 2) {
+                const float sign = (part & h) ? -1.0f : 1.0f;
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    v[i] = __builtin_fmaf(sign, v[i], __shfl_xor(v[i], h, 64));
+            }
+            const float c = (B == 16) ? 0.25f : __uint_as_float(0x3E3504F3u); // fl32(1/sqrt(B))
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                v[i] = v[i] * c;
+        }
+        float top = block_absmax<E>(v);
+#pragma unroll
+        for (int h = 1; h < B / E; h *= 2)
+            top = __builtin_fmaxf(top, __shfl_xor(top, h, 64));
+        int64_t page, off;
+        slot_place(a.kv, slot, most, page, off);
+        uint8_t* codes = a.kv.codes[side] + page * a.kv.c_page + head * a.kv.c_head + off * a.kv.c_token;
+        uint8_t* scales = a.kv.scales[side] + page * a.kv.s_page + head * a.kv.s_head + off * a.kv.s_token;
+        float r;
+        uint32_t sb;
+        if constexpr (MX) {
+            const int e = block_exponent(top);
+            r = exp2i(-e);
+            sb = (uint32_t)(e + 127);
+        } else {
+            const int near = (int)e4m3_round(top / S6);
+            sb = top == 0.0f ? 0u : (uint32_t)(near < 1 ? 1 : near);
+            r = sb == 0u ? 1.0f : 1.0f / (e4m3_value(sb) * S); // an all-zero block keeps only its signs
+        }
+        uint32_t w[E / 8];
+#pragma unroll
+        for (int g = 0; g < E / 8; ++g) {
+            const float* y = v + 8 * g;
+            w[g] = fresh_word(y[0]); // every byte of it is written
+            w[g] = fp4_pack2<0>(w[g], y[0] * r, y[1] * r);
+            w[g] = fp4_pack2<1>(w[g], y[2] * r, y[3] * r);
+            w[g] = fp4_pack2<2>(w[g], y[4] * r, y[5] * r);
+            w[g] = fp4_pack2<3>(w[g], y[6] * r, y[7] * r);
+        }
+        if constexpr (BF16)
+            reinterpret_cast<uint2*>(codes)[part] = make_uint2(w[0], w[E / 8 - 1]);
+        else
+            reinterpret_cast<uint32_t*>(codes)[part] = w[0];
+        if (part % (B / E) == 0)
+            scales[part / (B / E)] = (uint8_t)sb;
     }
 }
 
@@ -424,20 +512,30 @@ void launch_write(const KvWriteArgs& a, int shift, uint32_t items)
         kv_write<MX, RULE, BF16, false><<<grid, kThreads, 0, a.stream>>>(a, shift, items);
 }
 
+template <bool MX, bool BF16>
+void launch_write_absmax(const KvWriteArgs& a, int shift, uint32_t items)
+{
+    const dim3 grid(groups_for(items, kWriteGroups), 2);
+    if (a.rotate)
+        kv_write_absmax<MX, BF16, true><<<grid, kThreads, 0, a.stream>>>(a, shift, items);
+    else
+        kv_write_absmax<MX, BF16, false><<<grid, kThreads, 0, a.stream>>>(a, shift, items);
+}
+
 template <bool BF16>
 void launch_write_rule(const KvWriteArgs& a, int shift, uint32_t items)
 {
-    if (a.kv.mx) {
-        if (a.rule == kRuleSweep)
-            launch_write<true, kRuleSweep, BF16>(a, shift, items);
+    if (a.rule == kRuleAbsMax) {
+        if (a.kv.mx)
+            launch_write_absmax<true, BF16>(a, shift, items);
         else
-            launch_write<true, kRuleAbsMax, BF16>(a, shift, items);
+            launch_write_absmax<false, BF16>(a, shift, items);
+    } else if (a.kv.mx) {
+        launch_write<true, kRuleSweep, BF16>(a, shift, items);
     } else if (a.rule == kRuleSweep) {
         launch_write<false, kRuleSweep, BF16>(a, shift, items);
-    } else if (a.rule == kRuleFourSix) {
-        launch_write<false, kRuleFourSix, BF16>(a, shift, items);
     } else {
-        launch_write<false, kRuleAbsMax, BF16>(a, shift, items);
+        launch_write<false, kRuleFourSix, BF16>(a, shift, items);
     }
 }
 
@@ -446,8 +544,8 @@ void launch_write_rule(const KvWriteArgs& a, int shift, uint32_t items)
 hipError_t launch_kv_write(const KvWriteArgs& all)
 {
     KvWriteArgs a = all;
-    const int blocks = a.kv.head_dim / (a.kv.mx ? 32 : 16);
-    const int64_t most = tokens_per_launch(a.kv.heads, blocks);
+    const int lanes = a.kv.head_dim / (a.rule == kRuleAbsMax ? (a.bf16 ? 16 : 8) : (a.kv.mx ? 32 : 16)); // per row
+    const int64_t most = tokens_per_launch(a.kv.heads, lanes);
     if (most == 0)
         return hipErrorInvalidValue;
     for (int64_t t0 = 0; t0 < all.tokens; t0 += most) {
@@ -455,11 +553,11 @@ hipError_t launch_kv_write(const KvWriteArgs& all)
         a.slots = all.slots + t0;
         for (int side = 0; side < 2; ++side)
             a.x[side] = static_cast<const char*>(all.x[side]) + t0 * all.x_token[side] * (a.bf16 ? 2 : 4);
-        const uint32_t items = (uint32_t)(a.tokens * a.kv.heads * blocks);
+        const uint32_t items = (uint32_t)(a.tokens * a.kv.heads * lanes);
         if (a.bf16)
-            launch_write_rule<true>(a, log2_of(blocks), items);
+            launch_write_rule<true>(a, log2_of(lanes), items);
         else
-            launch_write_rule<false>(a, log2_of(blocks), items);
+            launch_write_rule<false>(a, log2_of(lanes), items);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;

@@ -915,7 +915,7 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
 // Bound by issue: in a step the products take 37% of the cycles and the vector
 // ALU (exponentials, maxima, parts, expansion) 47%, on two waves per SIMD that
 // meet at the step's barrier.  8192 queries after themselves, 32 heads of
-// 128 over 8 KV heads, NVFP4, 562-595 us: 920-980 TFLOP/s of the pairs seen, where
+// 128 over 8 KV heads, NVFP4, 562-600 us: 915-980 TFLOP/s of the pairs seen, where
 // a library's large f16 product reaches 1175.  Two times 509 queries after 16384
 // keys, MXFP4, 32 heads: 356 us with the joining (MXFP4's probabilities are two
 // products each).  Measured and left: waves 4-7 half a step behind 0-3 (a third

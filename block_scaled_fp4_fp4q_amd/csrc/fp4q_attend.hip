@@ -186,12 +186,24 @@ __device__ __forceinline__ int64_t uniform64(int64_t x)
 }
 
 // The granules of keys [k0, k1) of sequence b (k0 a multiple of 16) into LDS,
-// by the whole workgroup.
+// by the whole workgroup.  Those wholly below key `first` are not looked up.
 template <int THREADS>
-__device__ __forceinline__ void find_granules(const AttendArgs& a, int b, int head, int k0, int k1, Granule* g)
+__device__ __forceinline__ void find_granules(const AttendArgs& a, int b, int head, int k0, int k1, int first, Granule* g)
 {
-    for (int j = threadIdx.x; j * 16 < k1 - k0; j += THREADS)
-        g[j] = granule_at(a, b, head, k0 + j * 16);
+    for (int j = threadIdx.x; j * 16 < k1 - k0; j += THREADS) {
+        const int key = k0 + j * 16;
+        g[j] = key + 16 <= first ? Granule{0, 0} : granule_at(a, b, head, key);
+    }
+}
+
+// A V row below the first key that is seen meets probabilities of zero, but its
+// scale may be NaN: its scales are read from past every buffer's end, as zeros.
+// Such keys stand only in the first tile of a workgroup (EDGE); K's need no
+// care, the mask replaces their logits.
+template <bool EDGE>
+__device__ __forceinline__ int seen_offset(int offset, int key, int first)
+{
+    return EDGE && key < first ? 0x7FFFFFFF : offset;
 }
 
 // ---- few queries: one wave per 16 rows and 32 keys ------------------------------
@@ -256,11 +268,12 @@ __device__ __forceinline__ Lane lane_offsets(const AttendArgs& a, int n, int g)
     return o;
 }
 
-// the codes and scales of keys [key, key + 32), of which those from `end` on
-// are not read; granule 0 is that of key k0
-template <bool MX, int D>
-__device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g, int k0, int key, int end,
-                                          const Lane& o, Tile<MX, D>& t)
+// the codes and scales of keys [key, key + 32), of which those from `end` on,
+// and with EDGE V's scales below `first`, are not read; granule 0 is that of key
+// k0
+template <bool MX, int D, bool EDGE>
+__device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g, int k0, int key, int first, int end,
+                                          int lane16, const Lane& o, Tile<MX, D>& t)
 {
     constexpr int B = MX ? 32 : 16;
     constexpr int QS = D / 4 >= B ? D / 4 / B : 1; // scales of a quarter row
@@ -268,6 +281,8 @@ __device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g,
     for (int h = 0; h < 2; ++h) {
         int rows = end - key - 16 * h;
         rows = rows < 0 ? 0 : (rows > 16 ? 16 : rows);
+        if (EDGE && key + 16 * h + 16 <= first)
+            rows = 0;
         const Granule at = g[rows > 0 ? (key - k0) / 16 + h : 0];
         const int64_t co = uniform64(at.codes), so = uniform64(at.scales);
         const bool lost = rows > 0 && co < 0;
@@ -309,7 +324,8 @@ __device__ __forceinline__ void load_tile(const AttendArgs& a, const Granule* g,
                 t.v[h][i][0] = w.x;
                 t.v[h][i][Tile<MX, D>::VW - 1] = w.y;
             }
-            t.vs[h][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(vs, o.vs[i], 0, 0);
+            t.vs[h][i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+                vs, seen_offset<EDGE>(o.vs[i], key + 16 * h + 4 * i + lane16, first), 0, 0);
         }
     }
 }
@@ -666,13 +682,14 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
         }
     }
     const Lane at = lane_offsets<MX, D>(a, n, g);
+    const int first = first_seen(a, e, r0);
     const int step = turns * kTileKeys;
     Tile<MX, D> now, next;
     int s0 = k0, s1 = k1 - k0 < kSegment ? k1 : k0 + kSegment;
-    find_granules<kThreads>(a, b, head, s0, s1, granule);
+    find_granules<kThreads>(a, b, head, s0, s1, first, granule);
     __syncthreads();
     int key = s0 + turn * kTileKeys;
-    load_tile<MX, D>(a, granule, s0, key, s1, at, now);
+    load_tile<MX, D, true>(a, granule, s0, key, first, s1, g, at, now);
 
     // the quarters, rotated, as parts
     u32x4 q[QT][NQ][KW];
@@ -747,7 +764,7 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
 
     for (;;) {
     for (; key < s1; key += step) {
-        load_tile<MX, D>(a, granule, s0, key + step, s1, at, next); // past the end: nothing
+        load_tile<MX, D, false>(a, granule, s0, key + step, 0, s1, g, at, next); // past the end: nothing
         f32x4 s[QT][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -827,10 +844,10 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
     s0 = s1; // the places of the next keys
     s1 = k1 - s0 < kSegment ? k1 : s0 + kSegment;
     __syncthreads();
-    find_granules<kThreads>(a, b, head, s0, s1, granule);
+    find_granules<kThreads>(a, b, head, s0, s1, 0, granule);
     __syncthreads();
     key = s0 + turn * kTileKeys;
-    load_tile<MX, D>(a, granule, s0, key, s1, at, now);
+    load_tile<MX, D, false>(a, granule, s0, key, 0, s1, g, at, now);
     }
 
     // join the waves that share rows, through LDS: D/8 lanes take a row
@@ -963,11 +980,15 @@ struct ManyBuffers {
     bool lost;
 };
 
-// resources over the rows of 16 keys from `key` that lie before `end`
-template <int B, int D>
-__device__ __forceinline__ ManyBuffers many_buffers(const AttendArgs& a, const Granule* g, int side, int key, int end)
+// resources over the rows of 16 keys from `key` that lie before `end`; none
+// where all of them lie below `first`
+template <int B, int D, bool EDGE>
+__device__ __forceinline__ ManyBuffers many_buffers(const AttendArgs& a, const Granule* g, int side, int key, int first,
+                                                    int end)
 {
     int rows = end - key;
+    if (EDGE && key + 16 <= first)
+        rows = 0;
     rows = __builtin_amdgcn_readfirstlane(rows < 0 ? 0 : (rows > 16 ? 16 : rows));
     const int64_t co = rows > 0 ? uniform64(g->codes) : 0, so = rows > 0 ? uniform64(g->scales) : 0;
     const bool lost = co < 0;
@@ -978,12 +999,13 @@ __device__ __forceinline__ ManyBuffers many_buffers(const AttendArgs& a, const G
     return ManyBuffers{buffer_of(a.kv.codes[side] + co, cb), buffer_of(a.kv.scales[side] + so, sb), lost};
 }
 
-template <bool MX, int D>
-__device__ __forceinline__ void stage_k(const AttendArgs& a, const Granule* g, int key, int end, int lane, StageK<D>& t)
+template <bool MX, int D, bool EDGE>
+__device__ __forceinline__ void stage_k(const AttendArgs& a, const Granule* g, int key, int first, int end, int lane,
+                                        StageK<D>& t)
 {
     constexpr int B = MX ? 32 : 16;
     constexpr int QS = D / 4 >= B ? D / 4 / B : 1;
-    const ManyBuffers m = many_buffers<B, D>(a, g, 0, key, end);
+    const ManyBuffers m = many_buffers<B, D, EDGE>(a, g, 0, key, first, end);
     const int row = lane >> 2, quarter = lane & 3;
     const int o = row * (int)a.kv.c_token + quarter * (D / 8);
     const int os = row * (int)a.kv.s_token + (quarter * (D / 4)) / B;
@@ -1010,11 +1032,12 @@ __device__ __forceinline__ void stage_k(const AttendArgs& a, const Granule* g, i
     t.lost = m.lost ? kNanScales : 0u;
 }
 
-template <bool MX, int D>
-__device__ __forceinline__ void stage_v(const AttendArgs& a, const Granule* g, int key, int end, int lane, StageV<D>& t)
+template <bool MX, int D, bool EDGE>
+__device__ __forceinline__ void stage_v(const AttendArgs& a, const Granule* g, int key, int first, int end, int lane,
+                                        StageV<D>& t)
 {
     constexpr int B = MX ? 32 : 16;
-    const ManyBuffers m = many_buffers<B, D>(a, g, 1, key, end);
+    const ManyBuffers m = many_buffers<B, D, EDGE>(a, g, 1, key, first, end);
     const int unit = lane >> 5, i = lane & 31;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -1026,7 +1049,8 @@ __device__ __forceinline__ void stage_v(const AttendArgs& a, const Granule* g, i
             t.w[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(m.codes, o, 0, 0);
         else
             t.w[j] = __builtin_amdgcn_raw_buffer_load_b32(m.codes, o, 0, 0);
-        t.s[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(m.scales, row * (int)a.kv.s_token + (i * (D / 32)) / B, 0, 0);
+        const int os = seen_offset<EDGE>(row * (int)a.kv.s_token + (i * (D / 32)) / B, key + row, first);
+        t.s[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(m.scales, os, 0, 0);
     }
 }
 
@@ -1169,23 +1193,26 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     StageK<D> sk;
     StageV<D> sv;
     int s0 = k0, s1 = k1 - k0 < kManySegment ? k1 : k0 + kManySegment;
-    auto load = [&](int key) {
+    const int first = first_seen(a, e, r0);
+    auto load = [&](int key, auto edge) {
         const int mine = key + 16 * w;
         const Granule* g = granule + (mine < s1 ? (mine - s0) / 16 : 0);
         if (does_k)
-            stage_k<MX, D>(a, g, mine, s1, lane, sk);
+            stage_k<MX, D, edge.value>(a, g, mine, first, s1, lane, sk);
         if (does_v)
-            stage_v<MX, D>(a, g, mine, s1, lane, sv);
+            stage_v<MX, D, edge.value>(a, g, mine, first, s1, lane, sv);
     };
+    constexpr std::true_type at_first{};
+    constexpr std::false_type later{};
     auto expand = [&](int to) {
         if (does_k)
             expand_k<MX, D>(sk, w, lane, kbuf[to]);
         if (does_v)
             expand_v<MX, D>(sv, w, lane, vbuf[to]);
     };
-    find_granules<64 * WAVES>(a, b, head, s0, s1, granule);
+    find_granules<64 * WAVES>(a, b, head, s0, s1, first, granule);
     __syncthreads();
-    load(s0);
+    load(s0, at_first);
 
     u32x4 q[NQ][C];
     float factor; // of the row's logits, to log2 units; positive
@@ -1256,14 +1283,14 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
     while (k0 < k1) {
         expand(0);
         if (s0 + kManyKeys < s1)
-            load(s0 + kManyKeys);
+            load(s0 + kManyKeys, later);
         __syncthreads();
         int at = 0;
         for (int key = s0; key < s1; key += kManyKeys, at ^= 1) {
             if (key + kManyKeys < s1) {
                 expand(at ^ 1);
                 if (key + 2 * kManyKeys < s1)
-                    load(key + 2 * kManyKeys);
+                    load(key + 2 * kManyKeys, later);
             }
             if (key < wave_hi && key + kManyKeys > wave_lo) {
                 f32x16 s[2];
@@ -1343,9 +1370,9 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
             break;
         s0 = s1; // the places of the next keys
         s1 = k1 - s0 < kManySegment ? k1 : s0 + kManySegment;
-        find_granules<64 * WAVES>(a, b, head, s0, s1, granule);
+        find_granules<64 * WAVES>(a, b, head, s0, s1, 0, granule);
         __syncthreads();
-        load(s0);
+        load(s0, later);
     }
     l += __shfl_xor(l, 32, 64);
     if (e.bad)

@@ -86,6 +86,16 @@ FP4Q_INDEX void tile_keys(const AttendArgs& a, const Extent& e, int r0, int r1, 
     lo &= ~(kTileKeys - 1);
 }
 
+// the first key that a row of a tile sees, the lowest row being r0: those from
+// the 32-key boundary up to it are computed with the tile's keys, but no query
+// sees them, and what they hold may be anything
+FP4Q_INDEX int first_seen(const AttendArgs& a, const Extent& e, int r0)
+{
+    int lo, hi;
+    seen_by(a, e, r0 / a.group, lo, hi);
+    return lo;
+}
+
 // the key chunks of a row tile that are computed; the first one always is,
 // and says that there is nothing where there is nothing
 FP4Q_INDEX int chunks_of(const AttendPlan& p, int lo, int hi)

@@ -6,6 +6,7 @@ arithmetic happens in the library's HIP kernels.  There is no fallback: if the
 library is missing, or a call is rejected, this module raises.
 """
 import ctypes as C
+import operator
 import os
 
 import torch
@@ -598,8 +599,16 @@ def kv_read(cache, slots, dtype=torch.float32, stream=None):
     return k, v
 
 
+def _numbers(max_kv, max_q, causal, window, scale):
+    """The numbers of an attention call as Python's own: what counts is an
+    argument's value now (a 0-dimensional tensor may change in place)."""
+    return (None if max_kv is None else operator.index(max_kv), None if max_q is None else operator.index(max_q),
+            int(causal), operator.index(window), None if scale is None else C.c_float(scale).value)
+
+
 def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, scale, out):
-    """The call's fp4q_attention without its pointers, from checked tensors."""
+    """The call's fp4q_attention without its pointers, from checked tensors and
+    _numbers."""
     dev = cache.device
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise TypeError("q must be a torch tensor [total_q, q_heads, head_dim]")
@@ -639,7 +648,7 @@ def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, 
     if scale is None:
         scale = cache.head_dim ** -0.5
     return fp4q_attention(None, qs[0], qs[1], None, os[0], os[1], None, None, None, None, stride,
-                          total, entries, batch, max_q, max_kv, heads, _dtype_code(q), int(causal),
+                          total, entries, batch, max_q, max_kv, heads, _dtype_code(q), causal,
                           window, scale, 0)
 
 
@@ -666,6 +675,7 @@ def attend_workspace_bytes(cache, q, kv_lens, max_kv=None, block_table=None, q_s
                            max_q=None, causal=True, window=0):
     """Bytes that `attend` of these arguments needs as its workspace (only
     their shapes and types matter)."""
+    max_kv, max_q, causal, window, _ = _numbers(max_kv, max_q, causal, window, None)
     call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, None, q)
     _point(call, q, q, None, kv_lens, block_table, q_starts)
     return _workspace_bytes(cache, call)
@@ -703,6 +713,7 @@ def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
+    max_kv, max_q, causal, window, scale = _numbers(max_kv, max_q, causal, window, scale)
     # calls that differ in addresses alone share their checks
     key = (_same(q), _same(kv_lens), _same(block_table), _same(q_starts), _same(out), max_kv, max_q,
            causal, window, scale)

@@ -136,6 +136,23 @@ __device__ __forceinline__ float column_sum(float x)
     return x + __shfl_xor(x, 32, 64);
 }
 
+// What the queries are multiplied by so that the largest product is the largest
+// logit: the sign of scale S.  A global scale that is not finite makes them NaN
+// (in the factor of the logits it would meet the infinities of masked keys).
+__device__ __forceinline__ float query_sign(float scale, float S)
+{
+    if (!(__builtin_fabsf(S) < __builtin_huge_valf()))
+        return __builtin_nanf("");
+    return (scale < 0.0f) != (S < 0.0f) ? -1.0f : 1.0f;
+}
+
+// the rest of scale S, in log2 units: finite, not negative
+__device__ __forceinline__ float logit_factor(float scale, float S)
+{
+    S = __builtin_fabsf(S);
+    return __builtin_fabsf(scale) * kLog2e * (S < __builtin_huge_valf() ? S : 1.0f);
+}
+
 // Orthonormal Hadamard of the blocks of B values of a row of D whose quarter g
 // (D/4 values) each of the lanes n + 16 g holds.
 template <int B, int D>
@@ -712,15 +729,13 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
         }
         if (a.rotate)
             rotate_quarter<B, D>(v, g);
-        // a negative factor goes to the query, so that the largest product is
-        // the largest logit
-        const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+        const float S = MX ? 1.0f : *a.kv.global[0];
+        const float sign = query_sign(a.scale, S);
 #pragma unroll
         for (int j = 0; j < N; ++j)
             v[j] *= sign;
-        factor[t] = a.scale * sign * kLog2e;
+        factor[t] = logit_factor(a.scale, S);
         if constexpr (!MX) {
-            factor[t] *= *a.kv.global[0];
             float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -1231,16 +1246,16 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
                 v[8 * c + 6] = bf16_lo(x.w); v[8 * c + 7] = bf16_hi(x.w);
             }
         }
-        const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+        const float S = MX ? 1.0f : *a.kv.global[0];
+        const float sign = query_sign(a.scale, S);
         const float turn = a.rotate ? (B == 16 ? 0.25f : __uint_as_float(0x3E3504F3u)) * sign : sign;
         if (a.rotate)
             rotate_half<B, D / 2>(v, h);
 #pragma unroll
         for (int j = 0; j < D / 2; ++j)
             v[j] *= turn;
-        factor = a.scale * sign * kLog2e;
+        factor = logit_factor(a.scale, S);
         if constexpr (!MX) {
-            factor *= *a.kv.global[0];
             float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 2; ++j)

@@ -344,7 +344,9 @@ fp4q_status fp4q_kv_read(const fp4q_spec* spec, const fp4q_kv_cache* cache, cons
  *            less (query i of n sees keys 0 .. kv_len - n + i).  0: all keys.
  *   window   with causal: only the last `window` of those keys; 0: all.
  *   scale    the factor of the logits, finite.
- * A query that sees no key gives zeros and lse = -inf.  A sequence whose
+ * A query that sees no key gives zeros and lse = -inf.  Where K's global scale is
+ * not finite, a query that sees a key gives NaN (V's acts as in
+ * fp4q_dequantize).  A sequence whose
  * kv_len is negative or above max_kv, or above what its pages hold, or that
  * reads through a page number out of range, gives NaN in the rows concerned.
  * Logits, softmax statistics and sums are binary32.  Dequantized values enter

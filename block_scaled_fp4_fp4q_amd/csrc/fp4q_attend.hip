@@ -146,11 +146,17 @@ __device__ __forceinline__ float query_sign(float scale, float S)
     return (scale < 0.0f) != (S < 0.0f) ? -1.0f : 1.0f;
 }
 
-// the rest of scale S, in log2 units: finite, not negative
-__device__ __forceinline__ float logit_factor(float scale, float S)
+// The rest of scale S 2^-up, in log2 units: finite and not zero, since it meets
+// infinities and zeros.  Exponents are added apart: scale S may be far below
+// binary32 where large queries (up < 0) bring the logits back.
+__device__ __forceinline__ float logit_factor(float scale, float S, int up)
 {
+    const float c = __builtin_fabsf(scale) * kLog2e;
     S = __builtin_fabsf(S);
-    return __builtin_fabsf(scale) * kLog2e * (S < __builtin_huge_valf() ? S : 1.0f);
+    S = S < __builtin_huge_valf() ? S : 1.0f;
+    const float f = __builtin_ldexpf(__builtin_amdgcn_frexp_mantf(c) * __builtin_amdgcn_frexp_mantf(S),
+                                     __builtin_amdgcn_frexp_expf(c) + __builtin_amdgcn_frexp_expf(S) - up);
+    return __builtin_fminf(__builtin_fmaxf(f, 0x1p-126f), 0x1.fffffep127f);
 }
 
 // Orthonormal Hadamard of the blocks of B values of a row of D whose quarter g
@@ -734,7 +740,7 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
 #pragma unroll
         for (int j = 0; j < N; ++j)
             v[j] *= sign;
-        factor[t] = logit_factor(a.scale, S);
+        int up = 0;
         if constexpr (!MX) {
             float top = 0.0f;
 #pragma unroll
@@ -742,14 +748,12 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
                 top = __builtin_fmaxf(top, __builtin_fabsf(v[j]));
             top = column_max(top);
             // a power of two to [2^14, 2^15); zero and non-finite rows stay
-            const int up = (top > 0.0f && top < __builtin_huge_valf())
-                               ? 141 - (int)(__float_as_uint(top) >> 23) : 0;
+            up = (top > 0.0f && top < __builtin_huge_valf()) ? 141 - (int)(__float_as_uint(top) >> 23) : 0;
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 v[j] = __builtin_ldexpf(v[j], up);
-            factor[t] = __builtin_ldexpf(factor[t], -up);
         }
-        factor[t] = __builtin_fmaxf(factor[t], 0x1p-126f); // not zero: it meets infinities
+        factor[t] = logit_factor(a.scale, S, up);
 #pragma unroll
         for (int s = 0; s < NQ; ++s)
 #pragma unroll
@@ -1254,21 +1258,19 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
 #pragma unroll
         for (int j = 0; j < D / 2; ++j)
             v[j] *= turn;
-        factor = logit_factor(a.scale, S);
+        int up = 0;
         if constexpr (!MX) {
             float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 2; ++j)
                 top = __builtin_fmaxf(top, __builtin_fabsf(v[j]));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-            const int up = (top > 0.0f && top < __builtin_huge_valf())
-                               ? 141 - (int)(__float_as_uint(top) >> 23) : 0;
+            up = (top > 0.0f && top < __builtin_huge_valf()) ? 141 - (int)(__float_as_uint(top) >> 23) : 0;
 #pragma unroll
             for (int j = 0; j < D / 2; ++j)
                 v[j] = __builtin_ldexpf(v[j], up);
-            factor = __builtin_ldexpf(factor, -up);
         }
-        factor = __builtin_fmaxf(factor, 0x1p-126f);
+        factor = logit_factor(a.scale, S, up);
 #pragma unroll
         for (int s = 0; s < NQ; ++s)
 #pragma unroll

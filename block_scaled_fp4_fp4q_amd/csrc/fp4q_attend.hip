@@ -435,6 +435,22 @@ __device__ __forceinline__ Partial partials_of(const AttendArgs& a, const Attend
     return r;
 }
 
+// What turns a row's sums into its result: the sums times `by`, times `rest`.
+// V's global scale over the sum of probabilities (up to 2^15 for each key) may
+// fall below binary32's normal range though the result does not, so a small
+// scale is applied times 2^60 and the power of two taken back at the end (exact,
+// and 1 for other scales).
+struct OutFactor {
+    float by, rest;
+};
+
+__device__ __forceinline__ OutFactor out_factor(float S, float l)
+{
+    const bool small = __builtin_fabsf(S) < 0x1p-60f;
+    // nothing seen: zeros
+    return OutFactor{l == 0.0f ? 0.0f : S * (small ? 0x1p60f : 1.0f) / l, small ? 0x1p-60f : 1.0f};
+}
+
 // One query row's result from its sums: eight of the D values (those from
 // 8 j on) in each of D/8 lanes, which are lanes of one wave in order.
 template <bool MX, int D, bool F32>
@@ -442,10 +458,10 @@ __device__ __forceinline__ void finish_row(const AttendArgs& a, const Extent& e,
                                            float* o, float m, float l)
 {
     constexpr int B = MX ? 32 : 16;
-    const float inv = l == 0.0f ? 0.0f : (MX ? 1.0f : *a.kv.global[1]) / l; // nothing seen: zeros
+    const OutFactor f = out_factor(MX ? 1.0f : *a.kv.global[1], l);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        o[k] *= inv;
+        o[k] *= f.by;
     if (a.rotate) {
 #pragma unroll
         for (int s = 1; s < 8; s *= 2)
@@ -468,6 +484,11 @@ __device__ __forceinline__ void finish_row(const AttendArgs& a, const Extent& e,
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             o[k] *= c;
+    }
+    if constexpr (!MX) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            o[k] *= f.rest;
     }
     const int i = r / a.group;
     const int64_t row = e.q0 + i;
@@ -1398,8 +1419,8 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
 
     // the lane's values: D/8 contiguous ones for each a, in order
     if (p.chunks == 1) {
-        const float inv = l == 0.0f ? 0.0f : (MX ? 1.0f : *a.kv.global[1]) / l;
-        const float turn = inv * (a.rotate ? (B == 16 ? 0.25f : __uint_as_float(0x3E3504F3u)) : 1.0f);
+        const OutFactor f = out_factor(MX ? 1.0f : *a.kv.global[1], l);
+        const float turn = f.by * (a.rotate ? (B == 16 ? 0.25f : __uint_as_float(0x3E3504F3u)) : 1.0f);
         const int i = live ? r / a.group : 0, j = r - i * a.group;
         const int64_t row = e.q0 + i;
         const int qh = head * a.group + j;
@@ -1433,6 +1454,11 @@ __global__ __launch_bounds__(64 * WAVES) void attend_many(const AttendArgs a, co
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const int at = T * (4 * h + 8 * x);
+            if constexpr (!MX) {
+#pragma unroll
+                for (int k = 0; k < 4 * T; ++k)
+                    y[x][k] *= f.rest;
+            }
             if (a.bf16) {
                 uint16_t* to = static_cast<uint16_t*>(a.out) + row * a.o_row + qh * a.o_head + at;
 #pragma unroll
@@ -1546,8 +1572,8 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
             o += sum[t * L + j] * f;
         }
     }
-    const float inv = l == 0.0f ? 0.0f : (MX ? 1.0f : *a.kv.global[1]) / l;
-    o *= inv;
+    const OutFactor f = out_factor(MX ? 1.0f : *a.kv.global[1], l);
+    o *= f.by;
     if (a.rotate) {
         const float p0 = o.x + o.y, p1 = o.x - o.y, p2 = o.z + o.w, p3 = o.z - o.w;
         o = f32x4{p0 + p2, p1 + p3, p0 - p2, p1 - p3};
@@ -1560,6 +1586,8 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a, cons
         }
         o *= (B == 16) ? 0.25f : __uint_as_float(0x3E3504F3u);
     }
+    if constexpr (!MX)
+        o *= f.rest;
     const int i = r / a.group;
     const int qh = head * a.group + (r - i * a.group);
     const int64_t row = e.q0 + i;

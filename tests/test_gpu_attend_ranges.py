@@ -64,6 +64,23 @@ def test_ends_of_the_scale_range(dtype, rotate, k_up, v_up, q_up):
         run(f, q, q_lens, f"{q_lens} {lens}")
 
 
+@pytest.mark.parametrize("q_lens,lens", [([1], [256]), ([1], [9216]), ([96], [500]), ([96], [9216])])
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_small_values_under_large_sums(dtype, rotate, q_lens, lens):
+    """V's scale at the low end, and logits that stay 5.9 (in log2 units) above the first ones of every 256 keys, so
+    that the sum of probabilities reaches thousands of times the largest that a running maximum would leave."""
+    rng = np.random.default_rng(54)
+    f = Filled(rng, "nvfp4", 64, 1, 64, lens, rotate)
+    times(f, 1, -111)
+    key = np.arange(max(lens))
+    first_values_only(f, np.where(key % 256 < 128, 0, 7).astype(np.uint8), np.full(len(key), 0x38, np.uint8))
+    q = np.zeros((sum(q_lens), 1, 64), np.float32)
+    q[:, :, :16 if rotate else 1] = (5.9 / 1.4427 / (6 * f.S[0] / 8)) / (4 if rotate else 1)  # rotated: element 0
+    q = torch.from_numpy(q)
+    run(f, q.to(torch.bfloat16) if dtype == "bf16" else q, q_lens, f"{q_lens} {lens}")
+
+
 @pytest.mark.parametrize("q_lens,lens", [([1], [256]), ([96], [500])])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_small_keys_large_queries_small_scale(dtype, q_lens, lens):

@@ -54,7 +54,8 @@ fp4q_status check_cache(const fp4q_spec* s, const fp4q_kv_cache* c, fp4q::KvView
         return FP4Q_E_SHAPE;
     // a byte offset into a cache fits in 63 bits
     const int64_t far = (c->code_page > c->scale_page ? c->code_page : c->scale_page);
-    if (far != 0 && c->num_pages > (INT64_MAX >> 2) / far)
+    const int64_t wide = (c->code_head > c->scale_head ? c->code_head : c->scale_head);
+    if ((far != 0 && c->num_pages > (INT64_MAX >> 2) / far) || (wide != 0 && c->kv_heads > (INT64_MAX >> 2) / wide))
         return FP4Q_E_SHAPE;
     if (c->num_pages > (INT64_MAX >> 2) / c->page_size)
         return FP4Q_E_SHAPE;
@@ -123,7 +124,8 @@ fp4q_status check_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
         !stride_ok(c->out_row_stride) || !stride_ok(c->out_head_stride))
         return FP4Q_E_SHAPE;
     const int64_t most = c->q_row_stride > c->out_row_stride ? c->q_row_stride : c->out_row_stride;
-    if (most != 0 && c->total_q > (INT64_MAX >> 4) / most)
+    const int64_t wide = c->q_head_stride > c->out_head_stride ? c->q_head_stride : c->out_head_stride;
+    if ((most != 0 && c->total_q > (INT64_MAX >> 4) / most) || (wide != 0 && c->q_heads > (INT64_MAX >> 4) / wide))
         return FP4Q_E_SHAPE;
     if (c->total_q > (INT64_MAX >> 4) / c->q_heads)
         return FP4Q_E_SHAPE;
@@ -206,7 +208,8 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
         !stride_ok(v_token_stride) || !stride_ok(v_head_stride))
         return FP4Q_E_SHAPE;
     const int64_t most = k_token_stride > v_token_stride ? k_token_stride : v_token_stride;
-    if ((most != 0 && tokens > (INT64_MAX >> 4) / most) ||
+    const int64_t wide = k_head_stride > v_head_stride ? k_head_stride : v_head_stride;
+    if ((most != 0 && tokens > (INT64_MAX >> 4) / most) || (wide != 0 && cache->kv_heads > (INT64_MAX >> 4) / wide) ||
         tokens > (INT64_MAX >> 4) / ((int64_t)cache->kv_heads * cache->head_dim))
         return FP4Q_E_SHAPE;
     if (tokens != 0 && (!k || !v || !slots))

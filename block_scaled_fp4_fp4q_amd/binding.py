@@ -441,7 +441,7 @@ class KvCache:
     one global scale float32 [1] each (None for MXFP4).  The tensors are the
     caller's; this handle checks them once, keeps references to them and passes
     their addresses on.  A contiguous cache [B, H, T, D] is one of B pages of T
-    tokens.  `scale_rule`, `window` and `rotate` say how rows are written (and
+    tokens.  Expanded dimensions can be read, not written.  `scale_rule`, `window` and `rotate` say how rows are written (and
     `rotate` how they are read)."""
 
     def __init__(self, k_codes, k_scales, k_global, v_codes, v_scales, v_global,
@@ -677,6 +677,7 @@ def attend_workspace_bytes(cache, q, kv_lens, max_kv=None, block_table=None, q_s
     their shapes and types matter)."""
     max_kv, max_q, causal, window, _ = _numbers(max_kv, max_q, causal, window, None)
     call = _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, None, q)
+    call.out_row_stride, call.out_head_stride = q.shape[1] * q.shape[2], q.shape[2]  # of any output
     _point(call, q, q, None, kv_lens, block_table, q_starts)
     return _workspace_bytes(cache, call)
 
@@ -699,6 +700,7 @@ def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_
                  before it one less; False: every query sees all.
     window       with causal, only the last `window` of those (0: all).
     scale        of the logits (default head_dim ** -0.5).
+    out          like q, of any strides without expanded dimensions.
     A query without keys gives zeros and lse -inf.  Rows of no sequence are not
     written: they stay what they are in `out`, unspecified where it is
     allocated here.  A given workspace (uint8, attend_workspace_bytes) must

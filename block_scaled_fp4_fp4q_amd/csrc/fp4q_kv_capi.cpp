@@ -104,6 +104,34 @@ bool rows_aligned(const void* p, int64_t stride1, int64_t stride2, int32_t dtype
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMostStride; }
 
+// Whether rows of `row` units, counts[i] of them strides[i] apart in each of N
+// dimensions, share no unit: in order of their strides, each dimension steps
+// past all that the ones before it cover (every view of a tensor does whose
+// elements are its own).  Counts and strides are such that extents fit 63 bits.
+template <int N>
+bool rows_apart(const int64_t (&counts)[N], const int64_t (&strides)[N], int64_t row)
+{
+    int64_t covered = row;
+    bool used[N] = {};
+    for (int turn = 0; turn < N; ++turn) {
+        int next = -1;
+        for (int i = 0; i < N; ++i) {
+            if (counts[i] == 0)
+                return true;
+            if (!used[i] && (next < 0 || strides[i] < strides[next] ||
+                             (strides[i] == strides[next] && counts[i] < counts[next])))
+                next = i;
+        }
+        used[next] = true;
+        if (counts[next] == 1)
+            continue;
+        if (strides[next] < covered)
+            return false;
+        covered += (counts[next] - 1) * strides[next];
+    }
+    return true;
+}
+
 fp4q_status check_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
                          const fp4q_attention* c, fp4q::AttendArgs& a)
 {
@@ -148,6 +176,8 @@ fp4q_status check_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
         !aligned(c->lse, 4) || !aligned(c->q_starts, 4) || !aligned(c->kv_lens, 4) ||
         !aligned(c->block_table, 4))
         return FP4Q_E_ALIGN;
+    if (!empty && !rows_apart<2>({c->total_q, c->q_heads}, {c->out_row_stride, c->out_head_stride}, cache->head_dim))
+        return FP4Q_E_SHAPE;
     a.rotate = spec->rotate;
     a.bf16 = c->dtype == FP4Q_BF16;
     a.causal = c->causal != 0;
@@ -217,6 +247,13 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
     if (!rows_aligned(k, k_token_stride, k_head_stride, dtype) ||
         !rows_aligned(v, v_token_stride, v_head_stride, dtype) || !aligned(slots, 8))
         return FP4Q_E_ALIGN;
+    // rows that share bytes would be written at once
+    const int64_t counts[3] = {cache->num_pages, cache->kv_heads, cache->page_size};
+    if (!rows_apart<3>(counts, {cache->code_page, cache->code_head, cache->code_token}, cache->head_dim / 2) ||
+        !rows_apart<3>(counts, {cache->scale_page, cache->scale_head, cache->scale_token},
+                       cache->head_dim / spec->block) ||
+        (cache->num_pages != 0 && (cache->k_codes == cache->v_codes || cache->k_scales == cache->v_scales)))
+        return FP4Q_E_SHAPE;
     if (tokens == 0)
         return FP4Q_OK;
     a.rule = spec->scale_rule;

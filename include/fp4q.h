@@ -299,6 +299,10 @@ typedef struct {
  *   k, v     [tokens, kv_heads, head_dim] (dtype FP4Q_F32 or FP4Q_BF16), the
  *            head_dim values contiguous, token and head strides in elements;
  *            bases and strides 16-byte aligned.
+ *   cache    one whose rows share no byte (FP4Q_E_SHAPE otherwise; the other
+ *            calls also take caches with strides of 0, or K's array as V's):
+ *            in order of its strides, each dimension steps past all that the
+ *            ones before it cover.
  *   slots    int64 [tokens] on the device; a token whose slot is negative or
  *            not below num_pages * page_size is skipped.  A slot named twice
  *            in one call ends with blocks of either token.
@@ -325,7 +329,8 @@ fp4q_status fp4q_kv_read(const fp4q_spec* spec, const fp4q_kv_cache* cache, cons
  * h / (q_heads / kv_heads).
  *   q, out   [total_q, q_heads, head_dim] of `dtype`, the head_dim values
  *            contiguous, row and head strides in elements; bases and strides
- *            16-byte aligned.
+ *            16-byte aligned.  The rows of out share no element, in the same
+ *            sense as those of a written cache.
  *   lse      fp32 [total_q, q_heads] contiguous, or NULL.
  *   q_starts int32 [batch + 1] on the device: the queries of sequence b are
  *            rows q_starts[b] .. q_starts[b+1] - 1.  NULL: every sequence has

@@ -441,8 +441,13 @@ class KvCache:
     one global scale float32 [1] each (None for MXFP4).  The tensors are the
     caller's; this handle checks them once, keeps references to them and passes
     their addresses on.  A contiguous cache [B, H, T, D] is one of B pages of T
-    tokens.  Expanded dimensions can be read, not written.  `scale_rule`, `window` and `rotate` say how rows are written (and
-    `rotate` how they are read)."""
+    tokens.  Expanded dimensions can be read, not written.  `scale_rule`,
+    `window` and `rotate` say how rows are written (and `rotate` how they are
+    read).
+
+    The calls run on torch's current stream of the cache's device, or on
+    `stream`, one of that device; tensors that they are given must be ready
+    there, and stay as they are until it has passed the call."""
 
     def __init__(self, k_codes, k_scales, k_global, v_codes, v_scales, v_global,
                  format=FP4Q_NVFP4, scale_rule=FP4Q_SCALE_ABSMAX, window=None, rotate=0,
@@ -542,6 +547,9 @@ class _on:
     def __init__(self, device, stream):
         self.inner = [torch.cuda.device(device)]
         if stream is not None:
+            # entered, it would make its own device the current one
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, but the cache is on {device}")
             self.inner.append(torch.cuda.stream(stream))
 
     def __enter__(self):

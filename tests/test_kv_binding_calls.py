@@ -69,3 +69,19 @@ def test_sizes_that_are_no_integers_are_refused(lib):
     for kw in (dict(max_kv=64.0), dict(max_q=2.0), dict(window=4.0)):
         with pytest.raises(TypeError):
             B.attend_workspace_bytes(c, a["q"], a["kv_lens"], q_starts=a["q_starts"], **kw)
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    """Such a stream would make its device the current one, and the call would run on the cache's device's own stream."""
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    c = cache()
+    monkeypatch.setattr(c, "device", torch.device("cuda", 0))
+    slots, x = torch.zeros(2, dtype=torch.int64), torch.zeros(2, 2, 128)
+    for call in (lambda s: B.kv_write(c, x, x, slots, stream=s), lambda s: B.kv_read(c, slots, stream=s),
+                 lambda s: B.attend(c, torch.zeros(2, 2, 128), torch.zeros(2, dtype=torch.int32), stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call(Stream(1))
+    B._on(torch.device("cuda", 0), Stream(0))  # nothing is entered yet

@@ -305,11 +305,13 @@ typedef struct {
  *            ones before it cover.
  *   slots    int64 [tokens] on the device; a token whose slot is negative or
  *            not below num_pages * page_size is skipped.  A slot named twice
- *            in one call ends with blocks of either token.
+ *            in one call ends with bytes of either token: its codes and its
+ *            scales may come from different ones.
  * Every block gets the codes and the scale that fp4q_quantize gives it under
  * the same spec with the global scale given: ABSMAX, SWEEP and, for NVFP4,
  * FOUR_OVER_SIX.
- * Launches one kernel and takes no workspace. */
+ * Launches one kernel (several past 2^34 values of K, where 31 bits no longer
+ * number the lanes) and takes no workspace. */
 fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, const void* k,
                           const void* v, int32_t dtype, int64_t tokens, int64_t k_token_stride,
                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,

@@ -610,8 +610,17 @@ def kv_read(cache, slots, dtype=torch.float32, stream=None):
 def _numbers(max_kv, max_q, causal, window, scale):
     """The numbers of an attention call as Python's own: what counts is an
     argument's value now (a 0-dimensional tensor may change in place)."""
-    return (None if max_kv is None else operator.index(max_kv), None if max_q is None else operator.index(max_q),
-            int(causal), operator.index(window), None if scale is None else C.c_float(scale).value)
+    if type(max_kv) is not int and max_kv is not None:
+        max_kv = operator.index(max_kv)
+    if type(max_q) is not int and max_q is not None:
+        max_q = operator.index(max_q)
+    if type(causal) is not bool:
+        causal = int(causal)
+    if type(window) is not int:
+        window = operator.index(window)
+    if type(scale) is not float and scale is not None:
+        scale = C.c_float(scale).value
+    return max_kv, max_q, causal, window, scale
 
 
 def _attention(cache, q, kv_lens, max_kv, block_table, q_starts, max_q, causal, window, scale, out):

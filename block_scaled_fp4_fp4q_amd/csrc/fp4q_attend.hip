@@ -249,13 +249,15 @@ __device__ __forceinline__ int seen_offset(int offset, int key, int first)
 // are loaded while these are computed.
 //
 // Bound by HBM where there are many keys: 64 sequences of 4096 keys and 32 heads
-// of 128 values (1.2 GB of codes and scales) take 219 us with the joining, a
-// steady 6.0 TB/s.  Short of that by the fixed cost of a workgroup (about 8 us:
-// lengths, pages, the first loads, the waves' join), which is all that 131 keys
-// of 8 heads cost; 32 sequences of up to 8192 keys and 8 heads (170 MB, 28 us at
-// that rate) take 45 us with it and with the joining.  With two 16-row tiles of a wave and two parts of
-// the probabilities the issue of conversions and products joins in: 3 sequences
-// of 4 queries over up to 65521 keys, MXFP4, 39 us for 95 MB.
+// of 128 values (1.21 GB of codes and scales) take 219 us with the joining's 5,
+// 5.65 TB/s over the kernel.  Short of that by the fixed cost of a workgroup
+// (about 8 us: lengths, pages, the first loads, the waves' join), which is all
+// that 131 keys of 8 heads cost; 32 sequences of up to 8192 keys and 8 heads
+// (170 MB, 30 us at that rate) take 45 us with it and with the joining.  With two
+// 16-row tiles of a wave and two parts of the probabilities the issue of
+// conversions and products joins in: 3 sequences of 4 queries over up to 65521
+// keys, MXFP4, 39 us for 95 MB; rotated (three parts of the queries) 51,
+// binary32 (three of both) 63.
 // Measured and left: codes two tiles ahead (219 -> 245 us), two steps
 // unrolled (no change), a pair's workgroups spread by slices of the whole work
 // (half the engines idle, 345 us).
@@ -975,7 +977,11 @@ __global__ __launch_bounds__(kThreads, few_waves_of(D, NQ, QT)) void attend_few(
 // 128 over 8 KV heads, NVFP4, 562-600 us: 915-980 TFLOP/s of the pairs seen, where
 // a library's large f16 product reaches 1175.  Two times 509 queries after 16384
 // keys, MXFP4, 32 heads: 356 us with the joining (MXFP4's probabilities are two
-// products each).  Measured and left: waves 4-7 half a step behind 0-3 (a third
+// products each).  Every part of the queries stays in registers, which costs the
+// forms of more than one: the same 8192 queries rotated take 702 us (MXFP4 1131,
+// 30 registers spilled) and in binary32 1436 (1694), one wave per SIMD; with 256
+// values a head there is always one, 1879 us (2185), and more parts spill 28 or
+// 94 registers, 2839 (4639).  Measured and left: waves 4-7 half a step behind 0-3 (a third
 // buffer of V and the logits kept over the barrier: 594 -> 630 us, and 361 ->
 // 413 with spilled registers), wave priorities around the products (no change),
 // workgroups of four waves (119 -> 109 us for 96 rows after 8192 keys, but 37 -> 45

@@ -20,9 +20,13 @@ constexpr int kSegment = 4096;                    // keys whose places are looke
 
 inline size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// waves per SIMD that the kernel for few queries is built for: what its
-// registers allow without spilling (rows16: 16-row tiles of a wave; parts: 16-bit
-// parts of a query)
+// Waves per SIMD that the kernel for few queries is built for (rows16: 16-row
+// tiles of a wave; parts: 16-bit parts of a query): as many as its registers
+// allow without spilling, but for three parts (MXFP4, rotated or binary32) at 128
+// values, which spill 9 to 17 of them.  One wave less spills nothing there and
+// was faster at most sizes (32 sequences of 8192 keys, 4 heads, binary32: 1 query
+// 43 -> 39 us, 4 queries 85 -> 68; 3 of 65521, rotated, 8 queries 81 -> 85), as at
+// 64 values, where it is taken.
 constexpr int few_waves_of(int dim, int parts, int rows16)
 {
     return dim == 64    ? (rows16 == 1 ? 4 : 3) - (parts == 3 ? 1 : 0)
@@ -213,12 +217,17 @@ inline AttendPlan plan_of(const AttendArgs& a)
     p.rows_per_tile = (a.bf16 && a.kv.head_dim < 256) ? 256 : 128; // 32 rows a wave
     p.tiles = (int)((rows + p.rows_per_tile - 1) / p.rows_per_tile);
     const int64_t units = pairs * p.tiles;
-    // One workgroup of eight waves fills a CU.  Fewer row tiles than CUs are cut
-    // along the keys where that pays: c chunks save steps of 64 keys (1.9 us
-    // each at 128 values a head), and cost the joining launch (5 us) and
-    // the partial results' way to memory and back (5 TB/s).  512 queries
-    // of 32 heads alone are not cut (26 us, 33 with two chunks), after 16384
-    // keys they are.
+    // A workgroup is given a CU of its own (of those with four waves and 64 values
+    // a head two would fit).  Fewer row tiles than CUs are cut along the keys where
+    // that pays: c chunks save steps of 64 keys, and cost the joining launch (5 us)
+    // and the partial results' way to memory and back (5 TB/s).  A step is charged
+    // 1.9 us at 128 values a head, as measured for unrotated NVFP4 in bf16; forms
+    // with more products in a step take up to three times that and are cut no
+    // finer.  512 queries of 32 heads alone are not cut (26 us, 33 with two
+    // chunks), after 16384 keys they are (180 against 511 us; MXFP4 binary32 416
+    // against 799).  Of 70 to 1024 rows over 512 to 65536 keys, NVFP4 bf16 and MXFP4
+    // binary32, 64, 128 and 256 values, none was slower than without the cut: 96
+    // rows of one head over 1024 keys 21 against 33 us, over 8192 30 against 197.
     const int64_t most_cuts = (kCus + units - 1) / units;
     double best = 0.0;
     int64_t chunk = 0;

@@ -380,10 +380,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_absmax(const KvWriteArgs a,
 // values), so that a wave's stores are contiguous; the un-rotation's wide
 // stages cross the 2, 4 or 8 lanes that share a block, in the order and with
 // the roundings of the in-register transform.  Bound by HBM: 65536 rows of 8
-// heads of 128 values, K and V, rotated, to bf16 move 345 MB in 67 us (5.1 TB/s)
-// from slots in order, in 75 us from slots in no order, where a row's 64 bytes
-// of codes and 8 of scales are parts of 128-byte lines.  (Plain instead of
-// nontemporal stores: 100 against 75 us.)
+// heads of 128 values, K and V, rotated, to bf16 move 345 MB in 89 us (3.9 TB/s)
+// where every call reads other rows (six caches in turn, 450 MB), in 92 us from
+// slots in no order, whose 64 bytes of codes and 8 of scales a row are parts of
+// 128-byte lines.  Two or three caches in turn, 150 or 225 MB, stay in part in
+// the last-level cache: 68 and 75 us.  (Plain instead of nontemporal stores: 94
+// to 96 us whatever is cached.)
 template <bool MX, bool BF16, bool ROT>
 __global__ __launch_bounds__(kThreads) void kv_read(const KvReadArgs a, const int lane_shift,
                                                     const uint32_t items)
@@ -485,7 +487,8 @@ int log2_of(int n)
 // kernels stride over the rest).  A write gets one block per lane up to 2^20
 // workgroups: 2^20 tokens of 8 heads of 128 values take 1075 us with AbsMax
 // and 3519 us swept, with at most 8192 workgroups 1289 and 3562.  A read is
-// faster with at most 8192: 65536 such rows to bf16 67 against 76 us.
+// faster with at most 8192: 65536 such rows to bf16, in order, 89 against 105 us
+// from memory and 68 against 76 where much of them is cached.
 constexpr uint32_t kWriteGroups = 1u << 20, kReadGroups = 8192u;
 
 int groups_for(uint32_t items, uint32_t most)

@@ -357,8 +357,15 @@ fp4q_status fp4q_kv_read(const fp4q_spec* spec, const fp4q_kv_cache* cache, cons
  * kv_len is negative or above max_kv, or above what its pages hold, or that
  * reads through a page number out of range, gives NaN in the rows concerned.
  * Logits, softmax statistics and sums are binary32.  Dequantized values enter
- * the matrix products exactly; queries and probabilities as up to three
- * 16-bit parts, so that binary32 calls keep about binary32's precision.
+ * the matrix products exactly, queries and probabilities as sums of 16-bit parts:
+ *   queries        bf16 as they are; rotated or binary32 in 22 bits (NVFP4) or
+ *                  24 (MXFP4);
+ *   probabilities  for bf16 results in 11 bits (NVFP4) or 16 (MXFP4), for
+ *                  binary32 results in 22 or 24.
+ * Preconditions beside those above: rotated queries sum to less than 2^127 in
+ * magnitude over a block.  MXFP4 has no global scale that stays out of the sums:
+ * sum_d |q_d k_d|, and 2^15 sum_j |v_j| over the keys that a query sees, have to
+ * be below 2^127.
  *   workspace  fp4q_attend_workspace_bytes() bytes, 256-byte aligned (NULL
  *            where that is 0): partial results of keys split over workgroups. */
 typedef struct {

@@ -708,6 +708,8 @@ def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_
 
     kv_lens      int32 [batch]: keys of each sequence, its new ones among them.
     max_kv       a bound on kv_lens (default: what a sequence's pages hold).
+                 Calls of the same shapes and numbers share their checks: a
+                 bound that stays costs less than one that follows the lengths.
     block_table  int32 [batch, entries]: the pages of each sequence; None:
                  sequence b is page b (a contiguous cache).
     q_starts     int32 [batch + 1]: the queries of sequence b are the rows

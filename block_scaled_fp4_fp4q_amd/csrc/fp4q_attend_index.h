@@ -199,7 +199,8 @@ inline AttendPlan plan_of(const AttendArgs& a)
         p.rows_per_tile = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
         p.tiles = 1;
         const int64_t steps = (span + kStepKeys - 1) / kStepKeys;
-        if (pairs > most / (steps > rows ? steps : rows) || a.total_q > 0x7FFFFFFF)
+        // the joining launch has a workgroup for each row; all steps count in 31 bits
+        if (pairs > most / rows || (steps != 0 && pairs > 0x7FFFFFFF / steps) || a.total_q > 0x7FFFFFFF)
             return p; // groups == 0: refused
         p.groups = (int)pairs;
         if (steps > kMinPart) {

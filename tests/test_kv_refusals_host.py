@@ -89,3 +89,15 @@ def test_expanded_tensors():
     c.struct.k_scales, c.struct.v_codes, c.struct.v_scales = P[1], P[3], P[4]
     assert write(B.lib(), s=c.spec, c=c.struct) == SHAPE
     assert read(B.lib(), s=c.spec, c=c.struct, tokens=0) == 0
+
+
+def test_long_bounds_of_many_sequences_are_not_refused():
+    """512 sequences of 32 heads under a bound of 131072 keys: 16384 pairs of up to 1024 steps each, in 16384 workgroups
+    and one round more. Steps are counted in 31 bits, and only what goes past those is refused."""
+    L = B.lib()
+    s = B.make_spec(global_scale_given=True)
+    c = cache(kv_heads=32, code_page=32 * 1024, scale_page=32 * 128)
+    for max_kv, fits in ((131072, True), (1 << 23, True), (1 << 25, False)):
+        a = call(batch=512, total_q=512, max_q=1, q_heads=32, out_row_stride=4096, q_row_stride=4096, max_kv=max_kv)
+        assert (L.fp4q_attend_workspace_bytes(C.byref(s), C.byref(c), C.byref(a)) > 0) == fits, max_kv
+        assert attend(L, s=s, c=c, a=a) == (-1 if fits else SHAPE), max_kv  # -1: the workspace is missing

@@ -18,6 +18,7 @@ FP4Q_NVFP4, FP4Q_MXFP4, FP4Q_IF4, FP4Q_IF3, FP4Q_IF6 = 0, 1, 2, 3, 4
 FP4Q_F32, FP4Q_BF16 = 0, 1
 FP4Q_SCALE_ABSMAX, FP4Q_SCALE_SWEEP, FP4Q_SCALE_FOUR_OVER_SIX = 0, 1, 2
 FP4Q_OBJ_MSE, FP4Q_OBJ_WMSE = 0, 1
+FP4Q_ACT_SILU, FP4Q_ACT_GELU, FP4Q_ACT_GELU_TANH = 0, 1, 2
 
 STATUS = {0: "FP4Q_OK", -1: "FP4Q_E_NULL", -2: "FP4Q_E_ARG", -3: "FP4Q_E_SHAPE",
           -4: "FP4Q_E_UNSUPPORTED", -5: "FP4Q_E_HIP", -6: "FP4Q_E_ALIGN", -7: "FP4Q_E_SCRATCH"}
@@ -26,7 +27,8 @@ STATUS = {0: "FP4Q_OK", -1: "FP4Q_E_NULL", -2: "FP4Q_E_ARG", -3: "FP4Q_E_SHAPE",
 EXPORTS = ("fp4q_workspace_bytes", "fp4q_quantize", "fp4q_quantize_noalloc",
            "fp4q_quantize_relaxed", "fp4q_dequantize", "fp4q_error", "fp4q_status_string",
            "fp4q_abi_version", "fp4q_kv_write", "fp4q_kv_read", "fp4q_attend",
-           "fp4q_attend_workspace_bytes")
+           "fp4q_attend_workspace_bytes", "fp4q_matmul", "fp4q_matmul_workspace_bytes",
+           "fp4q_gated", "fp4q_gated_workspace_bytes")
 
 
 class fp4q_spec(C.Structure):
@@ -53,6 +55,11 @@ class fp4q_attention(C.Structure):
                 ("max_kv", C.c_int32), ("q_heads", C.c_int32), ("dtype", C.c_int32),
                 ("causal", C.c_int32), ("window", C.c_int32), ("scale", C.c_float),
                 ("reserved", C.c_int32)]
+
+
+class fp4q_weight(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("global_scale", C.c_void_p),
+                ("rows", C.c_int64), ("cols", C.c_int64)]
 
 
 class Fp4qError(RuntimeError):
@@ -97,6 +104,14 @@ def _lib_handle():
         L.fp4q_attend_workspace_bytes.argtypes = [sp, kp, ap]
         L.fp4q_attend.restype = C.c_int
         L.fp4q_attend.argtypes = [sp, kp, ap, vp, sz, vp]
+        wp = C.POINTER(fp4q_weight)
+        L.fp4q_matmul_workspace_bytes.restype = L.fp4q_gated_workspace_bytes.restype = sz
+        L.fp4q_matmul_workspace_bytes.argtypes = [sp, wp, i64, i32]
+        L.fp4q_gated_workspace_bytes.argtypes = [sp, wp, i64, i32]
+        L.fp4q_matmul.restype = C.c_int
+        L.fp4q_matmul.argtypes = [sp, wp, vp, i32, i64, i64, vp, i64, vp, sz, vp]
+        L.fp4q_gated.restype = C.c_int
+        L.fp4q_gated.argtypes = [sp, wp, wp, i32, vp, i32, i64, i64, vp, i64, vp, sz, vp]
         L.fp4q_status_string.restype = C.c_char_p
         L.fp4q_status_string.argtypes = [C.c_int]
         L.fp4q_abi_version.restype = C.c_int
@@ -544,12 +559,12 @@ class _on:
     """The device as the current one, and a given stream as torch's current
     one there, so that what a call allocates belongs to its stream."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, what="cache"):
         self.inner = [torch.cuda.device(device)]
         if stream is not None:
             # entered, it would make its own device the current one
             if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, but the cache is on {device}")
+                raise ValueError(f"stream is on {stream.device}, but the {what} is on {device}")
             self.inner.append(torch.cuda.stream(stream))
 
     def __enter__(self):
@@ -764,3 +779,150 @@ def attend(cache, q, kv_lens, max_kv=None, block_table=None, q_starts=None, max_
         cache._calls.pop(key, None)
         _check("fp4q_attend", st)
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# products with 4-bit weights
+# ---------------------------------------------------------------------------
+
+class QuantizedWeight:
+    """A weight [rows, cols] (outputs x inputs) in NVFP4 or MXFP4, as `quantize`
+    returns it: codes uint8 [rows * cols / 2], scales uint8 [rows * cols /
+    block] (any contiguous shapes) and the global scale float32 [1] (None for
+    MXFP4).  `rotate` is what it was quantized with.  The tensors are the
+    caller's; this handle checks them once, keeps references to them and passes
+    their addresses on."""
+
+    def __init__(self, codes, scales, global_scale, rows, cols, format=FP4Q_NVFP4, rotate=0,
+                 require_cuda=True):
+        if format not in (FP4Q_NVFP4, FP4Q_MXFP4):
+            raise ValueError("products take NVFP4 or MXFP4 weights")
+        rows, cols = operator.index(rows), operator.index(cols)
+        self.spec = make_spec(format, rotate=rotate)
+        if rotate not in (0, self.spec.block):
+            raise ValueError(f"rotate is {rotate}; expected 0 or the block, {self.spec.block}")
+        if rows < 0 or cols < 0 or cols % self.spec.block or cols > 1 << 24 or rows > 1 << 36:
+            raise ValueError(f"a weight of [{rows}, {cols}] is not supported: cols must be a multiple of "
+                             f"{self.spec.block}, at most 2^24")
+        if not isinstance(codes, torch.Tensor):
+            raise TypeError("codes must be a torch tensor")
+        self.rows, self.cols, self.device = rows, cols, codes.device
+        _check_device("codes", codes, None, require_cuda)
+        for name, t, n in (("codes", codes, rows * cols // 2), ("scales", scales, rows * cols // self.spec.block)):
+            _check_tensor(name, t, _U8, n, self.device, require_cuda)
+        _check_tensor("global_scale", global_scale, _F32, 1, self.device, require_cuda,
+                      optional=format == FP4Q_MXFP4)
+        self.tensors = (codes, scales, global_scale)
+        ptr = [None if t is None else t.data_ptr() for t in self.tensors]
+        self.struct = fp4q_weight(*ptr, rows, cols)
+        self._spec, self._struct = C.byref(self.spec), C.byref(self.struct)
+        self._needs = {}  # workspace bytes by (number of weights, tokens, dtype)
+
+
+def _token_rows(name, t, cols, device, dtype=None):
+    """A [tokens, cols] tensor whose last dimension is contiguous; returns its
+    rows and their stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, but the weight is on {device}")
+    if t.dtype not in (_X if dtype is None else (dtype,)):
+        want = " or ".join(map(str, _X if dtype is None else (dtype,)))
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {want}")
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected [tokens, {cols}]")
+    rows, st = t.shape[0], t.stride()
+    if st[1] != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    # torch gives a single row any stride
+    return rows, st[0] if rows > 1 else cols
+
+
+def _product_need(weights, tokens, code):
+    """Workspace bytes of a product, asked of the library once for each size."""
+    w = weights[0]
+    key = (len(weights), tokens, code)
+    need = w._needs.get(key)
+    if need is None:
+        ask = _lib_handle().fp4q_matmul_workspace_bytes if len(weights) == 1 else \
+            _lib_handle().fp4q_gated_workspace_bytes
+        if len(w._needs) >= 256:
+            w._needs.clear()
+        need = w._needs[key] = int(ask(w._spec, w._struct, tokens, code))
+    return need
+
+
+def matmul_workspace_bytes(weight, tokens, dtype=torch.bfloat16):
+    """Bytes that `matmul` needs as its workspace for x [tokens, cols] of `dtype`."""
+    return _product_need((weight,), operator.index(tokens), FP4Q_BF16 if dtype == torch.bfloat16 else FP4Q_F32)
+
+
+def gated_workspace_bytes(gate, up, tokens, dtype=torch.bfloat16):
+    """Bytes that `gated` needs as its workspace for x [tokens, cols] of `dtype`."""
+    return _product_need((gate, up), operator.index(tokens), FP4Q_BF16 if dtype == torch.bfloat16 else FP4Q_F32)
+
+
+def _product(fn, weights, extra, x, out, workspace):
+    w = weights[0]
+    dev = w.device
+    if isinstance(x, torch.Tensor) and x.dim() != 2:
+        if x.dim() < 1 or not x.is_contiguous() or (out is not None and not out.is_contiguous()):
+            raise ValueError("x (and out) of other than 2 dimensions must be contiguous")
+        if out is not None and tuple(out.shape) != (*x.shape[:-1], w.rows):
+            raise ValueError(f"out has shape {tuple(out.shape)}; expected {(*x.shape[:-1], w.rows)}")
+        lead = x.shape[:-1]
+        tokens = 1
+        for n in lead:
+            tokens *= n
+        y = _product(fn, weights, extra, x.reshape(tokens, x.shape[-1]),
+                     None if out is None else out.view(tokens, w.rows), workspace)
+        return y.view(*lead, w.rows)
+    tokens, xs = _token_rows("x", x, w.cols, dev)
+    if out is None:
+        out = torch.empty((tokens, w.rows), dtype=x.dtype, device=dev)
+        ys = w.rows
+    else:
+        rows, ys = _token_rows("out", out, w.rows, dev, x.dtype)
+        if rows != tokens:
+            raise ValueError(f"out has {rows} rows; expected {tokens}")
+    code = FP4Q_BF16 if x.dtype == torch.bfloat16 else FP4Q_F32
+    need = _product_need(weights, tokens, code)
+    space = None
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _check_tensor("workspace", workspace, _U8, need, dev, require_cuda=False)
+        space = workspace.data_ptr()
+    st = getattr(_lib_handle(), fn)(w._spec, *[u._struct for u in weights], *extra, x.data_ptr(), code, tokens, xs,
+                                    out.data_ptr(), ys, space, need, _current_stream(dev.index))
+    if st:
+        _check(fn, st)
+    return out
+
+
+def matmul(weight, x, out=None, workspace=None, stream=None):
+    """x W^T for x float32 or bfloat16 [tokens, cols] (the last dimension
+    contiguous; more or fewer leading dimensions if all are), W the values of
+    the quantized weight [rows, cols]: [tokens, rows] of x's dtype.  out may
+    have any row stride.  Runs on torch's current stream of the weight's
+    device, or on `stream`, one of that device.  A given workspace (uint8,
+    matmul_workspace_bytes) must not be shared by calls that may run at the
+    same time."""
+    if not _here(weight.device, stream):
+        with _on(weight.device, stream, "weight"):
+            return matmul(weight, x, out, workspace)
+    return _product("fp4q_matmul", (weight,), (), x, out, workspace)
+
+
+def gated(gate, up, x, activation=FP4Q_ACT_SILU, out=None, workspace=None, stream=None):
+    """act(x Wgate^T) * (x Wup^T), the first half of a gated feed-forward block,
+    for two weights of the same sizes, format and rotation; `activation` is
+    FP4Q_ACT_SILU, FP4Q_ACT_GELU or FP4Q_ACT_GELU_TANH.  Else as `matmul`."""
+    if (gate.rows, gate.cols, gate.spec.format, gate.spec.rotate, gate.device) != \
+            (up.rows, up.cols, up.spec.format, up.spec.rotate, up.device):
+        raise ValueError("gate and up must have the same sizes, format, rotation and device")
+    if not _here(gate.device, stream):
+        with _on(gate.device, stream, "weight"):
+            return gated(gate, up, x, activation, out, workspace)
+    return _product("fp4q_gated", (gate, up), (operator.index(activation),), x, out, workspace)

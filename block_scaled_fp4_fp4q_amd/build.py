@@ -9,12 +9,14 @@ Code-generation flags that the library's exactness depends on:
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp4q.so")
-SOURCES = ["fp4q_kernels.hip", "fp4q_kv.hip", "fp4q_attend.hip", "fp4q_capi.cpp", "fp4q_kv_capi.cpp"]
+SOURCES = ["fp4q_kernels.hip", "fp4q_kv.hip", "fp4q_attend.hip", "fp4q_matmul.hip", "fp4q_capi.cpp",
+           "fp4q_kv_capi.cpp", "fp4q_matmul_capi.cpp"]
 ARCH = os.environ.get("FP4Q_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -29,14 +31,16 @@ FLAGS = [
 
 
 def build(verbose=False):
-    objs = []
-    for src in SOURCES:
+    def compile_one(src):
         obj = os.path.join(CSRC, src.rsplit(".", 1)[0] + ".o")
         cmd = [HIPCC, *FLAGS, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(4) as pool:  # a compiler process each
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:

@@ -399,6 +399,51 @@ size_t fp4q_attend_workspace_bytes(const fp4q_spec* spec, const fp4q_kv_cache* c
 fp4q_status fp4q_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
                         const fp4q_attention* call, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- products with 4-bit weights ---------------------------------------------
+ *
+ * A weight [rows, cols] (outputs x inputs) as fp4q_quantize writes it: NVFP4 or
+ * MXFP4 codes [rows*cols/2] and scales [rows*cols/block], and for NVFP4 the
+ * global scale (read at each call; may be NULL for MXFP4).  spec of the calls
+ * below: format (others: FP4Q_E_UNSUPPORTED), block, and rotate = 0, or = block
+ * for a weight that was quantized with it; the other members are ignored.
+ * cols is at most 2^24.  codes 8-byte aligned (16 for MXFP4), scales of any
+ * alignment. */
+typedef struct {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const float* global_scale;
+    int64_t rows, cols;
+} fp4q_weight;
+
+typedef enum { FP4Q_ACT_SILU = 0, FP4Q_ACT_GELU = 1, FP4Q_ACT_GELU_TANH = 2 } fp4q_activation;
+
+/* y [tokens, rows] = x [tokens, cols] W^T, W the dequantized weight (un-rotated,
+ * where it is stored rotated: x is rotated instead).
+ *   x        dtype FP4Q_F32 or FP4Q_BF16, 16-byte aligned, row stride in
+ *            elements, a multiple of 16 bytes.
+ *   y        of the same dtype, row stride in elements, at least `rows`.
+ *   workspace  fp4q_matmul_workspace_bytes() bytes, 256-byte aligned (NULL where
+ *            that is 0).
+ * Weights enter the products exactly; bf16 x does, binary32 x in 24 bits, rotated
+ * bf16 x in 16 bits (rotated in binary32).  Sums are binary32, in an order
+ * that the sizes alone decide, and the global scale is a factor of the sum.
+ * Precondition beside those above: sum_k |x_k w_k| / S (MXFP4: S = 1) is below
+ * 2^127.  A row of x with values that are not finite gives what it gives in
+ * its own row of y alone. */
+size_t fp4q_matmul_workspace_bytes(const fp4q_spec* spec, const fp4q_weight* w, int64_t tokens, int32_t dtype);
+fp4q_status fp4q_matmul(const fp4q_spec* spec, const fp4q_weight* w, const void* x, int32_t dtype, int64_t tokens,
+                        int64_t x_stride, void* y, int64_t y_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/* y = act(x Wgate^T) * (x Wup^T), element by element, for two weights of the same
+ * sizes: both products, the activation (fp4q_activation: g / (1 + exp(-g)),
+ * g Phi(g) with the normal distribution Phi, or its tanh form 0.5 g (1 + tanh(
+ * sqrt(2/pi) (g + 0.044715 g^3)))) and the product in one pass over x; the sums are
+ * not rounded in between.  Arguments as for fp4q_matmul. */
+size_t fp4q_gated_workspace_bytes(const fp4q_spec* spec, const fp4q_weight* gate, int64_t tokens, int32_t dtype);
+fp4q_status fp4q_gated(const fp4q_spec* spec, const fp4q_weight* gate, const fp4q_weight* up, int32_t activation,
+                       const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, void* y, int64_t y_stride,
+                       void* workspace, size_t ws_bytes, void* stream);
+
 const char* fp4q_status_string(fp4q_status status);
 int fp4q_abi_version(void);
 

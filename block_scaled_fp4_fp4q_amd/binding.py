@@ -6,6 +6,7 @@ arithmetic happens in the library's HIP kernels.  There is no fallback: if the
 library is missing, or a call is rejected, this module raises.
 """
 import ctypes as C
+import math
 import operator
 import os
 
@@ -26,7 +27,7 @@ STATUS = {0: "FP4Q_OK", -1: "FP4Q_E_NULL", -2: "FP4Q_E_ARG", -3: "FP4Q_E_SHAPE",
 # every symbol include/fp4q.h declares
 EXPORTS = ("fp4q_workspace_bytes", "fp4q_quantize", "fp4q_quantize_noalloc",
            "fp4q_quantize_relaxed", "fp4q_dequantize", "fp4q_error", "fp4q_status_string",
-           "fp4q_abi_version", "fp4q_kv_write", "fp4q_kv_read", "fp4q_attend",
+           "fp4q_abi_version", "fp4q_kv_write", "fp4q_kv_append", "fp4q_kv_read", "fp4q_attend",
            "fp4q_attend_workspace_bytes", "fp4q_matmul", "fp4q_matmul_workspace_bytes",
            "fp4q_gated", "fp4q_gated_workspace_bytes")
 
@@ -44,6 +45,18 @@ class fp4q_kv_cache(C.Structure):
                 ("head_dim", C.c_int32), ("reserved", C.c_int32),
                 ("code_page", C.c_int64), ("code_head", C.c_int64), ("code_token", C.c_int64),
                 ("scale_page", C.c_int64), ("scale_head", C.c_int64), ("scale_token", C.c_int64)]
+
+
+class fp4q_append(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_row_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("q_out", C.c_void_p), ("out_row_stride", C.c_int64), ("out_head_stride", C.c_int64),
+                ("k", C.c_void_p), ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("v", C.c_void_p), ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("rope", C.c_void_p),
+                ("rope_stride", C.c_int64), ("rope_rows", C.c_int64), ("positions", C.c_void_p),
+                ("slots", C.c_void_p), ("tokens", C.c_int64), ("q_heads", C.c_int32),
+                ("rope_dim", C.c_int32), ("interleaved", C.c_int32), ("dtype", C.c_int32),
+                ("eps", C.c_float), ("reserved", C.c_int32)]
 
 
 class fp4q_attention(C.Structure):
@@ -98,6 +111,8 @@ def _lib_handle():
         kp, ap = C.POINTER(fp4q_kv_cache), C.POINTER(fp4q_attention)
         L.fp4q_kv_write.restype = C.c_int
         L.fp4q_kv_write.argtypes = [sp, kp, vp, vp, i32, i64, i64, i64, i64, i64, vp, vp]
+        L.fp4q_kv_append.restype = C.c_int
+        L.fp4q_kv_append.argtypes = [sp, kp, C.POINTER(fp4q_append), vp]
         L.fp4q_kv_read.restype = C.c_int
         L.fp4q_kv_read.argtypes = [sp, kp, vp, i64, vp, vp, i32, vp]
         L.fp4q_attend_workspace_bytes.restype = sz
@@ -601,6 +616,120 @@ def kv_write(cache, k, v, slots, stream=None):
     _check("fp4q_kv_write", _lib_handle().fp4q_kv_write(
         cache._spec, cache._struct, k.data_ptr(), v.data_ptr(), _dtype_code(k), n, ks[0], ks[1],
         vs[0], vs[1], slots.data_ptr(), _current_stream(dev.index)))
+
+
+def rope_table(length, rope_dim, base=10000.0, frequencies=None, factor=1.0, magnitude=1.0, device="cuda"):
+    """The table that `kv_append` turns rows by: float32 [length, rope_dim], for
+    each position p the cosines of p / factor * frequency_i, then the sines,
+    times `magnitude`; the angles are taken in binary64.  frequencies (of any
+    scaling, rope_dim / 2 of them) default to base ** (-2 i / rope_dim)."""
+    if rope_dim % 2 or rope_dim < 0 or length < 0:
+        raise ValueError("rope_dim must be even, and sizes not negative")
+    if frequencies is None:
+        frequencies = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / max(rope_dim, 1))
+    else:
+        frequencies = torch.as_tensor(frequencies, dtype=torch.float64, device=device)
+        if frequencies.shape != (rope_dim // 2,):
+            raise ValueError(f"frequencies has shape {tuple(frequencies.shape)}; expected [{rope_dim // 2}]")
+    angles = (torch.arange(length, dtype=torch.float64, device=device) / factor)[:, None] * frequencies
+    return (torch.cat((angles.cos(), angles.sin()), 1) * magnitude).to(torch.float32)
+
+
+def rope_frequencies(rope_dim, base=10000.0, factor=1.0, original_length=None, fast=32.0, slow=1.0, device="cuda"):
+    """Frequencies (binary64) for contexts `factor` times as long as the original
+    length: those that turn at least `fast` times over it stay, those that turn
+    at most `slow` times are divided by the factor, and those between are mixed
+    linearly in their index.  Without an original length all are divided."""
+    f = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / rope_dim)
+    if original_length is None:
+        return f / factor
+
+    def index(turns):  # of the frequency that turns so often over the original length
+        return rope_dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rope_dim - 1)
+    i = torch.arange(rope_dim // 2, dtype=torch.float64, device=device)
+    divided = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    return f * (1 - divided) + f / factor * divided
+
+
+def _norm_weight(name, t, dim, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, but the cache is on {device}")
+    if t.dtype != torch.float32 or tuple(t.shape) != (dim,) or t.stride(0) != 1:
+        raise ValueError(f"{name} must be float32 [{dim}], contiguous")
+    return t.data_ptr()
+
+
+def kv_append(cache, k, v, slots, q=None, positions=None, rope=None, interleaved=False, q_weight=None,
+              k_weight=None, eps=1e-6, out=None, stream=None):
+    """New tokens' rows as a projection leaves them, in one launch: each head of q
+    and k is normed (where its weight is given), turned by its position (where
+    a table is given), and k and v are written into the cache as `kv_write`
+    writes them.  Returns q so, or None without q.
+
+    k, v         float32 or bfloat16 [tokens, kv_heads, head_dim], the last
+                 dimension contiguous; q likewise with any number of heads.
+    slots        int64 [tokens]; a negative or too large slot skips the writing.
+    q_weight, k_weight  float32 [head_dim]: x / sqrt(mean x^2 + eps) * weight.
+    rope         float32 [positions, rope_dim], cosines then sines (rope_table);
+                 rope_dim a multiple of 16, the values of a head that turn.
+    positions    int64 [tokens], rows of the table; one out of range gives NaN in
+                 q and is not written.
+    interleaved  pairs are neighbours (2i, 2i + 1), not halves (i, i + rope_dim / 2).
+    out          like q, of any strides without expanded dimensions; may be q."""
+    dev = cache.device
+    if not _here(dev, stream):
+        with _on(dev, stream):
+            return kv_append(cache, k, v, slots, q, positions, rope, interleaved, q_weight, k_weight, eps, out)
+    _ints("slots", slots, torch.int64, dev)
+    n, dim = slots.shape[0], cache.head_dim
+    ks = _rows("k", k, n, cache.heads, dim, dev)
+    vs = _rows("v", v, n, cache.heads, dim, dev)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    call = fp4q_append(k=k.data_ptr(), k_token_stride=ks[0], k_head_stride=ks[1], v=v.data_ptr(),
+                       v_token_stride=vs[0], v_head_stride=vs[1], slots=slots.data_ptr(), tokens=n,
+                       dtype=_dtype_code(k), interleaved=bool(interleaved), eps=eps,
+                       q_weight=_norm_weight("q_weight", q_weight, dim, dev),
+                       k_weight=_norm_weight("k_weight", k_weight, dim, dev))
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise TypeError("q must be a torch tensor [tokens, q_heads, head_dim]")
+        heads = q.shape[1]
+        qs = _rows("q", q, n, heads, dim, dev, (k.dtype,))
+        if out is None:
+            out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+        os = _rows("out", out, n, heads, dim, dev, (q.dtype,))
+        call.q, call.q_row_stride, call.q_head_stride, call.q_heads = q.data_ptr(), qs[0], qs[1], heads
+        call.q_out, call.out_row_stride, call.out_head_stride = out.data_ptr(), os[0], os[1]
+    elif out is not None:
+        raise ValueError("out is given without q")
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor):
+            raise TypeError("rope must be a torch tensor")
+        if rope.device != dev:
+            raise ValueError(f"rope is on {rope.device}, but the cache is on {dev}")
+        if rope.dtype != torch.float32 or rope.dim() != 2 or (rope.numel() > 0 and rope.stride(1) != 1):
+            raise ValueError("rope must be float32 [positions, rope_dim], the last dimension contiguous")
+        if rope.shape[1] % 16 or not 0 < rope.shape[1] <= dim:
+            raise ValueError(f"rope_dim is {rope.shape[1]}; expected a multiple of 16 up to head_dim, {dim}")
+        if positions is None:
+            raise ValueError("rope needs positions")
+        _ints("positions", positions, torch.int64, dev)
+        if positions.shape[0] != n:
+            raise ValueError(f"positions has {positions.shape[0]} entries; expected {n}")
+        call.rope, call.rope_rows, call.rope_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
+        # torch gives a single row any stride
+        call.rope_stride = rope.stride(0) if rope.shape[0] > 1 else rope.shape[1]
+        call.positions = positions.data_ptr()
+    _check("fp4q_kv_append", _lib_handle().fp4q_kv_append(cache._spec, cache._struct, C.byref(call),
+                                                          _current_stream(dev.index)))
+    return out
 
 
 def kv_read(cache, slots, dtype=torch.float32, stream=None):

@@ -132,6 +132,35 @@ bool rows_apart(const int64_t (&counts)[N], const int64_t (&strides)[N], int64_t
     return true;
 }
 
+// the rule of a write into the cache
+fp4q_status check_write_spec(const fp4q_spec* spec)
+{
+    if (spec->scale_rule != FP4Q_SCALE_ABSMAX && spec->scale_rule != FP4Q_SCALE_SWEEP &&
+        spec->scale_rule != FP4Q_SCALE_FOUR_OVER_SIX)
+        return FP4Q_E_ARG;
+    if (spec->objective != FP4Q_OBJ_MSE && spec->objective != FP4Q_OBJ_WMSE)
+        return FP4Q_E_ARG;
+    if (spec->objective != FP4Q_OBJ_MSE ||
+        (spec->scale_rule == FP4Q_SCALE_FOUR_OVER_SIX && spec->format != FP4Q_NVFP4))
+        return FP4Q_E_UNSUPPORTED;
+    if (spec->format == FP4Q_NVFP4 && spec->global_scale_given != 1)
+        return FP4Q_E_ARG;
+    if (spec->scale_rule == FP4Q_SCALE_SWEEP &&
+        (spec->sweep_lo > spec->sweep_hi || spec->sweep_lo < -126 || spec->sweep_hi > 126))
+        return FP4Q_E_ARG;
+    return FP4Q_OK;
+}
+
+// rows that share bytes would be written at once
+bool writable(const fp4q_spec* spec, const fp4q_kv_cache* cache)
+{
+    const int64_t counts[3] = {cache->num_pages, cache->kv_heads, cache->page_size};
+    return rows_apart<3>(counts, {cache->code_page, cache->code_head, cache->code_token}, cache->head_dim / 2) &&
+           rows_apart<3>(counts, {cache->scale_page, cache->scale_head, cache->scale_token},
+                         cache->head_dim / spec->block) &&
+           !(cache->num_pages != 0 && (cache->k_codes == cache->v_codes || cache->k_scales == cache->v_scales));
+}
+
 fp4q_status check_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
                          const fp4q_attention* c, fp4q::AttendArgs& a)
 {
@@ -217,19 +246,8 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
     fp4q_status st = check_spec(spec);
     if (st != FP4Q_OK)
         return st;
-    if (spec->scale_rule != FP4Q_SCALE_ABSMAX && spec->scale_rule != FP4Q_SCALE_SWEEP &&
-        spec->scale_rule != FP4Q_SCALE_FOUR_OVER_SIX)
-        return FP4Q_E_ARG;
-    if (spec->objective != FP4Q_OBJ_MSE && spec->objective != FP4Q_OBJ_WMSE)
-        return FP4Q_E_ARG;
-    if (spec->objective != FP4Q_OBJ_MSE ||
-        (spec->scale_rule == FP4Q_SCALE_FOUR_OVER_SIX && spec->format != FP4Q_NVFP4))
-        return FP4Q_E_UNSUPPORTED;
-    if (spec->format == FP4Q_NVFP4 && spec->global_scale_given != 1)
-        return FP4Q_E_ARG;
-    if (spec->scale_rule == FP4Q_SCALE_SWEEP &&
-        (spec->sweep_lo > spec->sweep_hi || spec->sweep_lo < -126 || spec->sweep_hi > 126))
-        return FP4Q_E_ARG;
+    if ((st = check_write_spec(spec)) != FP4Q_OK)
+        return st;
     if ((st = check_cache(spec, cache, a.kv)) != FP4Q_OK)
         return st;
     if (!valid_dtype(dtype))
@@ -247,12 +265,7 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
     if (!rows_aligned(k, k_token_stride, k_head_stride, dtype) ||
         !rows_aligned(v, v_token_stride, v_head_stride, dtype) || !aligned(slots, 8))
         return FP4Q_E_ALIGN;
-    // rows that share bytes would be written at once
-    const int64_t counts[3] = {cache->num_pages, cache->kv_heads, cache->page_size};
-    if (!rows_apart<3>(counts, {cache->code_page, cache->code_head, cache->code_token}, cache->head_dim / 2) ||
-        !rows_apart<3>(counts, {cache->scale_page, cache->scale_head, cache->scale_token},
-                       cache->head_dim / spec->block) ||
-        (cache->num_pages != 0 && (cache->k_codes == cache->v_codes || cache->k_scales == cache->v_scales)))
+    if (!writable(spec, cache))
         return FP4Q_E_SHAPE;
     if (tokens == 0)
         return FP4Q_OK;
@@ -271,6 +284,87 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
     a.tokens = tokens;
     a.stream = static_cast<hipStream_t>(stream);
     return fp4q::launch_kv_write(a) == hipSuccess ? FP4Q_OK : FP4Q_E_HIP;
+}
+
+fp4q_status fp4q_kv_append(const fp4q_spec* spec, const fp4q_kv_cache* cache, const fp4q_append* c, void* stream)
+{
+    fp4q::KvAppendArgs a{};
+    fp4q_status st = check_spec(spec);
+    if (st != FP4Q_OK || (st = check_write_spec(spec)) != FP4Q_OK || (st = check_cache(spec, cache, a.kv)) != FP4Q_OK)
+        return st;
+    if (!c)
+        return FP4Q_E_NULL;
+    if (!valid_dtype(c->dtype) || (c->interleaved != 0 && c->interleaved != 1) || c->reserved != 0)
+        return FP4Q_E_ARG;
+    // a norm divides by what it finds: eps keeps a row of zeros from 1 / 0
+    if ((c->q_weight || c->k_weight) && !(std::isfinite(c->eps) && c->eps > 0.0f))
+        return FP4Q_E_ARG;
+    if (c->tokens < 0 || c->q_heads < 0 || c->rope_dim < 0 || c->rope_dim > cache->head_dim || c->rope_dim % 16 != 0 ||
+        (c->rope_dim != 0 && (c->rope_rows < 0 || c->rope_stride < 0 || c->rope_stride > kMostStride)))
+        return FP4Q_E_SHAPE;
+    const int64_t rows[4] = {c->q_row_stride, c->out_row_stride, c->k_token_stride, c->v_token_stride};
+    const int64_t heads[4] = {c->q_head_stride, c->out_head_stride, c->k_head_stride, c->v_head_stride};
+    for (int i = c->q_heads == 0 ? 2 : 0; i < 4; ++i) {
+        const int n = i < 2 ? c->q_heads : cache->kv_heads;
+        if (!stride_ok(rows[i]) || !stride_ok(heads[i]) || (rows[i] != 0 && c->tokens > (INT64_MAX >> 4) / rows[i]) ||
+            (heads[i] != 0 && n > (INT64_MAX >> 4) / heads[i]))
+            return FP4Q_E_SHAPE;
+    }
+    const int64_t wide = c->q_heads > cache->kv_heads ? c->q_heads : cache->kv_heads;
+    if (c->tokens > (INT64_MAX >> 4) / (wide * cache->head_dim) || wide > ((int64_t)1 << 31) / (cache->head_dim / 8))
+        return FP4Q_E_SHAPE;
+    if (c->rope_dim != 0 && c->rope_stride != 0 && c->rope_rows > (INT64_MAX >> 4) / c->rope_stride)
+        return FP4Q_E_SHAPE;
+    if (c->tokens != 0 && (!c->k || !c->v || !c->slots || (c->q_heads != 0 && (!c->q || !c->q_out)) ||
+                           (c->rope_dim != 0 && (!c->positions || (c->rope_rows != 0 && !c->rope)))))
+        return FP4Q_E_NULL;
+    if (!rows_aligned(c->k, c->k_token_stride, c->k_head_stride, c->dtype) ||
+        !rows_aligned(c->v, c->v_token_stride, c->v_head_stride, c->dtype) || !aligned(c->slots, 8) ||
+        !aligned(c->q_weight, 16) || !aligned(c->k_weight, 16))
+        return FP4Q_E_ALIGN;
+    if (c->q_heads != 0 && (!rows_aligned(c->q, c->q_row_stride, c->q_head_stride, c->dtype) ||
+                            !rows_aligned(c->q_out, c->out_row_stride, c->out_head_stride, c->dtype)))
+        return FP4Q_E_ALIGN;
+    if (c->rope_dim != 0 && (!aligned(c->rope, 16) || c->rope_stride % 4 != 0 || !aligned(c->positions, 8)))
+        return FP4Q_E_ALIGN;
+    if (!writable(spec, cache))
+        return FP4Q_E_SHAPE;
+    if (c->tokens != 0 && c->q_heads != 0 &&
+        !rows_apart<2>({c->tokens, c->q_heads}, {c->out_row_stride, c->out_head_stride}, cache->head_dim))
+        return FP4Q_E_SHAPE;
+    if (c->tokens == 0)
+        return FP4Q_OK;
+    a.rule = spec->scale_rule;
+    a.lo = spec->sweep_lo;
+    a.hi = spec->sweep_hi;
+    a.rotate = spec->rotate;
+    a.bf16 = c->dtype == FP4Q_BF16;
+    a.interleaved = c->interleaved != 0;
+    a.q = c->q;
+    a.q_row = c->q_row_stride;
+    a.q_head = c->q_head_stride;
+    a.q_out = c->q_out;
+    a.out_row = c->out_row_stride;
+    a.out_head = c->out_head_stride;
+    a.x[0] = c->k;
+    a.x[1] = c->v;
+    a.x_token[0] = c->k_token_stride;
+    a.x_token[1] = c->v_token_stride;
+    a.x_head[0] = c->k_head_stride;
+    a.x_head[1] = c->v_head_stride;
+    a.q_weight = c->q_weight;
+    a.k_weight = c->k_weight;
+    a.rope = c->rope;
+    a.rope_row = c->rope_stride;
+    a.rope_rows = c->rope_rows;
+    a.positions = c->positions;
+    a.slots = c->slots;
+    a.tokens = c->tokens;
+    a.q_heads = c->q_heads;
+    a.turned = c->rope_dim;
+    a.eps = c->eps;
+    a.stream = static_cast<hipStream_t>(stream);
+    return fp4q::launch_kv_append(a) == hipSuccess ? FP4Q_OK : FP4Q_E_HIP;
 }
 
 fp4q_status fp4q_kv_read(const fp4q_spec* spec, const fp4q_kv_cache* cache, const int64_t* slots,

@@ -40,6 +40,35 @@ struct KvReadArgs {
     hipStream_t stream;
 };
 
+struct KvAppendArgs {
+    KvView kv;
+    int rule, lo, hi, rotate;
+    bool bf16, interleaved;
+    const void* q; // null where q_heads == 0
+    int64_t q_row, q_head; // strides in elements
+    void* q_out;
+    int64_t out_row, out_head;
+    const void* x[2]; // K, V
+    int64_t x_token[2], x_head[2];
+    const float* q_weight; // [head_dim], null: no norm
+    const float* k_weight;
+    const float* rope; // [rope_rows, turned]: cosines, then sines
+    int64_t rope_row, rope_rows;
+    const int64_t* positions;
+    const int64_t* slots;
+    int64_t tokens;
+    int q_heads, turned; // turned: values of a head that the positions turn
+    float eps;
+    hipStream_t stream;
+};
+
+// How one launch is shared out: workgroups of K, as many of V, then q's.
+struct AppendPlan {
+    uint32_t kv_groups, q_groups; // workgroups
+    uint32_t kv_items, q_items;   // lanes with work
+    int lane_shift;               // log2 of the lanes of a row
+};
+
 struct AttendArgs {
     KvView kv;
     int rotate;
@@ -87,6 +116,7 @@ inline int64_t attend_span(const AttendArgs& a)
 AttendPlan plan_attend(const AttendArgs& a);
 
 hipError_t launch_kv_write(const KvWriteArgs& a);
+hipError_t launch_kv_append(const KvAppendArgs& a);
 hipError_t launch_kv_read(const KvReadArgs& a);
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p);
 

@@ -317,6 +317,58 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                           const int64_t* slots, void* stream);
 
+/* New tokens' rows as a projection leaves them: the norm of each head of q and k,
+ * the rotary positions, and the write of k and v into the cache, in one launch.
+ *   norm     r = fl32(1 / sqrt(mean_i x_i^2 + eps)) over the head_dim values of
+ *            a row, taken in binary64; y_i = fl32(fl32(x_i r) w_i).
+ *   turn     the first rope_dim values of each row of q and k, in pairs
+ *            (a, b) -> (fl32(fl32(a c) - fl32(b s)), fl32(fl32(b c) + fl32(a s))),
+ *            c and s from the row of the table that the token's position names.
+ *            Pair i is the values i and i + rope_dim / 2, or with `interleaved`
+ *            2i and 2i + 1.
+ *   q        rounded to its type into q_out; k, after this, and v are written
+ *            as fp4q_kv_write writes rows of these binary32 values.
+ * Members of the call:
+ *   q, q_out [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim] of
+ *            `dtype`, strides and alignment as for fp4q_kv_write; the rows of q_out
+ *            share no element.  q_out may be q, with the same strides.  q_heads 0:
+ *            no q (its members are ignored).
+ *   q_weight, k_weight  fp32 [head_dim], 16-byte aligned; NULL: no norm of these
+ *            rows.  eps is positive where one is given.
+ *   rope     fp32 [rope_rows, rope_dim], row stride in elements (a multiple of
+ *            4), 16-byte aligned: rope_dim / 2 cosines, then as many sines.
+ *            Any scaling of positions, frequencies or magnitudes is in the table.
+ *   rope_dim a multiple of 16, at most head_dim; 0: nothing is turned, and rope
+ *            and positions are ignored.
+ *   positions int64 [tokens] on the device.  A token whose position has no row in
+ *            the table gives NaN in q_out and is not written.
+ *   slots    as for fp4q_kv_write; a token that is skipped still has its q. */
+typedef struct {
+    const void* q;
+    int64_t q_row_stride, q_head_stride;
+    void* q_out;
+    int64_t out_row_stride, out_head_stride;
+    const void* k;
+    int64_t k_token_stride, k_head_stride;
+    const void* v;
+    int64_t v_token_stride, v_head_stride;
+    const float* q_weight;
+    const float* k_weight;
+    const float* rope;
+    int64_t rope_stride, rope_rows;
+    const int64_t* positions;
+    const int64_t* slots;
+    int64_t tokens;
+    int32_t q_heads;
+    int32_t rope_dim;
+    int32_t interleaved;
+    int32_t dtype;
+    float eps;
+    int32_t reserved; /* 0 */
+} fp4q_append;
+
+fp4q_status fp4q_kv_append(const fp4q_spec* spec, const fp4q_kv_cache* cache, const fp4q_append* call, void* stream);
+
 /* Dequantize the rows of `tokens` slots into k and v, each contiguous
  * [tokens, kv_heads, head_dim] of `dtype` (16-byte aligned), un-rotated when
  * spec->rotate is set: the values fp4q_dequantize gives.  A slot out of range

@@ -83,7 +83,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t* p, in
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
 }
 
-constexpr int kPast = 0x7FFFFFFF; // an offset past every buffer's end
+// OR-ed to an offset, past every buffer's end (a select would become a branch
+// around the load)
+constexpr int kPast = 0x7FFFFFFF;
+
+// the scale bytes of 32 values of a row from value k on, as scales_of takes them;
+// `past` as above.  NVFP4: of two blocks; a row may end after the first, and the
+// second's scale is then zero.
+template <bool MX>
+__device__ __forceinline__ uint32_t load_scales(__amdgpu_buffer_rsrc_t scales, int at, int k, int cols, int past)
+{
+    const uint32_t lo = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, at | past, 0, 0);
+    if constexpr (MX)
+        return lo;
+    const uint32_t hi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, (at + 1) | (k + 16 < cols ? past : kPast), 0, 0);
+    return lo | (hi << 8);
+}
 
 // ---- activations ------------------------------------------------------------------
 
@@ -167,10 +182,11 @@ __device__ __forceinline__ f32x4 finish4(const MatmulArgs& a, const f32x4* sum)
 }
 
 // partial sums of split s: [weight][m][n, padded to four]
-__device__ __forceinline__ f32x4* partial_of(const MatmulArgs& a, int s, int w, int64_t m, int64_t n)
+__device__ __forceinline__ f32x4* partial_of(const MatmulArgs& a, const MatmulPlan& p, int s, int w, int64_t m, int64_t n)
 {
     const int64_t wide = (a.n + 3) & ~(int64_t)3;
-    return reinterpret_cast<f32x4*>(static_cast<float*>(a.workspace) + (((int64_t)s * a.weights + w) * a.m + m) * wide + n);
+    float* sums = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partials);
+    return reinterpret_cast<f32x4*>(sums + (((int64_t)s * a.weights + w) * a.m + m) * wide + n);
 }
 
 // ---- few rows of x ------------------------------------------------------------------
@@ -220,26 +236,16 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
         codes[w] = buffer_of(a.codes[w] + first * crow, live * crow);
         scales[w] = buffer_of(a.scales[w] + first * srow, live * srow);
     }
-    const bool pairs = (a.k & 31) == 0 && ((reinterpret_cast<uintptr_t>(a.scales[0]) | reinterpret_cast<uintptr_t>(a.scales[NW - 1])) & 1) == 0;
     auto load = [&](int step, Codes<MX, RT * NW>& t) {
         const int k = step * kStepK + 32 * g;
-        const bool in = step < s1 && k < (int)a.k;
+        const int past = step < s1 && k < (int)a.k ? 0 : kPast;
 #pragma unroll
         for (int w = 0; w < NW; ++w)
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
                 const int row = 16 * i + r;
-                t.c[w * RT + i] = __builtin_amdgcn_raw_buffer_load_b128(codes[w], in ? row * crow + k / 2 : kPast, 0, 0);
-                const int so = in ? row * srow + k / B : kPast;
-                if constexpr (MX) {
-                    t.s[w * RT + i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], so, 0, 0);
-                } else if (pairs) {
-                    t.s[w * RT + i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales[w], so, 0, 0);
-                } else { // a row may end after the first of two blocks: the second's scale is then zero
-                    const uint32_t lo = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], so, 0, 0);
-                    const uint32_t hi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], in && k + 16 < (int)a.k ? so + 1 : kPast, 0, 0);
-                    t.s[w * RT + i] = lo | (hi << 8);
-                }
+                t.c[w * RT + i] = __builtin_amdgcn_raw_buffer_load_b128(codes[w], (row * crow + k / 2) | past, 0, 0);
+                t.s[w * RT + i] = load_scales<MX>(scales[w], row * srow + k / B, k, (int)a.k, past);
             }
     };
 
@@ -383,7 +389,193 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
         } else {
 #pragma unroll
             for (int w = 0; w < NW; ++w)
-                *partial_of(a, split, w, m, n) = sum[w];
+                *partial_of(a, p, split, w, m, n) = sum[w];
+        }
+    }
+}
+
+// ---- many rows of x -------------------------------------------------------------------
+//
+// A workgroup of WN waves takes 16 TM rows of x and 64 WN of the weight (32 WN of each
+// of two).  The x of a step, 128 values of each row, lies in LDS, double buffered,
+// loaded there directly; every wave reads all of it and multiplies it by its own 64
+// rows of the weight, which it loads and expands itself, so that no code is expanded
+// twice in a workgroup and no expanded weight passes through LDS.  16-byte units
+// of a row of x are exchanged by an XOR with the row: 16 lanes that read one unit
+// of 16 rows meet all banks, and a lane loads the unit that belongs at its place.
+//   Rows of the weight: row r of the 16-row tile t is row 16 (r / 4) + 4 t + r % 4 of the
+// wave's, so that a lane ends with 16 neighbouring columns of y (two weights: tiles 0 and
+// 1 are the first's, with 8).
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of_x(const void* p, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
+}
+
+template <bool MX, int NW, int TM, int WN>
+__global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
+{
+    constexpr int B = MX ? 32 : 16;
+    constexpr int BM = 16 * TM;
+    constexpr int BN = 64 * WN / NW; // columns of y
+    constexpr int WC = 64 / NW;      // of a wave
+    constexpr int TN = 4;
+    constexpr int U = kStepK / 8;    // 16-byte units of a row of x
+    __shared__ u32x4 xbuf[2][BM * U];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
+
+    // workgroups of one XCD (every eighth) take neighbouring tiles: kGroup rows of tiles at a
+    // time, the rows of tiles fastest
+    const uint32_t tiles_m = (uint32_t)((a.m + BM - 1) / BM), tiles_n = (uint32_t)((a.n + BN - 1) / BN);
+    const uint32_t all = tiles_m * tiles_n;
+    uint32_t id = blockIdx.x;
+    {
+        const uint32_t xcd = id % 8, per = all / 8, more = all % 8;
+        id = xcd * per + (xcd < more ? xcd : more) + id / 8;
+    }
+    constexpr uint32_t kGroup = 8;
+    const uint32_t band = id / (kGroup * tiles_n), first = band * kGroup;
+    const uint32_t high = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+    const uint32_t in = id - band * kGroup * tiles_n;
+    const int64_t m0 = (int64_t)(first + in % high) * BM, n0 = (int64_t)(in / high) * BN;
+
+    const int steps = (int)((a.k + kStepK - 1) / kStepK);
+    const int s0 = (int)blockIdx.z * p.split_steps;
+    const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
+    const int turns = (s1 - s0) * p.parts; // a step for each part of x, the small ones first
+
+    // x, or its parts: plane q, row m
+    const int64_t m_left = a.m - m0;
+    const int rows = (int)(m_left < BM ? m_left : BM);
+    const int x_row = (int)(p.parts == 1 ? a.x_row : a.k) * 2; // bytes
+    const char* x = p.parts == 1 ? static_cast<const char*>(a.x) : static_cast<const char*>(a.workspace);
+    const int64_t plane = a.m * a.k * 2;
+    auto load_x_tile = [&](int turn, int to) {
+        const int q = p.parts == 1 ? 0 : p.parts - 1 - turn % p.parts, step = s0 + (p.parts == 1 ? turn : turn / p.parts);
+        const auto src = buffer_of_x(x + q * plane + m0 * x_row, (int64_t)(rows - 1) * x_row + a.k * 2);
+#pragma unroll
+        for (int i = 0; i < BM / (4 * WN); ++i) {
+            const int row = (wave * (BM / (4 * WN)) + i) * 4 + g;
+            const int k = step * kStepK + ((r ^ (row & 15)) * 8);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(&xbuf[to][(wave * (BM / (4 * WN)) + i) * 64]), 16,
+                                                     (row * x_row + k * 2) | (k < (int)a.k ? 0 : kPast), 0, 0, 0);
+        }
+    };
+
+    // the wave's rows of each weight
+    const int64_t nw = n0 + wave * WC;
+    const int64_t left = a.n - nw;
+    const int live = left <= 0 ? 0 : (int)(left < WC ? left : WC);
+    const int crow = (int)(a.k / 2), srow = (int)(a.k / B);
+    __amdgpu_buffer_rsrc_t codes[NW], scales[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const int64_t from = live > 0 ? nw : 0;
+        codes[w] = buffer_of(a.codes[w] + from * crow, live * crow);
+        scales[w] = buffer_of(a.scales[w] + from * srow, live * srow);
+    }
+    auto load_w = [&](int turn, Codes<MX, TN>& t) {
+        const int step = s0 + (p.parts == 1 ? turn : turn / p.parts);
+        const int k = step * kStepK + 32 * g;
+        const int past = turn < turns && k < (int)a.k ? 0 : kPast;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const int w = NW == 2 ? i >> 1 : 0;
+            const int row = (16 / NW) * (r >> 2) + 4 * (NW == 2 ? i & 1 : i) + (r & 3);
+            t.c[i] = __builtin_amdgcn_raw_buffer_load_b128(codes[w], (row * crow + k / 2) | past, 0, 0);
+            t.s[i] = load_scales<MX>(scales[w], row * srow + k / B, k, (int)a.k, past);
+        }
+    };
+
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    Codes<MX, TN> now, next;
+    if (turns > 0) {
+        load_x_tile(0, 0);
+        load_w(0, now);
+    }
+    for (int turn = 0; turn < turns; ++turn) {
+        const int at = turn & 1;
+        __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0): this wave's part of the step's x has arrived
+        __syncthreads();                    // everybody's has, and the other buffer is free
+        if (turn + 1 < turns)
+            load_x_tile(turn + 1, at ^ 1);
+        load_w(turn + 1, next);
+        Scales sc[TN];
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+            sc[i] = scales_of<MX>(now.s[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u32x4 wv[TN];
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                wv[i] = expand<MX>(now.c[i][j], j < 2 ? sc[i].lo : sc[i].hi);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const u32x4 xv = xbuf[at][(16 * i + r) * U + ((4 * g + j) ^ r)];
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+                    acc[i][t] = mfma16(wv[t], xv, acc[i][t]);
+            }
+        }
+        now = next;
+    }
+
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t m = m0 + 16 * i + r;
+        if (m >= a.m)
+            continue;
+#pragma unroll
+        for (int t = 0; t < TN / NW; ++t) {
+            const int64_t n = nw + (16 / NW) * g + 4 * t;
+            if (n >= a.n)
+                continue;
+            f32x4 sum[NW];
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                sum[w] = acc[i][w * (TN / NW) + t];
+            if (p.splits == 1) {
+                store4(a, m, n, finish4<MX, NW>(a, sum));
+            } else {
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+                    *partial_of(a, p, (int)blockIdx.z, w, m, n) = sum[w];
+            }
+        }
+    }
+}
+
+// the parts of x, rotated: [part][m][k] bf16 in the workspace, a block of values a thread
+template <int B, int PARTS>
+__global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
+{
+    const int64_t blocks = a.k / B, all = a.m * blocks, plane = a.m * a.k;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
+        const int64_t row = u / blocks, b = u - row * blocks;
+        float v[B];
+        load_x<B, PARTS == 2>(a.x, row * a.x_row + b * B, v);
+        if (PARTS == 2 || a.rotate)
+            fwht<B>(v);
+        uint16_t* to = static_cast<uint16_t*>(a.workspace) + u * B;
+#pragma unroll
+        for (int i = 0; i < B / 8; ++i) {
+            uint32_t h[8][PARTS];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                parts_of<PARTS>(v[8 * i + j], h[j]);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                *reinterpret_cast<u32x4*>(to + q * plane + 8 * i) =
+                    u32x4{h[0][q] >> 16 | h[1][q], h[2][q] >> 16 | h[3][q], h[4][q] >> 16 | h[5][q], h[6][q] >> 16 | h[7][q]};
         }
     }
 }
@@ -400,12 +592,12 @@ __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const Mat
     for (int w = 0; w < NW; ++w) {
         sum[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < p.splits; ++s)
-            sum[w] += *partial_of(a, s, w, m, n);
+            sum[w] += *partial_of(a, p, s, w, m, n);
     }
     store4(a, m, n, finish4<MX, NW>(a, sum));
 }
 
-enum { kFew1 = 0, kFew16 = 1, kFew32 = 2, kFew64 = 3 };
+enum { kFew1 = 0, kFew16 = 1, kFew32 = 2, kFew64 = 3, kMany = 4 };
 
 int parts_for(const MatmulArgs& a) { return !a.bf16 ? 3 : (a.rotate ? 2 : 1); }
 
@@ -426,11 +618,25 @@ void launch_few(const MatmulArgs& a, const MatmulPlan& p, dim3 grid)
 template <bool MX, int NW>
 hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
 {
-    const dim3 grid((uint32_t)((a.n + p.rows - 1) / p.rows), (uint32_t)((a.m + p.tokens - 1) / p.tokens), (uint32_t)p.splits);
-    switch (parts_for(a)) {
-    case 1: launch_few<MX, NW, 1>(a, p, grid); break;
-    case 2: launch_few<MX, NW, 2>(a, p, grid); break;
-    default: launch_few<MX, NW, 3>(a, p, grid); break;
+    const uint32_t tiles_n = (uint32_t)((a.n + p.rows - 1) / p.rows), tiles_m = (uint32_t)((a.m + p.tokens - 1) / p.tokens);
+    if (p.form == kMany) {
+        if (p.parts > 1) {
+            constexpr int B = MX ? 32 : 16;
+            const int64_t all = (a.m * (a.k / B) + 255) / 256;
+            const dim3 cover((uint32_t)(all < 65536 ? all : 65536));
+            if (p.parts == 2)
+                matmul_parts<B, 2><<<cover, 256, 0, a.stream>>>(a);
+            else
+                matmul_parts<B, 3><<<cover, 256, 0, a.stream>>>(a);
+        }
+        matmul_many<MX, NW, 8, 4><<<dim3(tiles_n * tiles_m, 1, (uint32_t)p.splits), 256, 0, a.stream>>>(a, p);
+    } else {
+        const dim3 grid(tiles_n, tiles_m, (uint32_t)p.splits);
+        switch (p.parts) {
+        case 1: launch_few<MX, NW, 1>(a, p, grid); break;
+        case 2: launch_few<MX, NW, 2>(a, p, grid); break;
+        default: launch_few<MX, NW, 3>(a, p, grid); break;
+        }
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
@@ -445,7 +651,21 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
 MatmulPlan plan_matmul(const MatmulArgs& a)
 {
     MatmulPlan p{};
-    const int parts = parts_for(a);
+    const int parts = p.parts = parts_for(a);
+    const int64_t steps = (a.k + kStepK - 1) / kStepK;
+    p.splits = 1;
+    p.split_steps = (int)steps;
+    if (a.m > 64 && a.k < ((int64_t)1 << 22) && a.x_row < ((int64_t)1 << 22)) {
+        p.form = kMany;
+        p.rows = 256 / a.weights;
+        p.tokens = 128;
+        p.partials = parts == 1 ? 0 : (size_t)parts * a.m * a.k * 2;
+        p.partials = (p.partials + 255) & ~(size_t)255;
+        p.workspace = p.partials;
+        const int64_t tiles_n = (a.n + p.rows - 1) / p.rows, tiles_m = (a.m + p.tokens - 1) / p.tokens;
+        p.refused = tiles_n > 0x7FFFFF / tiles_m;
+        return p;
+    }
     int kw, rt, mt, rw;
     if (a.m <= 4) {
         p.form = kFew1, rt = 1, rw = 1, kw = 8, mt = 1;
@@ -458,11 +678,8 @@ MatmulPlan plan_matmul(const MatmulArgs& a)
     }
     p.rows = 16 * rt * rw;
     p.tokens = 16 * mt;
-    p.splits = 1;
-    const int steps = (int)((a.k + kStepK - 1) / kStepK);
-    p.split_steps = steps;
     const int rows = (int)(a.m < p.tokens ? a.m : p.tokens);
-    const int whole = (steps + kw - 1) / kw * kw; // steps, filled up to the waves' number
+    const int whole = (int)(steps + kw - 1) / kw * kw; // steps, filled up to the waves' number
     p.chunk_steps = whole;
     while (p.chunk_steps > kw && (size_t)rows * parts * (p.chunk_steps * 256 + 16) > 56 * 1024)
         p.chunk_steps = (p.chunk_steps / 2 + kw - 1) / kw * kw;

@@ -33,6 +33,7 @@ constexpr int kStepK = 128; // values of the long axis in one step of a wave
 // How one call is cut into workgroups, from its sizes and types alone.
 struct MatmulPlan {
     int form;        // which instance of the kernel
+    int parts;       // bf16 parts of x
     int rows;        // weight rows of a workgroup
     int tokens;      // rows of x of a workgroup
     int splits;      // workgroups that share a tile's long axis
@@ -40,7 +41,8 @@ struct MatmulPlan {
     int chunk_steps; // steps whose x is held in LDS at once
     size_t lds;
     bool refused;    // more workgroups than a launch holds
-    size_t workspace; // bytes of partial sums (0 where splits == 1)
+    size_t partials;  // where the partial sums begin in the workspace, behind the parts of x
+    size_t workspace; // bytes
 };
 
 MatmulPlan plan_matmul(const MatmulArgs& a);

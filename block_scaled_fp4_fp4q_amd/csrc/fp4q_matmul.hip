@@ -64,14 +64,21 @@ struct Scales {
     float lo, hi;
 };
 
+// as loaded; the two of NVFP4 are put together where they are used, so that nothing
+// waits for them before
 template <bool MX>
-__device__ __forceinline__ Scales scales_of(uint32_t bytes)
+struct Bytes {
+    uint32_t b[MX ? 1 : 2];
+};
+
+template <bool MX>
+__device__ __forceinline__ Scales scales_of(const Bytes<MX>& s)
 {
     if constexpr (MX) {
-        const float s = __uint_as_float(bytes << 23);
-        return Scales{s, s};
+        const float x = __uint_as_float(s.b[0] << 23);
+        return Scales{x, x};
     } else {
-        const auto t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(bytes, 1.0f, false);
+        const auto t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(s.b[0] | (s.b[1] << 8), 1.0f, false);
         return Scales{t[0], t[1]};
     }
 }
@@ -91,13 +98,13 @@ constexpr int kPast = 0x7FFFFFFF;
 // `past` as above.  NVFP4: of two blocks; a row may end after the first, and the
 // second's scale is then zero.
 template <bool MX>
-__device__ __forceinline__ uint32_t load_scales(__amdgpu_buffer_rsrc_t scales, int at, int k, int cols, int past)
+__device__ __forceinline__ Bytes<MX> load_scales(__amdgpu_buffer_rsrc_t scales, int at, int k, int cols, int past)
 {
-    const uint32_t lo = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, at | past, 0, 0);
-    if constexpr (MX)
-        return lo;
-    const uint32_t hi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, (at + 1) | (k + 16 < cols ? past : kPast), 0, 0);
-    return lo | (hi << 8);
+    Bytes<MX> r;
+    r.b[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, at | past, 0, 0);
+    if constexpr (!MX)
+        r.b[1] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, (at + 1) | (k + 16 < cols ? past : kPast), 0, 0);
+    return r;
 }
 
 // ---- activations ------------------------------------------------------------------
@@ -203,7 +210,7 @@ constexpr int kAhead = 4;
 template <bool MX, int RT>
 struct Codes {
     u32x4 c[RT];
-    uint32_t s[RT];
+    Bytes<MX> s[RT];
 };
 
 template <bool MX, int NW, int PARTS, int RT, int RW, int KW, int MT>
@@ -394,37 +401,76 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     }
 }
 
+constexpr int kReadAhead = 2; // reads of x from LDS before their products
+
 // ---- many rows of x -------------------------------------------------------------------
 //
-// A workgroup of WN waves takes 16 TM rows of x and 64 WN of the weight (32 WN of each
-// of two).  The x of a step, 128 values of each row, lies in LDS, double buffered,
-// loaded there directly; every wave reads all of it and multiplies it by its own 64
-// rows of the weight, which it loads and expands itself, so that no code is expanded
-// twice in a workgroup and no expanded weight passes through LDS.  16-byte units
-// of a row of x are exchanged by an XOR with the row: 16 lanes that read one unit
-// of 16 rows meet all banks, and a lane loads the unit that belongs at its place.
-//   Rows of the weight: row r of the 16-row tile t is row 16 (r / 4) + 4 t + r % 4 of the
-// wave's, so that a lane ends with 16 neighbouring columns of y (two weights: tiles 0 and
-// 1 are the first's, with 8).
+// A workgroup of WN waves takes 32 TM rows of x and 64 WN of the weight (32 WN of each
+// of two), in 32x32x16 products.  The x of a step, 128 values of each row, lies in LDS,
+// double buffered, loaded there directly; every wave reads all of it and multiplies it
+// by its own 64 rows of the weight, which it loads and expands itself, so that no code
+// is expanded twice in a workgroup and no expanded weight passes through LDS.
+//   Lane n + 32 h holds, of a row, the values 64 h .. 64 h + 63 of a step, eight for each
+// product: W's come as 32 bytes of codes.  16-byte units of a row of x are exchanged in LDS by
+// an XOR with the row, so that 16 lanes that read one unit of 16 rows meet all banks; a
+// lane loads the unit that belongs at its place.
+//   Row 8 q + 4 h + e of a product's 32 rows of W is column 16 h + 4 q + e of y, so that a
+// lane ends with 16 neighbouring columns.
+//   While the products of eight values run, the weights of the next eight are expanded; the
+// last ones' are those of the next step.
 typedef __attribute__((address_space(3))) void lds_void;
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
+}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of_x(const void* p, int64_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
 }
 
+// 64 values of a row of the weight: codes, and scale bytes as they came, in one load or in
+// one each (put together where they are used, so that nothing waits for them before)
+template <bool MX>
+struct Wide {
+    static constexpr int NS = MX ? 2 : 4;
+    u32x4 c[2];
+    uint32_t s[NS];
+};
+
+template <bool MX>
+__device__ __forceinline__ uint32_t scale_word(const Wide<MX>& w)
+{
+    if constexpr (MX)
+        return w.s[0] | (w.s[1] << 8);
+    else
+        return w.s[0] | (w.s[1] << 8) | (w.s[2] << 16) | (w.s[3] << 24);
+}
+
+// the factor of values 8 j .. 8 j + 7 of 64
+template <bool MX>
+__device__ __forceinline__ float factor_of(uint32_t word, int j)
+{
+    if constexpr (MX)
+        return __uint_as_float((j < 4 ? word & 0xFFu : word >> 8) << 23);
+    const auto t = j < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, false)
+                         : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, true);
+    return t[(j >> 1) & 1];
+}
+
 template <bool MX, int NW, int TM, int WN>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
     constexpr int B = MX ? 32 : 16;
-    constexpr int BM = 16 * TM;
+    constexpr int BM = 32 * TM;
     constexpr int BN = 64 * WN / NW; // columns of y
     constexpr int WC = 64 / NW;      // of a wave
-    constexpr int TN = 4;
     constexpr int U = kStepK / 8;    // 16-byte units of a row of x
     __shared__ u32x4 xbuf[2][BM * U];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int r = lane & 15, g = lane >> 4;
+    const int n = lane & 31, h = lane >> 5;
 
     // workgroups of one XCD (every eighth) take neighbouring tiles: kGroup rows of tiles at a
     // time, the rows of tiles fastest
@@ -441,116 +487,189 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     const uint32_t in = id - band * kGroup * tiles_n;
     const int64_t m0 = (int64_t)(first + in % high) * BM, n0 = (int64_t)(in / high) * BN;
 
-    const int steps = (int)((a.k + kStepK - 1) / kStepK);
+    const int cols = (int)a.k;
+    const int steps = (cols + kStepK - 1) / kStepK;
     const int s0 = (int)blockIdx.z * p.split_steps;
     const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
     const int turns = (s1 - s0) * p.parts; // a step for each part of x, the small ones first
+    // Offsets are a lane's own (in a vector register) and a uniform part that never passes
+    // the buffer's end, where the check against it would wrap: rows of a tile that do not
+    // exist are replaced by others, whose results are not stored.
 
     // x, or its parts: plane q, row m
     const int64_t m_left = a.m - m0;
     const int rows = (int)(m_left < BM ? m_left : BM);
     const int x_row = (int)(p.parts == 1 ? a.x_row : a.k) * 2; // bytes
-    const char* x = p.parts == 1 ? static_cast<const char*>(a.x) : static_cast<const char*>(a.workspace);
+    const char* x = (p.parts == 1 ? static_cast<const char*>(a.x) : static_cast<const char*>(a.workspace)) + m0 * x_row;
     const int64_t plane = a.m * a.k * 2;
-    auto load_x_tile = [&](int turn, int to) {
-        const int q = p.parts == 1 ? 0 : p.parts - 1 - turn % p.parts, step = s0 + (p.parts == 1 ? turn : turn / p.parts);
-        const auto src = buffer_of_x(x + q * plane + m0 * x_row, (int64_t)(rows - 1) * x_row + a.k * 2);
+    constexpr int LOADS = BM / (4 * WN); // of a wave: four rows each
+    static_assert(LOADS % 4 == 0, "the exchange of units repeats every four loads");
+    const int quad = lane >> 4; // row of the four
+    int x_unit[4];
 #pragma unroll
-        for (int i = 0; i < BM / (4 * WN); ++i) {
-            const int row = (wave * (BM / (4 * WN)) + i) * 4 + g;
-            const int k = step * kStepK + ((r ^ (row & 15)) * 8);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(&xbuf[to][(wave * (BM / (4 * WN)) + i) * 64]), 16,
-                                                     (row * x_row + k * 2) | (k < (int)a.k ? 0 : kPast), 0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+        x_unit[i] = (lane & 15) ^ (4 * i + quad);
+    auto load_x_tile = [&](int step, int part, int to) {
+        const auto src = buffer_of_x(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
+        const bool whole = (step + 1) * kStepK <= cols;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = (wave * LOADS + i) * 4;
+            int at = quad * x_row + x_unit[i % 4] * 16;
+            if (!whole) // values past the row's end are zeros
+                at |= step * kStepK + x_unit[i % 4] * 8 < cols ? 0 : kPast;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(&xbuf[to][(wave * LOADS + i) * 64]), 16, at,
+                                                     __builtin_amdgcn_readfirstlane((row < rows ? row : 0) * x_row + step * (kStepK * 2)), 0, 0);
         }
     };
 
-    // the wave's rows of each weight
+    // the wave's rows of each weight, 32 for a product
     const int64_t nw = n0 + wave * WC;
     const int64_t left = a.n - nw;
-    const int live = left <= 0 ? 0 : (int)(left < WC ? left : WC);
-    const int crow = (int)(a.k / 2), srow = (int)(a.k / B);
+    const int64_t from = left > 0 ? nw : 0;
+    const int live = (int)(left <= 0 ? 1 : (left < WC ? left : WC));
+    const int crow = cols / 2, srow = cols / B;
     __amdgpu_buffer_rsrc_t codes[NW], scales[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const int64_t from = live > 0 ? nw : 0;
         codes[w] = buffer_of(a.codes[w] + from * crow, live * crow);
         scales[w] = buffer_of(a.scales[w] + from * srow, live * srow);
     }
-    auto load_w = [&](int turn, Codes<MX, TN>& t) {
-        const int step = s0 + (p.parts == 1 ? turn : turn / p.parts);
-        const int k = step * kStepK + 32 * g;
-        const int past = turn < turns && k < (int)a.k ? 0 : kPast;
+    const int w_row = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
+    const int c_at = w_row * crow + 32 * h, s_at = w_row * srow + 64 * h / B;
+    constexpr int SB = 64 / B; // scale bytes of 64 values, in one load where they lie so
+    const bool one = (cols & 63) == 0 &&
+                     ((reinterpret_cast<uintptr_t>(a.scales[0]) | reinterpret_cast<uintptr_t>(a.scales[NW - 1])) & (SB - 1)) == 0;
+    auto load_w = [&](int step, Wide<MX> (&t)[2]) {
+        const int k = step * kStepK + 64 * h;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            const int w = NW == 2 ? i >> 1 : 0;
-            const int row = (16 / NW) * (r >> 2) + 4 * (NW == 2 ? i & 1 : i) + (r & 3);
-            t.c[i] = __builtin_amdgcn_raw_buffer_load_b128(codes[w], (row * crow + k / 2) | past, 0, 0);
-            t.s[i] = load_scales<MX>(scales[w], row * srow + k / B, k, (int)a.k, past);
+        for (int i = 0; i < 2; ++i) {
+            const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) // past the row's end: any codes, with scales of zero
+                t[i].c[c] = __builtin_amdgcn_raw_buffer_load_b128(codes[w], (c_at + 16 * c) | (k + 32 * c < cols ? 0 : kPast),
+                                                                  __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2)), 0);
+        }
+        if (one) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
+                const int at = s_at | (k < cols ? 0 : kPast);
+                const int to = __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B));
+                t[i].s[0] = MX ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales[w], at, to, 0)
+                               : __builtin_amdgcn_raw_buffer_load_b32(scales[w], at, to, 0);
+#pragma unroll
+                for (int q = 1; q < SB; ++q)
+                    t[i].s[q] = 0u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
+#pragma unroll
+                for (int q = 0; q < SB; ++q)
+                    t[i].s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], (s_at + q) | (k + q * B < cols ? 0 : kPast),
+                                                                             __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B)), 0);
+            }
         }
     };
 
-    f32x4 acc[TM][TN];
+    f32x16 acc[TM][2];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[i][j][e] = 0.0f;
 
-    Codes<MX, TN> now, next;
+    Wide<MX> now[2], next[2];
+    u32x4 wv[2][2];
+    uint32_t word[2];
+    auto expand_tile = [&](const Wide<MX>& from_w, int j, int i) {
+        if (j == 0)
+            word[i] = scale_word<MX>(from_w);
+        wv[j & 1][i] = expand<MX>(from_w.c[j >> 2][j & 3], factor_of<MX>(word[i], j));
+    };
+    int step = s0, part = p.parts - 1; // of the next loads
+    auto advance = [&]() {
+        if (part == 0) {
+            part = p.parts;
+            ++step;
+        }
+        --part;
+    };
     if (turns > 0) {
-        load_x_tile(0, 0);
-        load_w(0, now);
+        load_w(step, now);
+        load_x_tile(step, part, 0);
+        advance();
+        expand_tile(now[0], 0, 0);
+        expand_tile(now[1], 0, 1);
     }
     for (int turn = 0; turn < turns; ++turn) {
         const int at = turn & 1;
         __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0): this wave's part of the step's x has arrived
         __syncthreads();                    // everybody's has, and the other buffer is free
-        if (turn + 1 < turns)
-            load_x_tile(turn + 1, at ^ 1);
-        load_w(turn + 1, next);
-        Scales sc[TN];
+        if (turn + 1 < turns) {
+            load_w(step, next);
+            load_x_tile(step, part, at ^ 1);
+            advance();
+        }
+        auto read_x = [&](int i) { // the i-th of the step's reads
+            const int row = 32 * (i % TM) + n;
+            return xbuf[at][row * U + ((8 * h + i / TM) ^ (n & 15))];
+        };
+        u32x4 xv[kReadAhead];
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-            sc[i] = scales_of<MX>(now.s[i]);
+        for (int i = 0; i < kReadAhead; ++i)
+            xv[i] = read_x(i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            u32x4 wv[TN];
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-                wv[i] = expand<MX>(now.c[i][j], j < 2 ? sc[i].lo : sc[i].hi);
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                const u32x4 xv = xbuf[at][(16 * i + r) * U + ((4 * g + j) ^ r)];
+                const int x_turn = j * TM + i;
+                // the order of these is kept: a read for later, a part of the expansion, the products
+                __builtin_amdgcn_sched_barrier(0);
+                const u32x4 mine = xv[x_turn % kReadAhead];
+                if (x_turn + kReadAhead < 8 * TM)
+                    xv[x_turn % kReadAhead] = read_x(x_turn + kReadAhead);
+                if (i == 0 || i == TM / 2)
+                    expand_tile(j < 7 ? now[i != 0] : next[i != 0], (j + 1) & 7, i != 0);
 #pragma unroll
-                for (int t = 0; t < TN; ++t)
-                    acc[i][t] = mfma16(wv[t], xv, acc[i][t]);
+                for (int t = 0; t < 2; ++t)
+                    acc[i][t] = mfma32(wv[j & 1][t], mine, acc[i][t]);
             }
-        }
-        now = next;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            now[i] = next[i];
     }
 
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + 16 * i + r;
+        const int64_t m = m0 + 32 * i + n;
         if (m >= a.m)
             continue;
 #pragma unroll
-        for (int t = 0; t < TN / NW; ++t) {
-            const int64_t n = nw + (16 / NW) * g + 4 * t;
-            if (n >= a.n)
-                continue;
-            f32x4 sum[NW];
+        for (int t = 0; t < 2 / NW; ++t)
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                sum[w] = acc[i][w * (TN / NW) + t];
-            if (p.splits == 1) {
-                store4(a, m, n, finish4<MX, NW>(a, sum));
-            } else {
+            for (int q = 0; q < 4; ++q) {
+                const int64_t col = nw + 32 * t + 16 * h + 4 * q;
+                if (col >= a.n)
+                    continue;
+                f32x4 sum[NW];
 #pragma unroll
                 for (int w = 0; w < NW; ++w)
-                    *partial_of(a, p, (int)blockIdx.z, w, m, n) = sum[w];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[w][e] = acc[i][NW == 2 ? w : t][4 * q + e];
+                if (p.splits == 1) {
+                    store4(a, m, col, finish4<MX, NW>(a, sum));
+                } else {
+#pragma unroll
+                    for (int w = 0; w < NW; ++w)
+                        *partial_of(a, p, (int)blockIdx.z, w, m, col) = sum[w];
+                }
             }
-        }
     }
 }
 
@@ -629,7 +748,7 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
             else
                 matmul_parts<B, 3><<<cover, 256, 0, a.stream>>>(a);
         }
-        matmul_many<MX, NW, 8, 4><<<dim3(tiles_n * tiles_m, 1, (uint32_t)p.splits), 256, 0, a.stream>>>(a, p);
+        matmul_many<MX, NW, 4, 4><<<dim3(tiles_n * tiles_m, 1, (uint32_t)p.splits), 256, 0, a.stream>>>(a, p);
     } else {
         const dim3 grid(tiles_n, tiles_m, (uint32_t)p.splits);
         switch (p.parts) {

@@ -431,19 +431,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of_x(const void* p, int
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
 }
 
-// 64 values of a row of the weight: codes, and scale bytes as they came, in one load or in
-// one each (put together where they are used, so that nothing waits for them before)
-template <bool MX>
+// 64 values of a row of the weight: codes, and scale bytes as they came: in ONE load, or
+// each in one of its own, put together where they are used, so that nothing waits for
+// them before.
+template <bool MX, bool ONE>
 struct Wide {
-    static constexpr int NS = MX ? 2 : 4;
+    static constexpr int NS = ONE ? 1 : (MX ? 2 : 4);
     u32x4 c[2];
     uint32_t s[NS];
 };
 
-template <bool MX>
-__device__ __forceinline__ uint32_t scale_word(const Wide<MX>& w)
+template <bool MX, bool ONE>
+__device__ __forceinline__ uint32_t scale_word(const Wide<MX, ONE>& w)
 {
-    if constexpr (MX)
+    if constexpr (ONE)
+        return w.s[0];
+    else if constexpr (MX)
         return w.s[0] | (w.s[1] << 8);
     else
         return w.s[0] | (w.s[1] << 8) | (w.s[2] << 16) | (w.s[3] << 24);
@@ -460,7 +463,7 @@ __device__ __forceinline__ float factor_of(uint32_t word, int j)
     return t[(j >> 1) & 1];
 }
 
-template <bool MX, int NW, int TM, int WN>
+template <bool MX, int NW, int TM, int WN, bool ONE>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
     constexpr int B = MX ? 32 : 16;
@@ -537,10 +540,8 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     }
     const int w_row = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
     const int c_at = w_row * crow + 32 * h, s_at = w_row * srow + 64 * h / B;
-    constexpr int SB = 64 / B; // scale bytes of 64 values, in one load where they lie so
-    const bool one = (cols & 63) == 0 &&
-                     ((reinterpret_cast<uintptr_t>(a.scales[0]) | reinterpret_cast<uintptr_t>(a.scales[NW - 1])) & (SB - 1)) == 0;
-    auto load_w = [&](int step, Wide<MX> (&t)[2]) {
+    constexpr int SB = 64 / B; // scale bytes of 64 values
+    auto load_w = [&](int step, Wide<MX, ONE> (&t)[2]) {
         const int k = step * kStepK + 64 * h;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -550,26 +551,18 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
                 t[i].c[c] = __builtin_amdgcn_raw_buffer_load_b128(codes[w], (c_at + 16 * c) | (k + 32 * c < cols ? 0 : kPast),
                                                                   __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2)), 0);
         }
-        if (one) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
-                const int at = s_at | (k < cols ? 0 : kPast);
-                const int to = __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B));
-                t[i].s[0] = MX ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales[w], at, to, 0)
-                               : __builtin_amdgcn_raw_buffer_load_b32(scales[w], at, to, 0);
-#pragma unroll
-                for (int q = 1; q < SB; ++q)
-                    t[i].s[q] = 0u;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
+        for (int i = 0; i < 2; ++i) {
+            const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
+            const int to = __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B));
+            if constexpr (ONE) {
+                const int past = k < cols ? 0 : kPast;
+                t[i].s[0] = MX ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales[w], s_at | past, to, 0)
+                               : __builtin_amdgcn_raw_buffer_load_b32(scales[w], s_at | past, to, 0);
+            } else {
 #pragma unroll
                 for (int q = 0; q < SB; ++q)
-                    t[i].s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], (s_at + q) | (k + q * B < cols ? 0 : kPast),
-                                                                             __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B)), 0);
+                    t[i].s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], (s_at + q) | (k + q * B < cols ? 0 : kPast), to, 0);
             }
         }
     };
@@ -583,12 +576,12 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
             for (int e = 0; e < 16; ++e)
                 acc[i][j][e] = 0.0f;
 
-    Wide<MX> now[2], next[2];
+    Wide<MX, ONE> now[2], next[2];
     u32x4 wv[2][2];
     uint32_t word[2];
-    auto expand_tile = [&](const Wide<MX>& from_w, int j, int i) {
+    auto expand_tile = [&](const Wide<MX, ONE>& from_w, int j, int i) {
         if (j == 0)
-            word[i] = scale_word<MX>(from_w);
+            word[i] = scale_word<MX, ONE>(from_w);
         wv[j & 1][i] = expand<MX>(from_w.c[j >> 2][j & 3], factor_of<MX>(word[i], j));
     };
     int step = s0, part = p.parts - 1; // of the next loads
@@ -748,7 +741,15 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
             else
                 matmul_parts<B, 3><<<cover, 256, 0, a.stream>>>(a);
         }
-        matmul_many<MX, NW, 4, 4><<<dim3(tiles_n * tiles_m, 1, (uint32_t)p.splits), 256, 0, a.stream>>>(a, p);
+        const dim3 grid(tiles_n * tiles_m, 1, (uint32_t)p.splits);
+        // the scale bytes of 64 values in one load, where every row's begin so that they can be
+        uintptr_t places = (uintptr_t)(a.k / (MX ? 32 : 16));
+        for (int w = 0; w < NW; ++w)
+            places |= reinterpret_cast<uintptr_t>(a.scales[w]);
+        if (places % (MX ? 2 : 4) == 0)
+            matmul_many<MX, NW, 4, 4, true><<<grid, 256, 0, a.stream>>>(a, p);
+        else
+            matmul_many<MX, NW, 4, 4, false><<<grid, 256, 0, a.stream>>>(a, p);
     } else {
         const dim3 grid(tiles_n, tiles_m, (uint32_t)p.splits);
         switch (p.parts) {

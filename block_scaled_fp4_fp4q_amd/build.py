@@ -15,7 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp4q.so")
-SOURCES = ["fp4q_kernels.hip", "fp4q_kv.hip", "fp4q_append.hip", "fp4q_attend.hip", "fp4q_matmul.hip",
+SOURCES = ["fp4q_kernels.hip", "fp4q_kv.hip", "fp4q_append.hip", "fp4q_attend.hip", "fp4q_matmul_nv.hip",
+           "fp4q_matmul_mx.hip",
            "fp4q_capi.cpp", "fp4q_kv_capi.cpp", "fp4q_matmul_capi.cpp"]
 ARCH = os.environ.get("FP4Q_OFFLOAD_ARCH", "gfx950")
 

@@ -8,14 +8,16 @@
 #include <climits>
 
 #include "fp4q_matmul_launch.h"
+#include "fp4q_matmul_plan.h"
 
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int64_t kMostCols = (int64_t)1 << 24; // 64 rows of codes stay within 32-bit offsets
+constexpr int64_t kMostCols = (int64_t)1 << 22; // 128 rows stay within 32-bit offsets
 constexpr int64_t kMostRows = (int64_t)1 << 36; // and a weight within 63 bits
 constexpr int64_t kMostStride = (int64_t)1 << 46;
+constexpr int64_t kMostRowStride = (int64_t)1 << 22; // of x
 
 fp4q_status check_weight(const fp4q_spec* s, const fp4q_weight* w)
 {
@@ -62,7 +64,7 @@ size_t workspace_bytes(const fp4q_spec* spec, const fp4q_weight* w, int weights,
     a.weights = weights;
     if (check_weight(spec, w) != FP4Q_OK || check_sizes(spec, w, tokens, dtype, a) != FP4Q_OK || a.n == 0 || a.m == 0)
         return 0;
-    const fp4q::MatmulPlan p = fp4q::plan_matmul(a);
+    const fp4q::MatmulPlan p = fp4q::plan_of(a);
     return p.refused ? 0 : p.workspace;
 }
 
@@ -80,7 +82,7 @@ fp4q_status run(const fp4q_spec* spec, const fp4q_weight* const* w, int weights,
         return FP4Q_E_SHAPE;
     if ((st = check_sizes(spec, w[0], tokens, dtype, a)) != FP4Q_OK)
         return st;
-    if (x_stride < 0 || x_stride > kMostStride || y_stride < 0 || y_stride > kMostStride ||
+    if (x_stride < 0 || x_stride > kMostRowStride || y_stride < 0 || y_stride > kMostStride ||
         (x_stride != 0 && tokens > (INT64_MAX >> 4) / x_stride) || (y_stride != 0 && tokens > (INT64_MAX >> 4) / y_stride))
         return FP4Q_E_SHAPE;
     if (tokens > 1 && y_stride < a.n)
@@ -103,7 +105,7 @@ fp4q_status run(const fp4q_spec* spec, const fp4q_weight* const* w, int weights,
     a.y_row = y_stride;
     a.y_wide = aligned(y, a.bf16 ? 8 : 16) && y_stride % 4 == 0;
     a.stream = static_cast<hipStream_t>(stream);
-    const fp4q::MatmulPlan p = fp4q::plan_matmul(a);
+    const fp4q::MatmulPlan p = fp4q::plan_of(a);
     if (p.refused)
         return FP4Q_E_SHAPE; // more workgroups than a launch holds
     if (p.workspace != 0) {
@@ -115,7 +117,7 @@ fp4q_status run(const fp4q_spec* spec, const fp4q_weight* const* w, int weights,
             return FP4Q_E_ALIGN;
     }
     a.workspace = workspace;
-    return fp4q::launch_matmul(a, p) == hipSuccess ? FP4Q_OK : FP4Q_E_HIP;
+    return (a.mx ? fp4q::launch_matmul_mx(a, p) : fp4q::launch_matmul_nv(a, p)) == hipSuccess ? FP4Q_OK : FP4Q_E_HIP;
 }
 
 } // namespace

@@ -1,0 +1,788 @@
+// fp4q_matmul_kernels.h -- products of activations with 4-bit weights: the kernels
+// and their launch, for one format (fp4q_matmul_nv.hip, fp4q_matmul_mx.hip).
+//
+//   y_mn = S sum_k x_mk v_nk s_n(k)        (v a code's value, s its block's scale)
+//
+// and, of two weights, act(x W0^T) * (x W1^T).  A code times its E4M3 scale has
+// at most six significant bits and lies in [2^-10, 2688], and a code times 2^e has two:
+// dequantized weights enter the matrix cores exactly, NVFP4 as bf16 or as f16,
+// MXFP4 as bf16, and so does x of bf16; the global scale is one binary32 factor of the sum.
+// A weight that is stored rotated is never rotated back: x W^T = (x H)(W H)^T with H
+// the orthonormal block Hadamard, so x is rotated, in binary32.
+//
+// Parts.  Where x is not exact in bf16 it is given as a sum of 16-bit parts, one matrix product
+// each.  With NVFP4 they are f16, after a power of two per row that brings its
+// largest value to [2^14, 2^15) (what falls below f16's range is under 2^-38 of that
+// value): rotated bf16 in one part, 11 bits, 8 times finer than the rounding of a bf16
+// result; binary32 in two, 22 bits.  With MXFP4, whose weights f16 does not hold, they
+// are bf16: rotated bf16 in two, 16 bits, binary32 in three, which hold its 24 bits.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "fp4q_device.h"
+#include "fp4q_matmul_launch.h"
+
+namespace fp4q {
+namespace {
+
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// what the weights are, and enter the products as
+enum Kind { kNvBf16, kNvF16, kMxBf16 };
+
+template <Kind KIND>
+__device__ __forceinline__ f32x4 mfma16(u32x4 x, u32x4 y, f32x4 c)
+{
+    if constexpr (KIND == kNvF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
+}
+
+template <Kind KIND>
+__device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
+{
+    if constexpr (KIND == kNvF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
+}
+
+// ---- weights -------------------------------------------------------------------
+
+// Two codes of a word times their block's scale s.  The product has six bits: f16 holds it,
+// and cutting it from binary32 to bf16 loses nothing.  (A step of two codes costs about
+// 16 cycles of a SIMD as bf16, 11 as f16, 7 for a power of two.)
+template <Kind KIND, int SEL>
+__device__ __forceinline__ uint32_t expand_pair(uint32_t w, float s)
+{
+    if constexpr (KIND == kMxBf16) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, SEL));
+    } else if constexpr (KIND == kNvF16) {
+        const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL));
+        return __builtin_bit_cast(uint32_t, v * __builtin_bit_cast(f16x2, s));
+    } else {
+        float a, b;
+        fp4_unpack2<SEL>(w, a, b);
+        return __builtin_amdgcn_perm(__float_as_uint(b * s), __float_as_uint(a * s), 0x07060302u);
+    }
+}
+
+// the eight codes of a word; s from factor_of
+template <Kind KIND>
+__device__ __forceinline__ u32x4 expand(uint32_t w, float s)
+{
+    return u32x4{expand_pair<KIND, 0>(w, s), expand_pair<KIND, 1>(w, s), expand_pair<KIND, 2>(w, s), expand_pair<KIND, 3>(w, s)};
+}
+
+// 64 values of a row of the weight: codes, and scale bytes as they came: in ONE load, or
+// each in one of its own, put together where they are used, so that nothing waits for
+// them before.
+template <Kind KIND, bool ONE>
+struct Wide {
+    static constexpr int NS = ONE ? 1 : (KIND == kMxBf16 ? 2 : 4);
+    u32x4 c[2];
+    uint32_t s[NS];
+};
+
+template <Kind KIND, bool ONE>
+__device__ __forceinline__ uint32_t scale_word(const Wide<KIND, ONE>& w)
+{
+    if constexpr (ONE)
+        return w.s[0];
+    else if constexpr (KIND == kMxBf16)
+        return w.s[0] | (w.s[1] << 8);
+    else
+        return w.s[0] | (w.s[1] << 8) | (w.s[2] << 16) | (w.s[3] << 24);
+}
+
+// The factor of values 8 j .. 8 j + 7 of 64: the value of their E4M3 byte in binary32 or
+// twice in f16, or the power of two of their E8M0 byte, whose exponent alone the conversions
+// apply (255 stands for NaN).
+template <Kind KIND>
+__device__ __forceinline__ float factor_of(uint32_t word, int j)
+{
+    if constexpr (KIND == kMxBf16) {
+        return __uint_as_float((j < 4 ? word & 0xFFu : word >> 8) << 23);
+    } else if constexpr (KIND == kNvF16) {
+        const f16x2 t = __builtin_bit_cast(f16x2, j < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false)
+                                                        : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true));
+        const _Float16 one = t[(j >> 1) & 1];
+        return __builtin_bit_cast(float, f16x2{one, one});
+    } else {
+        const auto t = j < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, false)
+                             : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, true);
+        return t[(j >> 1) & 1];
+    }
+}
+
+// Raw buffer resource over `bytes` bytes from p (uniform): a load past the end
+// gives zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
+}
+
+// OR-ed to an offset, past every buffer's end (a select would become a branch
+// around the load)
+constexpr int kPast = 0x7FFFFFFF;
+
+// Values 64 of a row from value k on, the row's places within its buffers being c_at and
+// s_at (a lane's own) and c_to, s_to (uniform): past the row's end any codes, with scales
+// of zero.
+template <Kind KIND, bool ONE>
+__device__ __forceinline__ Wide<KIND, ONE> load_wide(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, int c_at, int s_at,
+                                                     int c_to, int s_to, int k, int cols)
+{
+    constexpr int B = KIND == kMxBf16 ? 32 : 16;
+    Wide<KIND, ONE> t;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        t.c[c] = __builtin_amdgcn_raw_buffer_load_b128(codes, (c_at + 16 * c) | (k + 32 * c < cols ? 0 : kPast), c_to, 0);
+    if constexpr (ONE) {
+        const int past = k < cols ? 0 : kPast;
+        t.s[0] = KIND == kMxBf16 ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales, s_at | past, s_to, 0)
+                                 : __builtin_amdgcn_raw_buffer_load_b32(scales, s_at | past, s_to, 0);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 64 / B; ++q)
+            t.s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, (s_at + q) | (k + q * B < cols ? 0 : kPast), s_to, 0);
+    }
+    return t;
+}
+
+// ---- activations ------------------------------------------------------------------
+
+// x as a sum of PARTS bf16 values, their bits in the upper halves of h: cut, the
+// remainder cut again, and for the last part rounded to nearest even (with three
+// parts it is exact).  A value that is not finite is its first part alone.
+template <int PARTS>
+__device__ __forceinline__ void parts_of(float x, uint32_t* h)
+{
+    const bool finite = __builtin_fabsf(x) < __builtin_huge_valf();
+    h[0] = finite ? __float_as_uint(x) & 0xFFFF0000u : f32_to_bf16(x) << 16;
+    float rest = finite ? x - __uint_as_float(h[0]) : 0.0f;
+    if constexpr (PARTS == 3) {
+        h[1] = __float_as_uint(rest) & 0xFFFF0000u;
+        rest -= __uint_as_float(h[1]);
+    }
+    h[PARTS - 1] = f32_to_bf16(rest) << 16;
+}
+
+// the same in f16, of values below 2^15, in the lower halves
+template <int PARTS>
+__device__ __forceinline__ void halves_of(float x, uint32_t* h)
+{
+    const _Float16 first = (_Float16)x;
+    h[0] = __builtin_bit_cast(uint16_t, first);
+    if constexpr (PARTS == 2)
+        h[1] = __builtin_bit_cast(uint16_t, (_Float16)(__builtin_fabsf(x) < __builtin_huge_valf() ? x - (float)first : 0.0f));
+}
+
+// the B values of a block of x, widened and rotated
+template <int B>
+__device__ __forceinline__ void load_x(const MatmulArgs& a, int64_t row, int64_t k, float* v)
+{
+    const int64_t at = row * a.x_row + k;
+    if (a.bf16)
+        load_block<B, true, false>(static_cast<const uint16_t*>(a.x) + at, 0, v);
+    else
+        load_block<B, false, false>(static_cast<const float*>(a.x) + at, 0, v);
+    if (a.rotate)
+        fwht<B>(v);
+}
+
+// The bf16 parts of x, for MXFP4: [part][m][k] in the workspace, a block of values a
+// thread.  Moves x once: bound by HBM.
+template <int PARTS>
+__global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
+{
+    constexpr int B = 32;
+    const int64_t blocks = a.k / B, all = a.m * blocks, plane = a.m * a.k;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
+        const int64_t row = u / blocks, b = u - row * blocks;
+        float v[B];
+        load_x<B>(a, row, b * B, v);
+        uint16_t* to = static_cast<uint16_t*>(a.workspace) + u * B;
+#pragma unroll
+        for (int i = 0; i < B / 8; ++i) {
+            uint32_t h[8][PARTS];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                parts_of<PARTS>(v[8 * i + j], h[j]);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                *reinterpret_cast<u32x4*>(to + q * plane + 8 * i) =
+                    u32x4{h[0][q] >> 16 | h[1][q], h[2][q] >> 16 | h[3][q], h[4][q] >> 16 | h[5][q], h[6][q] >> 16 | h[7][q]};
+        }
+    }
+}
+
+// The f16 parts of x, for NVFP4: [part][m][k] in the workspace, and behind them each row's
+// exponent (what its values were multiplied by is 2^exponent).  A workgroup has a row:
+// its largest finite value first, then the parts; blocks that a thread does not hold
+// itself it reads again, from cache.
+template <int PARTS>
+__global__ __launch_bounds__(256) void matmul_halves(const MatmulArgs a, const MatmulPlan p)
+{
+    constexpr int B = 16;
+    __shared__ float most[4];
+    const int64_t row = (int64_t)blockIdx.y * 65536 + blockIdx.x;
+    if (row >= a.m)
+        return;
+    const int blocks = (int)(a.k / B);
+    float v[B], top = 0.0f;
+    for (int b = threadIdx.x; b < blocks; b += 256) {
+        load_x<B>(a, row, (int64_t)b * B, v);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const float x = __builtin_fabsf(v[i]);
+            top = x < __builtin_huge_valf() ? __builtin_fmaxf(top, x) : top;
+        }
+    }
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0)
+        most[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = __builtin_fmaxf(__builtin_fmaxf(most[0], most[1]), __builtin_fmaxf(most[2], most[3]));
+    const int up = top > 0.0f ? 141 - (int)(__float_as_uint(top) >> 23) : 0; // to [2^14, 2^15)
+    if (threadIdx.x == 0)
+        reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + p.exponents)[row] = up;
+    for (int b = threadIdx.x; b < blocks; b += 256) {
+        if (blocks > 256)
+            load_x<B>(a, row, (int64_t)b * B, v);
+        uint16_t* to = static_cast<uint16_t*>(a.workspace) + row * a.k + (int64_t)b * B;
+#pragma unroll
+        for (int i = 0; i < B / 8; ++i) {
+            uint32_t h[8][PARTS];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                halves_of<PARTS>(__builtin_ldexpf(v[8 * i + j], up), h[j]);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                *reinterpret_cast<u32x4*>(to + q * a.m * a.k + 8 * i) =
+                    u32x4{h[0][q] | h[1][q] << 16, h[2][q] | h[3][q] << 16, h[4][q] | h[5][q] << 16, h[6][q] | h[7][q] << 16};
+        }
+    }
+}
+
+// ---- results --------------------------------------------------------------------------
+
+__device__ __forceinline__ float activation(int act, float g)
+{
+    if (act == kActSilu)
+        return g / (1.0f + expf(-g));
+    if (act == kActGelu)
+        return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    // 0.5 g (1 + tanh z) = g / (1 + exp(-2 z))
+    const float z = 0.79788456080286536f * (g + 0.044715f * g * g * g);
+    return g / (1.0f + expf(-2.0f * z));
+}
+
+// four values of row m of y from column n (a multiple of four) on
+__device__ __forceinline__ void store4(const MatmulArgs& a, int64_t m, int64_t n, f32x4 v)
+{
+    const int64_t at = m * a.y_row + n;
+    if (a.y_wide && n + 4 <= a.n) {
+        if (a.bf16)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+        else
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.n) {
+            if (a.bf16)
+                static_cast<uint16_t*>(a.y)[at + i] = (uint16_t)(bf16_pair(v[i], v[i]) & 0xFFFFu);
+            else
+                static_cast<float*>(a.y)[at + i] = v[i];
+        }
+}
+
+// y's values from the sums of one weight, or of two, of row m
+template <Kind KIND, int NW>
+__device__ __forceinline__ f32x4 finish4(const MatmulArgs& a, const MatmulPlan& p, int64_t m, f32x4* sum)
+{
+    if constexpr (KIND == kNvF16) {
+        const int up = reinterpret_cast<const int32_t*>(static_cast<const char*>(a.workspace) + p.exponents)[m];
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum[w][i] = __builtin_ldexpf(sum[w][i], -up);
+    }
+    if constexpr (KIND != kMxBf16) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            sum[w] *= *a.global[w];
+    }
+    f32x4 r = sum[0];
+    if constexpr (NW == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = activation(a.act, r[i]) * sum[1][i];
+    }
+    return r;
+}
+
+// partial sums of split s: [weight][m][n, padded to four]
+__device__ __forceinline__ f32x4* partial_of(const MatmulArgs& a, const MatmulPlan& p, int s, int w, int64_t m, int64_t n)
+{
+    const int64_t wide = (a.n + 3) & ~(int64_t)3;
+    float* sums = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partials);
+    return reinterpret_cast<f32x4*>(sums + (((int64_t)s * a.weights + w) * a.m + m) * wide + n);
+}
+
+// ---- few rows of x ------------------------------------------------------------------
+//
+// A workgroup of RW x KW waves takes 16 RW rows of the weight (of each of two) and up to 16
+// rows of x; RW waves share the rows, KW the long axis, 256 values a step.  W is the
+// first operand of 16x16x32 products: lane n + 16 g loads the 32 bytes of row n that hold
+// values 64 g .. 64 g + 63 of a step and gives them to eight products, eight at a
+// time; x comes from LDS, where the whole workgroup put it (CONV: rotated and cut into bf16
+// parts on the way; else as it is, or as matmul_parts and matmul_halves left it).  The
+// codes of the next kAhead steps are on their way while a step is computed.
+constexpr int kAhead = 2;
+
+template <Kind KIND, int NW, int PARTS, bool CONV, int RW, int KW, bool ONE>
+__global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, const MatmulPlan p)
+{
+    constexpr int B = KIND == kMxBf16 ? 32 : 16;
+    constexpr int T = 64 * RW * KW;
+    constexpr int U = kFewStep / 8; // 16-byte units of x in a step
+    extern __shared__ u32x4 lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
+    const int rw = wave % RW, kw = wave / RW;
+    const int64_t n0 = (int64_t)blockIdx.x * p.rows;
+    const int mt = (int)a.m;
+    const int cols = (int)a.k, steps = (cols + kFewStep - 1) / kFewStep;
+
+    // this wave's rows of each weight, from its first one on
+    const int64_t nw = n0 + rw * 16;
+    const int64_t left = a.n - nw;
+    const int live = left <= 0 ? 0 : (int)(left < 16 ? left : 16);
+    const int crow = cols / 2, srow = cols / B;
+    __amdgpu_buffer_rsrc_t codes[NW], scales[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const int64_t first = live > 0 ? nw : 0;
+        codes[w] = buffer_of(a.codes[w] + first * crow, live * crow);
+        scales[w] = buffer_of(a.scales[w] + first * srow, live * srow);
+    }
+    auto load = [&](int step, Wide<KIND, ONE> (&t)[NW]) {
+        const int k = step * kFewStep + 64 * g;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            t[w] = load_wide<KIND, ONE>(codes[w], scales[w], r * crow + k / 2, r * srow + k / B, 0, 0, k, cols);
+    };
+
+    Wide<KIND, ONE> ring[kAhead][NW];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        load(kw + KW * i, ring[i]);
+
+    // x of chunk_steps steps from step `from` on: [part][row][value], rows padded
+    // by 16 bytes so that 16 rows meet all banks
+    const int stride = p.chunk_steps * U + 1;
+    auto fill = [&](int from) {
+        if constexpr (CONV) {
+            const int per = p.chunk_steps * (kFewStep / B); // blocks of a row
+            for (int u = threadIdx.x; u < mt * per; u += T) {
+                const int row = u / per, b = u - row * per;
+                const int k = from * kFewStep + b * B;
+                u32x4* to = lds + row * stride + b * (B / 8);
+                float v[B];
+                if (k < cols) {
+                    load_x<B>(a, row, k, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < B; ++i)
+                        v[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < B / 8; ++i) {
+                    uint32_t h[8][PARTS];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        parts_of<PARTS>(v[8 * i + j], h[j]);
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q)
+                        to[q * mt * stride + i] =
+                            u32x4{h[0][q] >> 16 | h[1][q], h[2][q] >> 16 | h[3][q], h[4][q] >> 16 | h[5][q], h[6][q] >> 16 | h[7][q]};
+                }
+            }
+        } else {
+            const int per = p.chunk_steps * U; // units of a row
+            const uint16_t* x = static_cast<const uint16_t*>(p.prepared ? a.workspace : a.x);
+            const int64_t row_of = p.prepared ? a.k : a.x_row;
+            for (int u = threadIdx.x; u < PARTS * mt * per; u += T) {
+                const int row = u / per, b = u - row * per; // rows of all parts in turn
+                const int k = from * kFewStep + b * 8;
+                u32x4 v = u32x4{0u, 0u, 0u, 0u};
+                if (k < cols)
+                    v = *reinterpret_cast<const u32x4*>(x + row * row_of + k);
+                lds[row * stride + b] = v;
+            }
+        }
+    };
+
+    f32x4 acc[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // this lane's row of x; lanes past the last repeat it
+    const int x_at = (r < mt ? r : mt - 1) * stride + 8 * g;
+
+    const int turns = p.chunk_steps / KW; // of this wave in a chunk
+    const int all = (steps + KW - 1) / KW; // the same for every wave of the workgroup
+    int in_chunk = turns;
+    for (int base = 0; base < all; base += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            const int i = base + d;
+            if (i >= all)
+                break;
+            if (in_chunk == turns) {
+                if (i != 0)
+                    __syncthreads();
+                fill(i * KW);
+                __syncthreads();
+                in_chunk = 0;
+            }
+            const u32x4* x = lds + (in_chunk * KW + kw) * U + x_at;
+            uint32_t word[NW];
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                word[w] = scale_word(ring[d][w]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                u32x4 xv[PARTS];
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+                    xv[q] = x[q * mt * stride + j];
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const u32x4 wv = expand<KIND>(ring[d][w].c[j >> 2][j & 3], factor_of<KIND>(word[w], j));
+#pragma unroll
+                    for (int q = PARTS - 1; q >= 0; --q) // small parts first
+                        acc[w] = mfma16<KIND>(wv, xv[q], acc[w]);
+                }
+            }
+            load(kw + KW * (i + kAhead), ring[d]);
+            ++in_chunk;
+        }
+    }
+
+    // join the waves that share rows, in order
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        red[(wave * NW + w) * 64 + lane] = acc[w];
+    __syncthreads();
+    for (int u = threadIdx.x; u < RW * 64; u += T) {
+        const int l = u & 63, part = u >> 6;
+        const int64_t n = n0 + part * 16 + 4 * (l >> 4), m = l & 15;
+        if (n >= a.n || m >= a.m)
+            continue;
+        f32x4 sum[NW];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            sum[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < KW; ++k)
+                sum[w] += red[((k * RW + part) * NW + w) * 64 + l];
+        }
+        store4(a, m, n, finish4<KIND, NW>(a, p, m, sum));
+    }
+}
+
+constexpr int kReadAhead = 2; // reads of x from LDS before their products
+
+// ---- many rows of x -------------------------------------------------------------------
+//
+// A workgroup of WN waves takes 32 TM rows of x and 64 WN of the weight (32 WN of each
+// of two), in 32x32x16 products.  The x of a step, 128 values of each row, lies in LDS,
+// double buffered, loaded there directly; every wave reads all of it and multiplies it
+// by its own 64 rows of the weight, which it loads and expands itself, so that no code
+// is expanded twice in a workgroup and no expanded weight passes through LDS.
+//   Lane n + 32 h holds, of a row, the values 64 h .. 64 h + 63 of a step, eight for each
+// product: W's come as 32 bytes of codes.  16-byte units of a row of x are exchanged in LDS by
+// an XOR with the row, so that 16 lanes that read one unit of 16 rows meet all banks; a
+// lane loads the unit that belongs at its place.
+//   Row 8 q + 4 h + e of a product's 32 rows of W is column 16 h + 4 q + e of y, so that a
+// lane ends with 16 neighbouring columns.
+//   While the products of eight values run, the weights of the next eight are expanded; the
+// last ones' are those of the next step.
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <Kind KIND, int NW, int TM, int WN, bool ONE>
+__global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
+{
+    constexpr int B = KIND == kMxBf16 ? 32 : 16;
+    constexpr int BM = 32 * TM;
+    constexpr int BN = 64 * WN / NW; // columns of y
+    constexpr int WC = 64 / NW;      // of a wave
+    constexpr int U = kStepK / 8;    // 16-byte units of a row of x
+    __shared__ u32x4 xbuf[2][BM * U];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int n = lane & 31, h = lane >> 5;
+
+    // workgroups of one XCD (every eighth) take neighbouring tiles: kGroup rows of tiles at a
+    // time, the rows of tiles fastest
+    const uint32_t tiles_m = (uint32_t)((a.m + BM - 1) / BM), tiles_n = (uint32_t)((a.n + BN - 1) / BN);
+    const uint32_t all = tiles_m * tiles_n;
+    uint32_t id = blockIdx.x;
+    {
+        const uint32_t xcd = id % 8, per = all / 8, more = all % 8;
+        id = xcd * per + (xcd < more ? xcd : more) + id / 8;
+    }
+    constexpr uint32_t kGroup = 8;
+    const uint32_t band = id / (kGroup * tiles_n), first = band * kGroup;
+    const uint32_t high = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+    const uint32_t in = id - band * kGroup * tiles_n;
+    const int64_t m0 = (int64_t)(first + in % high) * BM, n0 = (int64_t)(in / high) * BN;
+
+    const int cols = (int)a.k;
+    const int steps = (cols + kStepK - 1) / kStepK;
+    const int s0 = (int)blockIdx.z * p.split_steps;
+    const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
+    const int turns = (s1 - s0) * p.parts; // a step for each part of x, the small ones first
+    // Offsets are a lane's own (in a vector register) and a uniform part that never passes
+    // the buffer's end, where the check against it would wrap: rows of a tile that do not
+    // exist are replaced by others, whose results are not stored.
+
+    // x, or its parts: plane q, row m
+    const int64_t m_left = a.m - m0;
+    const int rows = (int)(m_left < BM ? m_left : BM);
+    const int x_row = (int)(p.prepared ? a.k : a.x_row) * 2; // bytes
+    const char* x = static_cast<const char*>(p.prepared ? a.workspace : a.x) + m0 * x_row;
+    const int64_t plane = a.m * a.k * 2;
+    constexpr int LOADS = BM / (4 * WN); // of a wave: four rows each
+    const int quad = lane >> 4;          // row of the four
+    constexpr int KINDS = LOADS < 4 ? LOADS : 4; // the exchange of units repeats every four loads
+    int x_unit[KINDS];
+#pragma unroll
+    for (int i = 0; i < KINDS; ++i)
+        x_unit[i] = (lane & 15) ^ ((4 * (wave * LOADS + i) + quad) & 15);
+    auto load_x_tile = [&](int step, int part, int to) {
+        const auto src = buffer_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
+        const bool whole = (step + 1) * kStepK <= cols;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = (wave * LOADS + i) * 4;
+            int at = quad * x_row + x_unit[i % KINDS] * 16;
+            if (!whole) // values past the row's end are zeros
+                at |= step * kStepK + x_unit[i % KINDS] * 8 < cols ? 0 : kPast;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(&xbuf[to][(wave * LOADS + i) * 64]), 16, at,
+                                                     __builtin_amdgcn_readfirstlane((row < rows ? row : 0) * x_row + step * (kStepK * 2)), 0, 0);
+        }
+    };
+
+    // the wave's rows of each weight, 32 for a product
+    const int64_t nw = n0 + wave * WC;
+    const int64_t left = a.n - nw;
+    const int64_t from = left > 0 ? nw : 0;
+    const int live = (int)(left <= 0 ? 1 : (left < WC ? left : WC));
+    const int crow = cols / 2, srow = cols / B;
+    __amdgpu_buffer_rsrc_t codes[NW], scales[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        codes[w] = buffer_of(a.codes[w] + from * crow, live * crow);
+        scales[w] = buffer_of(a.scales[w] + from * srow, live * srow);
+    }
+    const int w_row = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
+    const int c_at = w_row * crow + 32 * h, s_at = w_row * srow + 64 * h / B;
+    auto load_w = [&](int step, Wide<KIND, ONE> (&t)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
+            t[i] = load_wide<KIND, ONE>(codes[w], scales[w], c_at, s_at,
+                                        __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2)),
+                                        __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B)), step * kStepK + 64 * h, cols);
+        }
+    };
+
+    f32x16 acc[TM][2];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[i][j][e] = 0.0f;
+
+    Wide<KIND, ONE> now[2], next[2];
+    u32x4 wv[2][2];
+    uint32_t word[2];
+    auto expand_tile = [&](const Wide<KIND, ONE>& from_w, int j, int i) {
+        if (j == 0)
+            word[i] = scale_word(from_w);
+        wv[j & 1][i] = expand<KIND>(from_w.c[j >> 2][j & 3], factor_of<KIND>(word[i], j));
+    };
+    int step = s0, part = p.parts - 1; // of the next loads
+    auto advance = [&]() {
+        if (part == 0) {
+            part = p.parts;
+            ++step;
+        }
+        --part;
+    };
+    if (turns > 0) {
+        load_w(step, now);
+        load_x_tile(step, part, 0);
+        advance();
+        expand_tile(now[0], 0, 0);
+        expand_tile(now[1], 0, 1);
+    }
+    for (int turn = 0; turn < turns; ++turn) {
+        const int at = turn & 1;
+        __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0): this wave's part of the step's x has arrived
+        __syncthreads();                    // everybody's has, and the other buffer is free
+        if (turn + 1 < turns) {
+            load_w(step, next);
+            load_x_tile(step, part, at ^ 1);
+            advance();
+        }
+        auto read_x = [&](int i) { // the i-th of the step's reads
+            const int row = 32 * (i % TM) + n;
+            return xbuf[at][row * U + ((8 * h + i / TM) ^ (n & 15))];
+        };
+        u32x4 xv[kReadAhead];
+#pragma unroll
+        for (int i = 0; i < kReadAhead; ++i)
+            xv[i] = read_x(i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int x_turn = j * TM + i;
+                // the order of these is kept: a read for later, a part of the expansion, the products
+                __builtin_amdgcn_sched_barrier(0);
+                const u32x4 mine = xv[x_turn % kReadAhead];
+                if (x_turn + kReadAhead < 8 * TM)
+                    xv[x_turn % kReadAhead] = read_x(x_turn + kReadAhead);
+                if (i == 0)
+                    expand_tile(j < 7 ? now[0] : next[0], (j + 1) & 7, 0);
+                if (i == TM / 2)
+                    expand_tile(j < 7 ? now[1] : next[1], (j + 1) & 7, 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    acc[i][t] = mfma32<KIND>(wv[j & 1][t], mine, acc[i][t]);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            now[i] = next[i];
+    }
+
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t m = m0 + 32 * i + n;
+        if (m >= a.m)
+            continue;
+#pragma unroll
+        for (int t = 0; t < 2 / NW; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t col = nw + 32 * t + 16 * h + 4 * q;
+                if (col >= a.n)
+                    continue;
+                f32x4 sum[NW];
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[w][e] = acc[i][NW == 2 ? w : t][4 * q + e];
+                if (p.splits == 1) {
+                    store4(a, m, col, finish4<KIND, NW>(a, p, m, sum));
+                } else {
+#pragma unroll
+                    for (int w = 0; w < NW; ++w)
+                        *partial_of(a, p, (int)blockIdx.z, w, m, col) = sum[w];
+                }
+            }
+    }
+}
+
+// the sums of all splits, in order, and the results
+template <Kind KIND, int NW>
+__global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const MatmulPlan p)
+{
+    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = (int64_t)blockIdx.z * 65535 + blockIdx.y;
+    if (n >= a.n || m >= a.m)
+        return;
+    f32x4 sum[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        sum[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < p.splits; ++s)
+            sum[w] += *partial_of(a, p, s, w, m, n);
+    }
+    store4(a, m, n, finish4<KIND, NW>(a, p, m, sum));
+}
+
+// ---- launch -------------------------------------------------------------------------------
+
+// whether the scale bytes of 64 values can be loaded at once in every row
+inline bool scales_together(const MatmulArgs& a)
+{
+    uintptr_t places = (uintptr_t)(a.k / (a.mx ? 32 : 16));
+    for (int w = 0; w < a.weights; ++w)
+        places |= reinterpret_cast<uintptr_t>(a.scales[w]);
+    return places % (a.mx ? 2 : 4) == 0;
+}
+
+template <Kind KIND, int NW, int PARTS, bool CONV>
+void few_form(const MatmulArgs& a, const MatmulPlan& p)
+{
+    const dim3 grid((uint32_t)((a.n + p.rows - 1) / p.rows));
+    const bool one = scales_together(a);
+    switch (p.waves_k) {
+#define FP4Q_FEW(RW, KW)                                                                             \
+    if (one)                                                                                         \
+        matmul_few<KIND, NW, PARTS, CONV, RW, KW, true><<<grid, 512, p.lds, a.stream>>>(a, p);       \
+    else                                                                                             \
+        matmul_few<KIND, NW, PARTS, CONV, RW, KW, false><<<grid, 512, p.lds, a.stream>>>(a, p);      \
+    break;
+    case 2: FP4Q_FEW(4, 2)
+    case 4: FP4Q_FEW(2, 4)
+    default: FP4Q_FEW(1, 8)
+#undef FP4Q_FEW
+    }
+}
+
+template <Kind KIND, int NW>
+void many_form(const MatmulArgs& a, const MatmulPlan& p)
+{
+    const uint32_t tiles_n = (uint32_t)((a.n + p.rows - 1) / p.rows), tiles_m = (uint32_t)((a.m + p.tokens - 1) / p.tokens);
+    const dim3 grid(tiles_n * tiles_m, 1, (uint32_t)p.splits);
+    const bool one = scales_together(a);
+    switch (p.tokens) {
+#define FP4Q_MANY(TM)                                                                    \
+    if (one)                                                                             \
+        matmul_many<KIND, NW, TM, 4, true><<<grid, 256, 0, a.stream>>>(a, p);            \
+    else                                                                                 \
+        matmul_many<KIND, NW, TM, 4, false><<<grid, 256, 0, a.stream>>>(a, p);           \
+    break;
+    case 32: FP4Q_MANY(1)
+    case 64: FP4Q_MANY(2)
+    default: FP4Q_MANY(4)
+#undef FP4Q_MANY
+    }
+}
+
+template <Kind KIND, int NW>
+void join_form(const MatmulArgs& a, const MatmulPlan& p)
+{
+    const dim3 cover((uint32_t)((a.n + 1023) / 1024), (uint32_t)(a.m < 65535 ? a.m : 65535), (uint32_t)((a.m + 65534) / 65535));
+    matmul_join<KIND, NW><<<cover, 256, 0, a.stream>>>(a, p);
+}
+
+} // namespace
+} // namespace fp4q

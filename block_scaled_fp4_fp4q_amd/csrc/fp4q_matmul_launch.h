@@ -1,6 +1,6 @@
 // fp4q_matmul_launch.h -- internal interface between the C ABI of the products
 // with 4-bit weights (fp4q_matmul_capi.cpp) and their kernel launchers
-// (fp4q_matmul.hip).  Not installed, not part of the ABI.
+// (fp4q_matmul_nv.hip, fp4q_matmul_mx.hip).  Not installed, not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -28,24 +28,29 @@ struct MatmulArgs {
     hipStream_t stream;
 };
 
-constexpr int kStepK = 128; // values of the long axis in one step of a wave
+constexpr int kStepK = 128;   // values of the long axis in one step of a workgroup of many rows
+constexpr int kFewStep = 256; // and of a wave of few
+constexpr int kCus = 256;
 
 // How one call is cut into workgroups, from its sizes and types alone.
 struct MatmulPlan {
-    int form;        // which instance of the kernel
-    int parts;       // bf16 parts of x
+    bool many;       // the kernel for many rows of x (else the one for few)
+    bool prepared;   // x is taken from the workspace, in 16-bit parts
+    bool refused;    // more workgroups than a launch holds
+    int parts;       // 16-bit parts of x
     int rows;        // weight rows of a workgroup
     int tokens;      // rows of x of a workgroup
-    int splits;      // workgroups that share a tile's long axis
-    int split_steps; // steps of each
-    int chunk_steps; // steps whose x is held in LDS at once
-    size_t lds;
-    bool refused;    // more workgroups than a launch holds
-    size_t partials;  // where the partial sums begin in the workspace, behind the parts of x
+    int waves_k;     // few: waves that share the long axis
+    int chunk_steps; // few: steps whose x is held in LDS at once
+    int splits;      // many: workgroups that share a tile's long axis
+    int split_steps; // many: steps of each
+    size_t lds;      // few
+    size_t exponents; // where the rows' exponents begin in the workspace (NVFP4, prepared)
+    size_t partials;  // where the partial sums begin
     size_t workspace; // bytes
 };
 
-MatmulPlan plan_matmul(const MatmulArgs& a);
-hipError_t launch_matmul(const MatmulArgs& a, const MatmulPlan& p);
+hipError_t launch_matmul_nv(const MatmulArgs& a, const MatmulPlan& p);
+hipError_t launch_matmul_mx(const MatmulArgs& a, const MatmulPlan& p);
 
 } // namespace fp4q

@@ -46,17 +46,19 @@ def product64(w, x):
     A product passes through at most `depth` additions: those of the 32 products of a matrix instruction, one for each
     instruction and part of x along the row, and the joining of the waves and splits; an addition inside the matrix
     core may cut instead of rounding, so each is charged 2^-23 of the sum of magnitudes.  Rotated x: log2(block) + 1
-    binary32 roundings of sums within a block, and for bf16 the second part's rounding, half a step of what cutting
-    to the first leaves (2^-7 2^-8).  The step fl32(s S) of a dequantized value is rounded once, where the kernels
-    apply S once at the end: 2^-23."""
+    binary32 roundings of sums within a block.  Parts of x: NVFP4 in f16, rotated bf16 in one (half a step, 2^-11), binary32
+    in two (2^-22), and what falls below f16's range under 2^-38 of the row's largest value; MXFP4 in bf16,
+    rotated bf16 in two (half a step of what cutting to the first leaves, 2^-7 2^-8), binary32 in three (none).  The
+    step fl32(s S) of a dequantized value is rounded once, where the kernels apply S once at the end: 2^-23."""
     v = x.double().numpy()
     n = w.block
     A = np.abs(v)
-    parts, cut = (3, 0.0) if x.dtype == torch.float32 else (1, 0.0)
+    nv = w.fmt == "nvfp4"
+    parts, cut = ((3, 2.0 ** -22 if nv else 0.0) if x.dtype == torch.float32 else (1, 0.0))
     extra = np.zeros_like(v)
     if w.rotate and w.k:
         if x.dtype == torch.bfloat16:
-            parts, cut = 2, 2.0 ** -15
+            parts, cut = 2, 2.0 ** -11 if nv else 2.0 ** -15
         v = blocks_times(v, n)
         whole = np.repeat(A.reshape(-1, n).sum(-1), n).reshape(A.shape) / math.sqrt(n)
         extra = whole * (math.log2(n) + 1) * 2.0 ** -24
@@ -64,6 +66,8 @@ def product64(w, x):
     mag = np.abs(w.values)
     depth = 32 + parts * (w.k / 32 + 1) + 40
     tol = (A @ mag.T) * (depth * 2.0 ** -23 + 2.0 ** -22 + cut) + extra @ mag.T
+    if nv and w.k and len(A):
+        tol = tol + 2.0 ** -38 * A.max(-1, keepdims=True) * mag.sum(-1)
     return v @ w.values.T, tol
 
 

@@ -142,7 +142,7 @@ __device__ __forceinline__ Wide<KIND, ONE> load_wide(__amdgpu_buffer_rsrc_t code
     Wide<KIND, ONE> t;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-        t.c[c] = __builtin_amdgcn_raw_buffer_load_b128(codes, (c_at + 16 * c) | (k + 32 * c < cols ? 0 : kPast), c_to, 0);
+        t.c[c] = __builtin_amdgcn_raw_buffer_load_b128(codes, (c_at + 16 * c) | (k < cols - 32 * c ? 0 : kPast), c_to, 0);
     if constexpr (ONE) {
         const int past = k < cols ? 0 : kPast;
         t.s[0] = KIND == kMxBf16 ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales, s_at | past, s_to, 0)
@@ -150,7 +150,7 @@ __device__ __forceinline__ Wide<KIND, ONE> load_wide(__amdgpu_buffer_rsrc_t code
     } else {
 #pragma unroll
         for (int q = 0; q < 64 / B; ++q)
-            t.s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, (s_at + q) | (k + q * B < cols ? 0 : kPast), s_to, 0);
+            t.s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales, (s_at + q) | (k < cols - q * B ? 0 : kPast), s_to, 0);
     }
     return t;
 }
@@ -519,10 +519,11 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 //   Row 8 q + 4 h + e of a product's 32 rows of W is column 16 h + 4 q + e of y, so that a
 // lane ends with 16 neighbouring columns.
 //   While the products of eight values run, the weights of the next eight are expanded; the
-// last ones' are those of the next step.
+// last ones' are those of the next step.  D steps' x and codes are held or on their way, each
+// in a buffer and registers of its own.
 typedef __attribute__((address_space(3))) void lds_void;
 
-template <Kind KIND, int NW, int TM, int WN, bool ONE>
+template <Kind KIND, int NW, int TM, int WN, int D, bool ONE>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
     constexpr int B = KIND == kMxBf16 ? 32 : 16;
@@ -530,7 +531,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     constexpr int BN = 64 * WN / NW; // columns of y
     constexpr int WC = 64 / NW;      // of a wave
     constexpr int U = kStepK / 8;    // 16-byte units of a row of x
-    __shared__ u32x4 xbuf[2][BM * U];
+    __shared__ u32x4 xbuf[D][BM * U];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, h = lane >> 5;
 
@@ -571,13 +572,13 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 #pragma unroll
     for (int i = 0; i < KINDS; ++i)
         x_unit[i] = (lane & 15) ^ ((4 * (wave * LOADS + i) + quad) & 15);
-    auto load_x_tile = [&](int step, int part, int to) {
+    auto load_x_tile = [&](int step, int part, bool real, int to) {
         const auto src = buffer_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
         const bool whole = (step + 1) * kStepK <= cols;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int row = (wave * LOADS + i) * 4;
-            int at = quad * x_row + x_unit[i % KINDS] * 16;
+            int at = (quad * x_row + x_unit[i % KINDS] * 16) | (real ? 0 : kPast);
             if (!whole) // values past the row's end are zeros
                 at |= step * kStepK + x_unit[i % KINDS] * 8 < cols ? 0 : kPast;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(&xbuf[to][(wave * LOADS + i) * 64]), 16, at,
@@ -599,13 +600,13 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     }
     const int w_row = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
     const int c_at = w_row * crow + 32 * h, s_at = w_row * srow + 64 * h / B;
-    auto load_w = [&](int step, Wide<KIND, ONE> (&t)[2]) {
+    auto load_w = [&](int step, bool real, Wide<KIND, ONE> (&t)[2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
             t[i] = load_wide<KIND, ONE>(codes[w], scales[w], c_at, s_at,
                                         __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2)),
-                                        __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B)), step * kStepK + 64 * h, cols);
+                                        __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B)), real ? step * kStepK + 64 * h : kPast, cols);
         }
     };
 
@@ -618,68 +619,93 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
             for (int e = 0; e < 16; ++e)
                 acc[i][j][e] = 0.0f;
 
-    Wide<KIND, ONE> now[2], next[2];
+    Wide<KIND, ONE> ring[D][2];
     u32x4 wv[2][2];
     uint32_t word[2];
-    auto expand_tile = [&](const Wide<KIND, ONE>& from_w, int j, int i) {
-        if (j == 0)
-            word[i] = scale_word(from_w);
-        wv[j & 1][i] = expand<KIND>(from_w.c[j >> 2][j & 3], factor_of<KIND>(word[i], j));
-    };
-    int step = s0, part = p.parts - 1; // of the next loads
-    auto advance = [&]() {
-        if (part == 0) {
-            part = p.parts;
-            ++step;
-        }
-        --part;
-    };
-    if (turns > 0) {
-        load_w(step, now);
-        load_x_tile(step, part, 0);
-        advance();
-        expand_tile(now[0], 0, 0);
-        expand_tile(now[1], 0, 1);
-    }
-    for (int turn = 0; turn < turns; ++turn) {
-        const int at = turn & 1;
-        __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0): this wave's part of the step's x has arrived
-        __syncthreads();                    // everybody's has, and the other buffer is free
-        if (turn + 1 < turns) {
-            load_w(step, next);
-            load_x_tile(step, part, at ^ 1);
-            advance();
-        }
-        auto read_x = [&](int i) { // the i-th of the step's reads
-            const int row = 32 * (i % TM) + n;
-            return xbuf[at][row * U + ((8 * h + i / TM) ^ (n & 15))];
-        };
-        u32x4 xv[kReadAhead];
+    float factor[2];
+    // pairs `at` .. `at` + COUNT - 1 of the eight of values 8 j .. 8 j + 7 of the two tiles
+    auto expand_pairs = [&](const Wide<KIND, ONE> (&t)[2], int j, int at, int count) {
 #pragma unroll
-        for (int i = 0; i < kReadAhead; ++i)
-            xv[i] = read_x(i);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int x_turn = j * TM + i;
-                // the order of these is kept: a read for later, a part of the expansion, the products
-                __builtin_amdgcn_sched_barrier(0);
-                const u32x4 mine = xv[x_turn % kReadAhead];
-                if (x_turn + kReadAhead < 8 * TM)
-                    xv[x_turn % kReadAhead] = read_x(x_turn + kReadAhead);
-                if (i == 0)
-                    expand_tile(j < 7 ? now[0] : next[0], (j + 1) & 7, 0);
-                if (i == TM / 2)
-                    expand_tile(j < 7 ? now[1] : next[1], (j + 1) & 7, 1);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    acc[i][t] = mfma32<KIND>(wv[j & 1][t], mine, acc[i][t]);
+        for (int q = at; q < at + count; ++q) {
+            const int i = q >> 2;
+            if ((q & 3) == 0) {
+                if (j == 0)
+                    word[i] = scale_word(t[i]);
+                factor[i] = factor_of<KIND>(word[i], j);
             }
+            const uint32_t w = t[i].c[j >> 2][j & 3];
+            switch (q & 3) {
+            case 0: wv[j & 1][i].x = expand_pair<KIND, 0>(w, factor[i]); break;
+            case 1: wv[j & 1][i].y = expand_pair<KIND, 1>(w, factor[i]); break;
+            case 2: wv[j & 1][i].z = expand_pair<KIND, 2>(w, factor[i]); break;
+            default: wv[j & 1][i].w = expand_pair<KIND, 3>(w, factor[i]); break;
+            }
+        }
+    };
+    // Loads of a step, whose number never changes: past the last step they are made past
+    // their buffers' ends.
+    int next_step = s0, next_part = p.parts - 1, next_turn = 0;
+    auto load_turn = [&](int to) {
+        const bool real = next_turn < turns;
+        asm volatile("" ::: "memory"); // the loads of two steps keep their order
+        load_w(next_step, real, ring[to]);
+        load_x_tile(next_step, next_part, real, to);
+        asm volatile("" ::: "memory");
+        ++next_turn;
+        if (next_part == 0) {
+            next_part = p.parts;
+            next_step += next_turn < turns ? 1 : 0;
+        }
+        --next_part;
+    };
+    constexpr int PER = LOADS + 4 + 2 * Wide<KIND, ONE>::NS; // loads of a step
+    static_assert((D - 2) * PER < 64, "what the counter of loads holds");
+    if (turns > 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            now[i] = next[i];
+        for (int d = 0; d < D - 1; ++d)
+            load_turn(d);
+        expand_pairs(ring[0], 0, 0, 8);
     }
+    for (int base = 0; base < turns; base += D)
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (base + d >= turns)
+                break;
+            // of this wave's loads only those of the D - 2 later steps are on their way still;
+            // after the barrier that holds for every wave, and the buffer of the step before
+            // this one is free: its reads have all been used by products (__syncthreads would
+            // wait for the later steps too)
+            constexpr int STAY = (D - 2) * PER;
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x0F70 | (STAY & 15) | ((STAY >> 4) << 14)); // vmcnt alone
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            load_turn((d + D - 1) % D);
+            auto read_x = [&](int i) { // the i-th of the step's reads
+                const int row = 32 * (i % TM) + n;
+                return xbuf[d][row * U + ((8 * h + i / TM) ^ (n & 15))];
+            };
+            u32x4 xv[kReadAhead];
+#pragma unroll
+            for (int i = 0; i < kReadAhead; ++i)
+                xv[i] = read_x(i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int x_turn = j * TM + i;
+                    const u32x4 mine = xv[x_turn % kReadAhead];
+                    if (x_turn + kReadAhead < 8 * TM)
+                        xv[x_turn % kReadAhead] = read_x(x_turn + kReadAhead);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        // the order of these is kept: a product, and what is expanded while it runs
+                        __builtin_amdgcn_sched_barrier(0);
+                        acc[i][t] = mfma32<KIND>(wv[j & 1][t], mine, acc[i][t]);
+                        expand_pairs(ring[j < 7 ? d : (d + 1) % D], (j + 1) & 7, (2 * i + t) * (4 / TM), 4 / TM);
+                    }
+                }
+        }
 
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -764,15 +790,15 @@ void many_form(const MatmulArgs& a, const MatmulPlan& p)
     const dim3 grid(tiles_n * tiles_m, 1, (uint32_t)p.splits);
     const bool one = scales_together(a);
     switch (p.tokens) {
-#define FP4Q_MANY(TM)                                                                    \
+#define FP4Q_MANY(TM, D)                                                                 \
     if (one)                                                                             \
-        matmul_many<KIND, NW, TM, 4, true><<<grid, 256, 0, a.stream>>>(a, p);            \
+        matmul_many<KIND, NW, TM, 4, D, true><<<grid, 256, 0, a.stream>>>(a, p);         \
     else                                                                                 \
-        matmul_many<KIND, NW, TM, 4, false><<<grid, 256, 0, a.stream>>>(a, p);           \
+        matmul_many<KIND, NW, TM, 4, D, false><<<grid, 256, 0, a.stream>>>(a, p);        \
     break;
-    case 32: FP4Q_MANY(1)
-    case 64: FP4Q_MANY(2)
-    default: FP4Q_MANY(4)
+    case 32: FP4Q_MANY(1, 2)
+    case 64: FP4Q_MANY(2, 2)
+    default: FP4Q_MANY(4, 2)
 #undef FP4Q_MANY
     }
 }

@@ -127,6 +127,39 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+// The resource as words, and 16 or 4 bytes of every lane from there to LDS, the lanes' in order from
+// `to` on (uniform).  The compiler's own form of these loads makes it wait for all of them
+// before any read of LDS in a loop; of these it knows nothing, and the caller waits.
+__device__ __forceinline__ u32x4 words_of(const void* p, int64_t bytes)
+{
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xFFFFu),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00027000u};
+}
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm" // m0 is named as written, though nothing is kept there
+template <int BYTES>
+__device__ __forceinline__ void load_to_lds(u32x4 from, void* to, int at)
+{
+    const uint32_t place = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)to);
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(place), "v"(at), "s"(from) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(place), "v"(at), "s"(from) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// the loads past the last step have to be over before the workgroup's LDS is another's
+__device__ __forceinline__ void all_loads_over()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
 // OR-ed to an offset, past every buffer's end (a select would become a branch
 // around the load)
 constexpr int kPast = 0x7FFFFFFF;
@@ -342,12 +375,15 @@ __device__ __forceinline__ f32x4* partial_of(const MatmulArgs& a, const MatmulPl
 //
 // A workgroup of RW x KW waves takes 16 RW rows of the weight (of each of two) and up to 16
 // rows of x; RW waves share the rows, KW the long axis, 256 values a step.  W is the
-// first operand of 16x16x32 products: lane n + 16 g loads the 32 bytes of row n that hold
+// first operand of 16x16x32 products: lane n + 16 g has the 32 bytes of row n that hold
 // values 64 g .. 64 g + 63 of a step and gives them to eight products, eight at a
-// time; x comes from LDS, where the whole workgroup put it (CONV: rotated and cut into bf16
-// parts on the way; else as it is, or as matmul_parts and matmul_halves left it).  The
-// codes of the next kAhead steps are on their way while a step is computed.
-constexpr int kAhead = 2;
+// time.  In memory neighbouring lanes would so read rows apart, an access of the cache each;
+// the codes are therefore loaded into LDS directly, eight neighbouring lanes 128 bytes of a row,
+// and read from there (each wave its own: no barrier; 16-byte units are exchanged by an XOR
+// with the row, so that 16 rows' meet all banks).  kStages steps are held or on their way.
+// x comes from LDS too, where the whole workgroup put it (CONV: rotated and cut into bf16
+// parts on the way; else as it is, or as matmul_parts and matmul_halves left it).
+constexpr int kStages = 3;
 
 template <Kind KIND, int NW, int PARTS, bool CONV, int RW, int KW, bool ONE>
 __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, const MatmulPlan p)
@@ -355,7 +391,11 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     constexpr int B = KIND == kMxBf16 ? 32 : 16;
     constexpr int T = 64 * RW * KW;
     constexpr int U = kFewStep / 8; // 16-byte units of x in a step
+    constexpr int NS = Wide<KIND, ONE>::NS;
+    constexpr bool MX = KIND == kMxBf16;
     extern __shared__ u32x4 lds[];
+    __shared__ u32x4 cbuf[RW * KW][kStages][NW][16 * 8]; // by wave
+    __shared__ uint32_t sbuf[RW * KW][kStages][NW][ONE ? 64 : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
     const int rw = wave % RW, kw = wave / RW;
@@ -368,24 +408,49 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     const int64_t left = a.n - nw;
     const int live = left <= 0 ? 0 : (int)(left < 16 ? left : 16);
     const int crow = cols / 2, srow = cols / B;
-    __amdgpu_buffer_rsrc_t codes[NW], scales[NW];
+    const int64_t first = live > 0 ? nw : 0;
+    u32x4 codes[NW];
+    __amdgpu_buffer_rsrc_t scales[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const int64_t first = live > 0 ? nw : 0;
-        codes[w] = buffer_of(a.codes[w] + first * crow, live * crow);
+        codes[w] = words_of(a.codes[w] + first * crow, live * crow);
         scales[w] = buffer_of(a.scales[w] + first * srow, live * srow);
     }
-    auto load = [&](int step, Wide<KIND, ONE> (&t)[NW]) {
-        const int k = step * kFewStep + 64 * g;
+    // one step's loads, whose number never changes: past the row's end any codes, with scales of
+    // zero; past the last step past the buffers' ends
+    constexpr int PER = NW * (2 + NS);
+    int c_unit[2], c_row[2]; // of this lane's 16 bytes of each load
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-            t[w] = load_wide<KIND, ONE>(codes[w], scales[w], r * crow + k / 2, r * srow + k / B, 0, 0, k, cols);
+    for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + (lane >> 3);
+        c_unit[i] = (lane & 7) ^ ((row >> 1) & 7);
+        c_row[i] = row * crow;
+    }
+    const int s_row = MX ? (lane >> 1) & 15 : lane >> 2, s_dword = MX ? lane & 1 : lane & 3;
+    uint32_t bytes[kStages][NW][NS];
+    auto load = [&](int step, int to) {
+        asm volatile("" ::: "memory"); // the loads of two steps keep their order
+        const int k = step * kFewStep;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                load_to_lds<16>(codes[w], &cbuf[wave][to][w][64 * i], (c_row[i] + k / 2 + c_unit[i] * 16) | (k < cols - c_unit[i] * 32 ? 0 : kPast));
+            if constexpr (ONE) {
+                load_to_lds<4>(words_of(a.scales[w] + first * srow, live * srow), &sbuf[wave][to][w][0],
+                               (s_row * srow + k / B + 4 * s_dword) | (k < cols - 4 * B * s_dword && !(MX && lane >= 32) ? 0 : kPast));
+            } else {
+                const int at = r * srow + (k + 64 * g) / B;
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+                    bytes[to][w][q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], (at + q) | (k < cols - 64 * g - q * B ? 0 : kPast), 0, 0);
+            }
+        }
+        asm volatile("" ::: "memory");
     };
-
-    Wide<KIND, ONE> ring[kAhead][NW];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        load(kw + KW * i, ring[i]);
+    for (int i = 0; i < kStages - 1; ++i)
+        load(kw + KW * i, i);
 
     // x of chunk_steps steps from step `from` on: [part][row][value], rows padded
     // by 16 bytes so that 16 rows meet all banks
@@ -442,9 +507,9 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     const int turns = p.chunk_steps / KW; // of this wave in a chunk
     const int all = (steps + KW - 1) / KW; // the same for every wave of the workgroup
     int in_chunk = turns;
-    for (int base = 0; base < all; base += kAhead) {
+    for (int base = 0; base < all; base += kStages) {
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
+        for (int d = 0; d < kStages; ++d) {
             const int i = base + d;
             if (i >= all)
                 break;
@@ -456,10 +521,28 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
                 in_chunk = 0;
             }
             const u32x4* x = lds + (in_chunk * KW + kw) * U + x_at;
+            load(kw + KW * (i + kStages - 1), (d + kStages - 1) % kStages);
+            // this step's loads have arrived; those of the later ones may still be on their way
+            constexpr int STAY = (kStages - 1) * PER;
+            static_assert(STAY < 64, "what the counter of loads holds");
+            __builtin_amdgcn_s_waitcnt(0x0F70 | (STAY & 15) | ((STAY >> 4) << 14)); // vmcnt alone
+            asm volatile("" ::: "memory");
+            Wide<KIND, ONE> t[NW];
             uint32_t word[NW];
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                word[w] = scale_word(ring[d][w]);
+            for (int w = 0; w < NW; ++w) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    t[w].c[c] = cbuf[wave][d][w][r * 8 + ((2 * g + c) ^ ((r >> 1) & 7))];
+                if constexpr (ONE) {
+                    word[w] = MX ? (sbuf[wave][d][w][2 * r + (g >> 1)] >> (16 * (g & 1))) & 0xFFFFu : sbuf[wave][d][w][4 * r + g];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NS; ++q)
+                        t[w].s[q] = bytes[d][w][q];
+                    word[w] = scale_word(t[w]);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 u32x4 xv[PARTS];
@@ -468,17 +551,18 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
                     xv[q] = x[q * mt * stride + j];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    const u32x4 wv = expand<KIND>(ring[d][w].c[j >> 2][j & 3], factor_of<KIND>(word[w], j));
+                    const u32x4 wv = expand<KIND>(t[w].c[j >> 2][j & 3], factor_of<KIND>(word[w], j));
 #pragma unroll
                     for (int q = PARTS - 1; q >= 0; --q) // small parts first
                         acc[w] = mfma16<KIND>(wv, xv[q], acc[w]);
                 }
             }
-            load(kw + KW * (i + kAhead), ring[d]);
+            asm volatile("" ::: "memory"); // the next load into this stage comes after these reads
             ++in_chunk;
         }
     }
 
+    all_loads_over();
     // join the waves that share rows, in order
     __syncthreads();
     f32x4* red = reinterpret_cast<f32x4*>(lds);
@@ -521,8 +605,6 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 //   While the products of eight values run, the weights of the next eight are expanded; the
 // last ones' are those of the next step.  D steps' x and codes are held or on their way, each
 // in a buffer and registers of its own.
-typedef __attribute__((address_space(3))) void lds_void;
-
 template <Kind KIND, int NW, int TM, int WN, int D, bool ONE>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
@@ -706,6 +788,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
                     }
                 }
         }
+    all_loads_over();
 
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -755,13 +838,13 @@ __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const Mat
 
 // ---- launch -------------------------------------------------------------------------------
 
-// whether the scale bytes of 64 values can be loaded at once in every row
+// whether the scale bytes of every row can be loaded four at a time
 inline bool scales_together(const MatmulArgs& a)
 {
     uintptr_t places = (uintptr_t)(a.k / (a.mx ? 32 : 16));
     for (int w = 0; w < a.weights; ++w)
         places |= reinterpret_cast<uintptr_t>(a.scales[w]);
-    return places % (a.mx ? 2 : 4) == 0;
+    return places % 4 == 0;
 }
 
 template <Kind KIND, int NW, int PARTS, bool CONV>

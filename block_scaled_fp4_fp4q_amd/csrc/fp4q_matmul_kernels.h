@@ -142,13 +142,13 @@ __device__ __forceinline__ u32x4 words_of(const void* p, int64_t bytes)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm" // m0 is named as written, though nothing is kept there
 template <int BYTES>
-__device__ __forceinline__ void load_to_lds(u32x4 from, void* to, int at)
+__device__ __forceinline__ void load_to_lds(u32x4 from, void* to, int at, int uniform = 0)
 {
     const uint32_t place = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)to);
     if constexpr (BYTES == 16)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(place), "v"(at), "s"(from) : "memory", "m0");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(place), "v"(at), "s"(from), "s"(uniform) : "memory", "m0");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(place), "v"(at), "s"(from) : "memory", "m0");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(place), "v"(at), "s"(from), "s"(uniform) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -613,7 +613,12 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     constexpr int BN = 64 * WN / NW; // columns of y
     constexpr int WC = 64 / NW;      // of a wave
     constexpr int U = kStepK / 8;    // 16-byte units of a row of x
+    constexpr bool MX = KIND == kMxBf16;
+    constexpr bool STAGED = TM <= 2; // codes through LDS
+    constexpr int NS = Wide<KIND, ONE>::NS;
     __shared__ u32x4 xbuf[D][BM * U];
+    __shared__ u32x4 cbuf[STAGED ? WN : 1][D][STAGED ? 64 * 4 : 1];
+    __shared__ uint32_t sbuf[STAGED && ONE ? WN : 1][D][STAGED && ONE ? (MX ? 64 : 128) : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, h = lane >> 5;
 
@@ -655,7 +660,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     for (int i = 0; i < KINDS; ++i)
         x_unit[i] = (lane & 15) ^ ((4 * (wave * LOADS + i) + quad) & 15);
     auto load_x_tile = [&](int step, int part, bool real, int to) {
-        const auto src = buffer_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
+        const u32x4 src = words_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
         const bool whole = (step + 1) * kStepK <= cols;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -663,8 +668,8 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
             int at = (quad * x_row + x_unit[i % KINDS] * 16) | (real ? 0 : kPast);
             if (!whole) // values past the row's end are zeros
                 at |= step * kStepK + x_unit[i % KINDS] * 8 < cols ? 0 : kPast;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)(&xbuf[to][(wave * LOADS + i) * 64]), 16, at,
-                                                     __builtin_amdgcn_readfirstlane((row < rows ? row : 0) * x_row + step * (kStepK * 2)), 0, 0);
+            load_to_lds<16>(src, &xbuf[to][(wave * LOADS + i) * 64], at,
+                            __builtin_amdgcn_readfirstlane((row < rows ? row : 0) * x_row + step * (kStepK * 2)));
         }
     };
 
@@ -680,17 +685,68 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         codes[w] = buffer_of(a.codes[w] + from * crow, live * crow);
         scales[w] = buffer_of(a.scales[w] + from * srow, live * srow);
     }
-    const int w_row = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
+    auto row_of = [](int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }; // of a product's
+    const int w_row = row_of(n);
     const int c_at = w_row * crow + 32 * h, s_at = w_row * srow + 64 * h / B;
-    auto load_w = [&](int step, bool real, Wide<KIND, ONE> (&t)[2]) {
+    // STAGED: 16 lanes load 16 rows' 64 bytes of codes, four neighbouring ones a row's (an access
+    // of the cache for each row, not for each lane), 16-byte units exchanged by an XOR with the
+    // row; the scales four bytes a lane
+    int c_unit[2], c_row[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 16 * i + (lane >> 2);
+        c_unit[i] = (lane & 3) ^ ((row >> 2) & 3);
+        c_row[i] = row_of(row) * crow;
+    }
+    auto load_w = [&](int step, bool real, int to, Wide<KIND, ONE> (&t)[2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
-            t[i] = load_wide<KIND, ONE>(codes[w], scales[w], c_at, s_at,
-                                        __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2)),
-                                        __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B)), real ? step * kStepK + 64 * h : kPast, cols);
+            const int c_to = __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2));
+            const int s_to = __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B));
+            const int k = real ? step * kStepK : kPast / 2;
+            if constexpr (!STAGED) {
+                t[i] = load_wide<KIND, ONE>(codes[w], scales[w], c_at, s_at, c_to, s_to, k + 64 * h, cols);
+                continue;
+            }
+            const u32x4 from_c = words_of(a.codes[w] + from * crow, live * crow);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                load_to_lds<16>(from_c, &cbuf[wave][to][128 * i + 64 * c], (c_row[c] + c_unit[c] * 16) | (k < cols - c_unit[c] * 32 ? 0 : kPast),
+                                c_to);
+            if constexpr (!ONE) {
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+                    t[i].s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], (s_at + q) | (k + 64 * h < cols - q * B ? 0 : kPast), s_to, 0);
+            } else if constexpr (MX) { // one dword a row: 32 lanes
+                load_to_lds<4>(words_of(a.scales[w] + from * srow, live * srow), &sbuf[wave][to][32 * i],
+                               (row_of(n) * srow) | (k < cols && lane < 32 ? 0 : kPast), s_to);
+            } else {
+                const int r = lane >> 1, half = lane & 1;
+                load_to_lds<4>(words_of(a.scales[w] + from * srow, live * srow), &sbuf[wave][to][64 * i],
+                               (row_of(r) * srow + 4 * half) | (k < cols - 64 * half ? 0 : kPast), s_to);
+            }
         }
     };
+    // STAGED: this lane's codes and scales of a step, once they have arrived
+    auto take_w = [&](int at, Wide<KIND, ONE> (&t)[2]) {
+        if constexpr (STAGED) {
+            // the step's x, loaded after them, may still be on its way
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x0F70 | LOADS);
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    t[i].c[c] = cbuf[wave][at][(32 * i + n) * 4 + ((2 * h + c) ^ ((n >> 2) & 3))];
+                if constexpr (ONE)
+                    t[i].s[0] = MX ? (sbuf[wave][at][32 * i + n] >> (16 * h)) & 0xFFFFu : sbuf[wave][at][2 * (32 * i + n) + h];
+            }
+            asm volatile("" ::: "memory");
+        }
+    };
+    static_assert(LOADS < 16 && (!STAGED || D == 2), "what take_w waits for");
 
     f32x16 acc[TM][2];
 #pragma unroll
@@ -730,7 +786,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     auto load_turn = [&](int to) {
         const bool real = next_turn < turns;
         asm volatile("" ::: "memory"); // the loads of two steps keep their order
-        load_w(next_step, real, ring[to]);
+        load_w(next_step, real, to, ring[to]);
         load_x_tile(next_step, next_part, real, to);
         asm volatile("" ::: "memory");
         ++next_turn;
@@ -740,12 +796,13 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         }
         --next_part;
     };
-    constexpr int PER = LOADS + 4 + 2 * Wide<KIND, ONE>::NS; // loads of a step
+    constexpr int PER = LOADS + 4 + 2 * NS; // loads of a step
     static_assert((D - 2) * PER < 64, "what the counter of loads holds");
     if (turns > 0) {
 #pragma unroll
         for (int d = 0; d < D - 1; ++d)
             load_turn(d);
+        take_w(0, ring[0]);
         expand_pairs(ring[0], 0, 0, 8);
     }
     for (int base = 0; base < turns; base += D)
@@ -776,6 +833,8 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     const int x_turn = j * TM + i;
+                    if (j == 6 && i == 0)
+                        take_w((d + 1) % D, ring[(d + 1) % D]);
                     const u32x4 mine = xv[x_turn % kReadAhead];
                     if (x_turn + kReadAhead < 8 * TM)
                         xv[x_turn % kReadAhead] = read_x(x_turn + kReadAhead);

@@ -124,27 +124,31 @@ __device__ __forceinline__ float factor_of(uint32_t word, int j)
 // gives zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
 
 // The resource as words, and 16 or 4 bytes of every lane from there to LDS, the lanes' in order from
-// `to` on (uniform).  The compiler's own form of these loads makes it wait for all of them
+// `place` on (uniform, as lds_place gives it).  The compiler's own form of these loads makes it wait for all of them
 // before any read of LDS in a loop; of these it knows nothing, and the caller waits.
 __device__ __forceinline__ u32x4 words_of(const void* p, int64_t bytes)
 {
     const uint64_t at = reinterpret_cast<uint64_t>(p);
-    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xFFFFu),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00027000u};
+    return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, 0x00027000u};
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t lds_place(T& array)
+{
+    return (uint32_t)(uintptr_t)(lds_void*)&array;
 }
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm" // m0 is named as written, though nothing is kept there
 template <int BYTES>
-__device__ __forceinline__ void load_to_lds(u32x4 from, void* to, int at, int uniform = 0)
+__device__ __forceinline__ void load_to_lds(u32x4 from, uint32_t place, int at, int uniform = 0)
 {
-    const uint32_t place = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)to);
     if constexpr (BYTES == 16)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(place), "v"(at), "s"(from), "s"(uniform) : "memory", "m0");
     else
@@ -363,12 +367,22 @@ __device__ __forceinline__ f32x4 finish4(const MatmulArgs& a, const MatmulPlan& 
     return r;
 }
 
-// partial sums of split s: [weight][m][n, padded to four]
-__device__ __forceinline__ f32x4* partial_of(const MatmulArgs& a, const MatmulPlan& p, int s, int w, int64_t m, int64_t n)
+// eight values of row m of y from column n (a multiple of eight) on
+__device__ __forceinline__ void store8(const MatmulArgs& a, int64_t m, int64_t n, f32x4 u, f32x4 v)
 {
-    const int64_t wide = (a.n + 3) & ~(int64_t)3;
-    float* sums = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partials);
-    return reinterpret_cast<f32x4*>(sums + (((int64_t)s * a.weights + w) * a.m + m) * wide + n);
+    if (a.y_wide && a.bf16 && n + 8 <= a.n) {
+        const u32x4 w = u32x4{bf16_pair(u.x, u.y), bf16_pair(u.z, u.w), bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(a.y) + m * a.y_row + n, 8), &w, 16);
+        return;
+    }
+    store4(a, m, n, u);
+    if (n + 4 < a.n)
+        store4(a, m, n + 4, v);
+}
+
+__device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulPlan& p)
+{
+    return reinterpret_cast<f32x4*>(static_cast<char*>(a.workspace) + p.partials);
 }
 
 // ---- few rows of x ------------------------------------------------------------------
@@ -428,6 +442,7 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     }
     const int s_row = MX ? (lane >> 1) & 15 : lane >> 2, s_dword = MX ? lane & 1 : lane & 3;
     uint32_t bytes[kStages][NW][NS];
+    const uint32_t c_place = lds_place(cbuf), s_place = lds_place(sbuf);
     auto load = [&](int step, int to) {
         asm volatile("" ::: "memory"); // the loads of two steps keep their order
         const int k = step * kFewStep;
@@ -435,9 +450,9 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
         for (int w = 0; w < NW; ++w) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                load_to_lds<16>(codes[w], &cbuf[wave][to][w][64 * i], (c_row[i] + k / 2 + c_unit[i] * 16) | (k < cols - c_unit[i] * 32 ? 0 : kPast));
+                load_to_lds<16>(codes[w], c_place + (((wave * kStages + to) * NW + w) * 128 + 64 * i) * 16, (c_row[i] + k / 2 + c_unit[i] * 16) | (k < cols - c_unit[i] * 32 ? 0 : kPast));
             if constexpr (ONE) {
-                load_to_lds<4>(words_of(a.scales[w] + first * srow, live * srow), &sbuf[wave][to][w][0],
+                load_to_lds<4>(words_of(a.scales[w] + first * srow, live * srow), s_place + ((wave * kStages + to) * NW + w) * 256,
                                (s_row * srow + k / B + 4 * s_dword) | (k < cols - 4 * B * s_dword && !(MX && lane >= 32) ? 0 : kPast));
             } else {
                 const int at = r * srow + (k + 64 * g) / B;
@@ -605,25 +620,40 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 //   While the products of eight values run, the weights of the next eight are expanded; the
 // last ones' are those of the next step.  D steps' x and codes are held or on their way, each
 // in a buffer and registers of its own.
-template <Kind KIND, int NW, int TM, int WN, int D, bool ONE>
+constexpr int WN = 4; // waves of a workgroup
+constexpr int TN = 2; // products of 32 weight rows in a wave
+
+// the tile of number id: eight rows of tiles at a time, the rows fastest
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t& m, uint32_t& n)
+{
+    constexpr uint32_t kGroup = 8;
+    const uint32_t band = id / (kGroup * tiles_n), first = band * kGroup;
+    const uint32_t high = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+    const uint32_t in = id - band * kGroup * tiles_n;
+    // (division is the vector unit's: the results are brought back to scalar registers)
+    m = __builtin_amdgcn_readfirstlane(first + in % high);
+    n = __builtin_amdgcn_readfirstlane(in / high);
+}
+
+template <Kind KIND, int NW, int TM, bool ONE>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
     constexpr int B = KIND == kMxBf16 ? 32 : 16;
     constexpr int BM = 32 * TM;
-    constexpr int BN = 64 * WN / NW; // columns of y
-    constexpr int WC = 64 / NW;      // of a wave
+    constexpr int D = 2;             // steps held
+    constexpr int WC = 32 * TN / NW; // columns of y of a wave
+    constexpr int BN = WC * WN;
     constexpr int U = kStepK / 8;    // 16-byte units of a row of x
     constexpr bool MX = KIND == kMxBf16;
-    constexpr bool STAGED = TM <= 2; // codes through LDS
+    constexpr bool STAGED = TM <= 2;     // codes through LDS
     constexpr int NS = Wide<KIND, ONE>::NS;
     __shared__ u32x4 xbuf[D][BM * U];
-    __shared__ u32x4 cbuf[STAGED ? WN : 1][D][STAGED ? 64 * 4 : 1];
-    __shared__ uint32_t sbuf[STAGED && ONE ? WN : 1][D][STAGED && ONE ? (MX ? 64 : 128) : 1];
+    __shared__ u32x4 cbuf[STAGED ? WN : 1][D][STAGED ? 128 * TN : 1];
+    __shared__ uint32_t sbuf[STAGED && ONE ? WN : 1][D][STAGED && ONE ? 64 * TN : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = lane & 31, h = lane >> 5;
 
-    // workgroups of one XCD (every eighth) take neighbouring tiles: kGroup rows of tiles at a
-    // time, the rows of tiles fastest
+    // workgroups of one XCD (every eighth) take neighbouring tiles
     const uint32_t tiles_m = (uint32_t)((a.m + BM - 1) / BM), tiles_n = (uint32_t)((a.n + BN - 1) / BN);
     const uint32_t all = tiles_m * tiles_n;
     uint32_t id = blockIdx.x;
@@ -631,11 +661,9 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         const uint32_t xcd = id % 8, per = all / 8, more = all % 8;
         id = xcd * per + (xcd < more ? xcd : more) + id / 8;
     }
-    constexpr uint32_t kGroup = 8;
-    const uint32_t band = id / (kGroup * tiles_n), first = band * kGroup;
-    const uint32_t high = tiles_m - first < kGroup ? tiles_m - first : kGroup;
-    const uint32_t in = id - band * kGroup * tiles_n;
-    const int64_t m0 = (int64_t)(first + in % high) * BM, n0 = (int64_t)(in / high) * BN;
+    uint32_t tile_m, tile_n;
+    tile_of(id, tiles_m, tiles_n, tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
 
     const int cols = (int)a.k;
     const int steps = (cols + kStepK - 1) / kStepK;
@@ -659,6 +687,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 #pragma unroll
     for (int i = 0; i < KINDS; ++i)
         x_unit[i] = (lane & 15) ^ ((4 * (wave * LOADS + i) + quad) & 15);
+    const uint32_t x_place = lds_place(xbuf), c_place = lds_place(cbuf), s_place = lds_place(sbuf);
     auto load_x_tile = [&](int step, int part, bool real, int to) {
         const u32x4 src = words_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
         const bool whole = (step + 1) * kStepK <= cols;
@@ -668,8 +697,8 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
             int at = (quad * x_row + x_unit[i % KINDS] * 16) | (real ? 0 : kPast);
             if (!whole) // values past the row's end are zeros
                 at |= step * kStepK + x_unit[i % KINDS] * 8 < cols ? 0 : kPast;
-            load_to_lds<16>(src, &xbuf[to][(wave * LOADS + i) * 64], at,
-                            __builtin_amdgcn_readfirstlane((row < rows ? row : 0) * x_row + step * (kStepK * 2)));
+            load_to_lds<16>(src, x_place + (to * BM * U + (wave * LOADS + i) * 64) * 16, at,
+                            (row < rows ? row : 0) * x_row + step * (kStepK * 2));
         }
     };
 
@@ -698,12 +727,11 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         c_unit[i] = (lane & 3) ^ ((row >> 2) & 3);
         c_row[i] = row_of(row) * crow;
     }
-    auto load_w = [&](int step, bool real, int to, Wide<KIND, ONE> (&t)[2]) {
+    auto load_w = [&](int step, bool real, int to, Wide<KIND, ONE> (&t)[TN]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int w = NW == 2 ? i : 0, row = NW == 2 ? 0 : 32 * i, up = row < live ? row : 0;
-            const int c_to = __builtin_amdgcn_readfirstlane(up * crow + step * (kStepK / 2));
-            const int s_to = __builtin_amdgcn_readfirstlane(up * srow + step * (kStepK / B));
+        for (int i = 0; i < TN; ++i) {
+            const int w = NW == 2 ? i / (TN / 2) : 0, row = 32 * (NW == 2 ? i % (TN / 2) : i), up = row < live ? row : 0;
+            const int c_to = up * crow + step * (kStepK / 2), s_to = up * srow + step * (kStepK / B);
             const int k = real ? step * kStepK : kPast / 2;
             if constexpr (!STAGED) {
                 t[i] = load_wide<KIND, ONE>(codes[w], scales[w], c_at, s_at, c_to, s_to, k + 64 * h, cols);
@@ -712,57 +740,54 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
             const u32x4 from_c = words_of(a.codes[w] + from * crow, live * crow);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                load_to_lds<16>(from_c, &cbuf[wave][to][128 * i + 64 * c], (c_row[c] + c_unit[c] * 16) | (k < cols - c_unit[c] * 32 ? 0 : kPast),
+                load_to_lds<16>(from_c, c_place + ((wave * D + to) * 128 * TN + 128 * i + 64 * c) * 16, (c_row[c] + c_unit[c] * 16) | (k < cols - c_unit[c] * 32 ? 0 : kPast),
                                 c_to);
             if constexpr (!ONE) {
 #pragma unroll
                 for (int q = 0; q < NS; ++q)
                     t[i].s[q] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(scales[w], (s_at + q) | (k + 64 * h < cols - q * B ? 0 : kPast), s_to, 0);
-            } else if constexpr (MX) { // one dword a row: 32 lanes
-                load_to_lds<4>(words_of(a.scales[w] + from * srow, live * srow), &sbuf[wave][to][32 * i],
+            } else if constexpr (MX) { // a dword a row: 32 lanes, the others bring zeros
+                load_to_lds<4>(words_of(a.scales[w] + from * srow, live * srow), s_place + ((wave * D + to) * 64 * TN + 64 * i) * 4,
                                (row_of(n) * srow) | (k < cols && lane < 32 ? 0 : kPast), s_to);
             } else {
                 const int r = lane >> 1, half = lane & 1;
-                load_to_lds<4>(words_of(a.scales[w] + from * srow, live * srow), &sbuf[wave][to][64 * i],
+                load_to_lds<4>(words_of(a.scales[w] + from * srow, live * srow), s_place + ((wave * D + to) * 64 * TN + 64 * i) * 4,
                                (row_of(r) * srow + 4 * half) | (k < cols - 64 * half ? 0 : kPast), s_to);
             }
         }
     };
-    // STAGED: this lane's codes and scales of a step, once they have arrived
-    auto take_w = [&](int at, Wide<KIND, ONE> (&t)[2]) {
-        if constexpr (STAGED) {
-            // the step's x, loaded after them, may still be on its way
+    // STAGED: half of this lane's codes of a step; with the first half, for which the step's
+    // loads must have arrived (but for those of x, which are the last ones), the scales
+    auto take_half = [&](int at, int c, Wide<KIND, ONE> (&t)[TN]) {
+        if (c == 0) {
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_waitcnt(0x0F70 | LOADS);
             asm volatile("" ::: "memory");
+        }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    t[i].c[c] = cbuf[wave][at][(32 * i + n) * 4 + ((2 * h + c) ^ ((n >> 2) & 3))];
-                if constexpr (ONE)
-                    t[i].s[0] = MX ? (sbuf[wave][at][32 * i + n] >> (16 * h)) & 0xFFFFu : sbuf[wave][at][2 * (32 * i + n) + h];
-            }
-            asm volatile("" ::: "memory");
+        for (int i = 0; i < TN; ++i) {
+            t[i].c[c] = cbuf[wave][at][(32 * i + n) * 4 + ((2 * h + c) ^ ((n >> 2) & 3))];
+            if (ONE && c == 0)
+                t[i].s[0] = MX ? (sbuf[wave][at][64 * i + n] >> (16 * h)) & 0xFFFFu : sbuf[wave][at][2 * (32 * i + n) + h];
         }
     };
-    static_assert(LOADS < 16 && (!STAGED || D == 2), "what take_w waits for");
+    static_assert(LOADS < 16, "what take_half waits for");
 
-    f32x16 acc[TM][2];
+    f32x16 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 acc[i][j][e] = 0.0f;
 
-    Wide<KIND, ONE> ring[D][2];
-    u32x4 wv[2][2];
-    uint32_t word[2];
-    float factor[2];
-    // pairs `at` .. `at` + COUNT - 1 of the eight of values 8 j .. 8 j + 7 of the two tiles
-    auto expand_pairs = [&](const Wide<KIND, ONE> (&t)[2], int j, int at, int count) {
+    Wide<KIND, ONE> ring[D][TN];
+    u32x4 wv[2][TN];
+    uint32_t word[TN];
+    float factor[TN];
+    // pairs `at` .. `at` + COUNT - 1 of those of values 8 j .. 8 j + 7, four a tile
+    auto expand_pairs = [&](const Wide<KIND, ONE> (&t)[TN], int j, int at, int count) {
 #pragma unroll
         for (int q = at; q < at + count; ++q) {
             const int i = q >> 2;
@@ -796,14 +821,15 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         }
         --next_part;
     };
-    constexpr int PER = LOADS + 4 + 2 * NS; // loads of a step
+    constexpr int PER = LOADS + TN * (2 + NS); // loads of a step
     static_assert((D - 2) * PER < 64, "what the counter of loads holds");
     if (turns > 0) {
 #pragma unroll
         for (int d = 0; d < D - 1; ++d)
             load_turn(d);
-        take_w(0, ring[0]);
-        expand_pairs(ring[0], 0, 0, 8);
+        if constexpr (STAGED)
+            take_half(0, 0, ring[0]);
+        expand_pairs(ring[0], 0, 0, 4 * TN);
     }
     for (int base = 0; base < turns; base += D)
 #pragma unroll
@@ -833,66 +859,99 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     const int x_turn = j * TM + i;
-                    if (j == 6 && i == 0)
-                        take_w((d + 1) % D, ring[(d + 1) % D]);
+                    if (STAGED && i == 0 && j == 2)
+                        take_half(d, 1, ring[d]);
+                    if (STAGED && i == 0 && j == 6)
+                        take_half((d + 1) % D, 0, ring[(d + 1) % D]);
                     const u32x4 mine = xv[x_turn % kReadAhead];
                     if (x_turn + kReadAhead < 8 * TM)
                         xv[x_turn % kReadAhead] = read_x(x_turn + kReadAhead);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                    for (int t = 0; t < TN; ++t) {
                         // the order of these is kept: a product, and what is expanded while it runs
                         __builtin_amdgcn_sched_barrier(0);
                         acc[i][t] = mfma32<KIND>(wv[j & 1][t], mine, acc[i][t]);
-                        expand_pairs(ring[j < 7 ? d : (d + 1) % D], (j + 1) & 7, (2 * i + t) * (4 / TM), 4 / TM);
+                        expand_pairs(ring[j < 7 ? d : (d + 1) % D], (j + 1) & 7, (TN * i + t) * (4 / TM), 4 / TM);
                     }
                 }
         }
     all_loads_over();
 
+    // a lane's results: of row m of y 16 neighbouring columns for each tile
+    constexpr int TC = TN / NW; // tiles of a weight
+    if (p.splits > 1) { // partial sums as they lie in the registers: four a lane, the lanes' in order
+        f32x4* to = partials_of(a, p) + ((size_t)blockIdx.z * all + id) * (WN * TM * TN * 4 * 64) + (size_t)wave * (TM * TN * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            if (32 * i + n >= rows)
+                break;
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16& v = acc[i][t];
+                    to[((i * TN + t) * 4 + q) * 64] = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int64_t m = m0 + 32 * i + n;
         if (m >= a.m)
             continue;
 #pragma unroll
-        for (int t = 0; t < 2 / NW; ++t)
+        for (int t = 0; t < TC; ++t)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 4; q += 2) {
                 const int64_t col = nw + 32 * t + 16 * h + 4 * q;
                 if (col >= a.n)
                     continue;
-                f32x4 sum[NW];
+                f32x4 y[2];
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sum[w][e] = acc[i][NW == 2 ? w : t][4 * q + e];
-                if (p.splits == 1) {
-                    store4(a, m, col, finish4<KIND, NW>(a, p, m, sum));
-                } else {
+                for (int o = 0; o < 2; ++o) {
+                    f32x4 sum[NW];
 #pragma unroll
                     for (int w = 0; w < NW; ++w)
-                        *partial_of(a, p, (int)blockIdx.z, w, m, col) = sum[w];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sum[w][e] = acc[i][w * TC + t][4 * (q + o) + e];
+                    y[o] = finish4<KIND, NW>(a, p, m, sum);
                 }
+                store8(a, m, col, y[0], y[1]);
             }
     }
 }
 
-// the sums of all splits, in order, and the results
-template <Kind KIND, int NW>
+// The sums of all splits, in order, and the results: a workgroup for the partial sums of 32 rows
+// of x and 32 of each weight, a wave for a quarter of the columns, whose lanes have what
+// the lanes that left them had.
+template <Kind KIND, int NW, int TM>
 __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const MatmulPlan p)
 {
-    const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = (int64_t)blockIdx.z * 65535 + blockIdx.y;
-    if (n >= a.n || m >= a.m)
+    constexpr int TC = TN / NW, WC = 32 * TC, BM = 32 * TM, BN = WC * WN;
+    const uint32_t tiles_m = (uint32_t)((a.m + BM - 1) / BM), tiles_n = (uint32_t)((a.n + BN - 1) / BN), all = tiles_m * tiles_n;
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
+    uint32_t rest = blockIdx.x;
+    const uint32_t t = rest % TC;
+    rest /= TC;
+    const uint32_t i = rest % TM;
+    rest /= TM;
+    const uint32_t wave = rest % WN, id = rest / WN;
+    uint32_t row, col;
+    tile_of(id, tiles_m, tiles_n, row, col);
+    const int64_t m = (int64_t)row * BM + 32 * i + n, c = (int64_t)col * BN + wave * WC + 32 * t + 16 * h + 4 * q;
+    if (m >= a.m || c >= a.n)
         return;
     f32x4 sum[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
+        const f32x4* from = partials_of(a, p) + (size_t)id * (WN * TM * TN * 256) + wave * (TM * TN * 256) + ((i * TN + w * TC + t) * 4 + q) * 64 + lane;
         sum[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < p.splits; ++s)
-            sum[w] += *partial_of(a, p, s, w, m, n);
+            sum[w] += from[(size_t)s * all * (WN * TM * TN * 256)];
     }
-    store4(a, m, n, finish4<KIND, NW>(a, p, m, sum));
+    store4(a, m, c, finish4<KIND, NW>(a, p, m, sum));
 }
 
 // ---- launch -------------------------------------------------------------------------------
@@ -925,31 +984,28 @@ void few_form(const MatmulArgs& a, const MatmulPlan& p)
     }
 }
 
-template <Kind KIND, int NW>
-void many_form(const MatmulArgs& a, const MatmulPlan& p)
+template <Kind KIND, int NW, int TM>
+void many_tiles(const MatmulArgs& a, const MatmulPlan& p)
 {
-    const uint32_t tiles_n = (uint32_t)((a.n + p.rows - 1) / p.rows), tiles_m = (uint32_t)((a.m + p.tokens - 1) / p.tokens);
-    const dim3 grid(tiles_n * tiles_m, 1, (uint32_t)p.splits);
-    const bool one = scales_together(a);
-    switch (p.tokens) {
-#define FP4Q_MANY(TM, D)                                                                 \
-    if (one)                                                                             \
-        matmul_many<KIND, NW, TM, 4, D, true><<<grid, 256, 0, a.stream>>>(a, p);         \
-    else                                                                                 \
-        matmul_many<KIND, NW, TM, 4, D, false><<<grid, 256, 0, a.stream>>>(a, p);        \
-    break;
-    case 32: FP4Q_MANY(1, 2)
-    case 64: FP4Q_MANY(2, 2)
-    default: FP4Q_MANY(4, 2)
-#undef FP4Q_MANY
-    }
+    const uint32_t tiles = (uint32_t)((a.n + p.rows - 1) / p.rows * ((a.m + p.tokens - 1) / p.tokens));
+    const dim3 grid(tiles, 1, (uint32_t)p.splits);
+    if (scales_together(a))
+        matmul_many<KIND, NW, TM, true><<<grid, 64 * WN, 0, a.stream>>>(a, p);
+    else
+        matmul_many<KIND, NW, TM, false><<<grid, 64 * WN, 0, a.stream>>>(a, p);
+    if (p.splits > 1)
+        matmul_join<KIND, NW, TM><<<tiles * (WN * TM * TN / NW), 256, 0, a.stream>>>(a, p);
 }
 
 template <Kind KIND, int NW>
-void join_form(const MatmulArgs& a, const MatmulPlan& p)
+void many_form(const MatmulArgs& a, const MatmulPlan& p)
 {
-    const dim3 cover((uint32_t)((a.n + 1023) / 1024), (uint32_t)(a.m < 65535 ? a.m : 65535), (uint32_t)((a.m + 65534) / 65535));
-    matmul_join<KIND, NW><<<cover, 256, 0, a.stream>>>(a, p);
+    if (p.tokens == 32)
+        many_tiles<KIND, NW, 1>(a, p);
+    else if (p.tokens == 64)
+        many_tiles<KIND, NW, 2>(a, p);
+    else
+        many_tiles<KIND, NW, 4>(a, p);
 }
 
 } // namespace

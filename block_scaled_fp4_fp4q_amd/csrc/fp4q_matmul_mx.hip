@@ -35,8 +35,6 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
             break;
         }
     }
-    if (p.splits > 1)
-        join_form<kMxBf16, NW>(a, p);
     return hipGetLastError();
 }
 

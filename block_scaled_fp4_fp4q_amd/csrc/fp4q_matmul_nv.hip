@@ -32,12 +32,6 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
         default: few_form<kNvBf16, NW, 3, true>(a, p); break;
         }
     }
-    if (p.splits > 1) {
-        if (p.prepared)
-            join_form<kNvF16, NW>(a, p);
-        else
-            join_form<kNvBf16, NW>(a, p);
-    }
     return hipGetLastError();
 }
 

@@ -1,14 +1,15 @@
-// fp4q_matmul_plan.h -- how a product with 4-bit weights is cut into workgroups: integer
-// work of the host.
+// fp4q_matmul_plan.h -- how a product with 4-bit weights is cut into workgroups, from its sizes
+// and types alone: integer work of the host.
 #pragma once
-
-#include <stdlib.h>
 
 #include "fp4q_matmul_launch.h"
 
 namespace fp4q {
 
-constexpr size_t kFewLds = 64 * 1024;
+constexpr size_t kFewLds = 64 * 1024; // of x, in a workgroup of few rows
+constexpr int kFewRows = 16;          // rows of x that the kernel for few takes
+constexpr int kConvertRows = 4;       // of these, rows that its workgroups convert themselves
+constexpr int kFewWaves = 1536;       // waves that it is given at least, where the long axis can be shared
 
 inline size_t whole256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -16,29 +17,29 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
 {
     MatmulPlan p{};
     p.splits = 1;
-    const bool exact = a.bf16 && !a.rotate; // x enters as it is
-    p.many = a.m > 16;
-    const char* e;
-    // few rows are converted by the workgroups that use them, more by a launch of its own
-    const int64_t conv_most = (e = getenv("FP4Q_CONV")) ? atoi(e) : 4;
-    p.prepared = !exact && (p.many || a.m > conv_most);
+    p.many = a.m > kFewRows;
+    // x of bf16, not rotated, enters as it is.  Else the workgroups convert few rows on the way (a
+    // launch less: one rotated row, 14336 x 4096, takes 11.8 us so and 12.8 prepared), and
+    // more are prepared by a launch of their own (16 such rows: 34.7 and 18.1 us).
+    const bool exact = a.bf16 && !a.rotate;
+    p.prepared = !exact && a.m > kConvertRows;
     if (exact)
         p.parts = 1;
     else if (a.mx || !p.prepared)
-        p.parts = a.bf16 ? 2 : 3;
+        p.parts = a.bf16 ? 2 : 3; // in bf16
     else
-        p.parts = a.bf16 ? 1 : 2;
+        p.parts = a.bf16 ? 1 : 2; // in f16
     size_t at = p.prepared ? whole256((size_t)p.parts * a.m * a.k * 2) : 0;
     p.exponents = at;
     if (p.prepared && !a.mx)
         at = whole256(at + (size_t)a.m * 4);
     p.partials = at;
     if (!p.many) {
-        // waves that share the long axis: as few as give the chip two waves a SIMD
+        // Waves of a workgroup that share the long axis: as few as give the chip kFewWaves
+        // waves (one token, 4096 x 4096: 2, 4 or 8 of them take 8.7, 6.0 and 4.7 us; 14336 x 4096
+        // 10.0, 10.1 and 11.5).
         const int64_t tiles = (a.n + 15) / 16;
-        int kw = tiles * 2 >= 2048 ? 2 : (tiles * 4 >= 2048 ? 4 : 8);
-        if ((e = getenv("FP4Q_KW")))
-            kw = atoi(e);
+        int kw = tiles * 2 >= kFewWaves ? 2 : (tiles * 4 >= kFewWaves ? 4 : 8);
         const size_t row = (size_t)p.parts * a.m;
         while (kw > 2 && row * (kw * kFewStep * 2 + 16) > kFewLds) // a chunk is a step of each of them
             kw /= 2;
@@ -55,21 +56,40 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
         p.refused = (a.n + p.rows - 1) / p.rows > 0x7FFFFF;
         return p;
     }
+    // Tiles of 32, 64 or 128 rows of x by 256 rows of weights, and splits of the long axis: what
+    // is least of a cost in us.  A compute unit works through its tiles' steps one
+    // after the other whether one or two workgroups are there; a launch costs 6, joining 3
+    // and the partial sums' way to memory and back (4 TB/s).  As measured against
+    // it: 48 rows, 4096 x 14336, MXFP4, 64-row tiles in 1, 4, 8, 16, 32 splits 114, 37, 25, 21,
+    // 30 us; 509 rows, 4096 x 4096, NVFP4 rotated, tiles of 32, 64, 128 rows at their best 41
+    // (1 split), 35 (2), 42 (4); 8192 rows, 14336 x 4096, tiles of 64 and 128 rows 1185 and 854.
     p.rows = 256 / a.weights;
-    p.tokens = a.m <= 32 ? 32 : (a.m <= 64 ? 64 : 128);
-    if ((e = getenv("FP4Q_BM")))
-        p.tokens = atoi(e);
-    const int64_t steps = (a.k + kStepK - 1) / kStepK;
-    const int64_t tiles = (a.n + p.rows - 1) / p.rows * ((a.m + p.tokens - 1) / p.tokens);
-    p.refused = (a.n + p.rows - 1) / p.rows > 0x7FFFFF / ((a.m + p.tokens - 1) / p.tokens);
-    int64_t splits = (e = getenv("FP4Q_SPLIT")) ? atoi(e) : 1;
-    p.split_steps = (int)((steps + splits - 1) / splits);
-    if (p.split_steps < 1)
-        p.split_steps = 1;
-    p.splits = steps == 0 ? 1 : (int)((steps + p.split_steps - 1) / p.split_steps);
-    (void)tiles;
-    const size_t wide = (size_t)((a.n + 3) & ~(int64_t)3);
-    p.workspace = at + (p.splits > 1 ? (size_t)p.splits * a.weights * a.m * wide * 4 : 0);
+    const int64_t steps = (a.k + kStepK - 1) / kStepK, tiles_n = (a.n + p.rows - 1) / p.rows;
+    int64_t best_tiles = 0;
+    double best = 0.0;
+    for (int tokens = 32; tokens <= 128 && (tokens == 32 || tokens / 2 < a.m); tokens *= 2) {
+        const int64_t tiles_m = (a.m + tokens - 1) / tokens;
+        if (tiles_n > 0x7FFFFF / tiles_m)
+            continue;
+        const int64_t tiles = tiles_n * tiles_m;
+        const double turn = tokens == 32 ? 0.95 : (tokens == 64 ? 1.15 : 1.9);
+        // more splits than fill the chip four times, or than give each two steps, cost more
+        for (int64_t c = 1; c == 1 || (c <= steps / 2 && tiles * c <= 4 * kCus); ++c) {
+            const int64_t each = (steps + c - 1) / c, splits = each == 0 ? 1 : (steps + each - 1) / each;
+            const double mb = (double)tiles * splits * tokens * 256 * 4e-6;
+            const double us = 6.0 + (double)((tiles * splits + kCus - 1) / kCus) * each * p.parts * turn +
+                              (splits > 1 ? 3.0 + mb * 2 / 4 : 0.0);
+            if (best_tiles == 0 || us < best) {
+                best = us;
+                best_tiles = tiles;
+                p.tokens = tokens;
+                p.splits = (int)splits;
+                p.split_steps = (int)each;
+            }
+        }
+    }
+    p.refused = best_tiles == 0;
+    p.workspace = at + (p.splits > 1 ? (size_t)p.splits * best_tiles * p.tokens * 256 * 4 : 0);
     return p;
 }
 

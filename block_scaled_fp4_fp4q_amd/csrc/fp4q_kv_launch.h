@@ -65,7 +65,6 @@ struct KvAppendArgs {
 // How one launch is shared out: workgroups of K, as many of V, then q's.
 struct AppendPlan {
     uint32_t kv_groups, q_groups; // workgroups
-    uint32_t kv_items, q_items;   // lanes with work
     int lane_shift;               // log2 of the lanes of a row
 };
 

@@ -37,7 +37,7 @@ def test_matmul(form, size):
 def act64(act, g):
     """The activation in 64 bits, and the largest slope of any of the three (1.13, at 1.5 or so) as a bound."""
     if act == B.FP4Q_ACT_SILU:
-        return g / (1 + np.exp(-g))
+        return g / (1 + np.exp(-np.maximum(g, -700)))
     if act == B.FP4Q_ACT_GELU:
         return 0.5 * g * np.array([math.erfc(-v / math.sqrt(2)) for v in g.reshape(-1)]).reshape(g.shape)
     return 0.5 * g * (1 + np.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)))

@@ -514,6 +514,7 @@ class KvCache:
                                     *k_codes.stride()[:3], *k_scales.stride()[:3])
         self._spec, self._struct = C.byref(self.spec), C.byref(self.struct)
         self._calls = {}  # attend's checked argument shapes
+        self._appends = {}  # kv_append's
 
 
 def alloc_kv_cache(pages, kv_heads, page_size, head_dim, k_global=None, v_global=None,
@@ -655,14 +656,51 @@ def rope_frequencies(rope_dim, base=10000.0, factor=1.0, original_length=None, f
 
 def _norm_weight(name, t, dim, device):
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, but the cache is on {device}")
     if t.dtype != torch.float32 or tuple(t.shape) != (dim,) or t.stride(0) != 1:
         raise ValueError(f"{name} must be float32 [{dim}], contiguous")
-    return t.data_ptr()
+
+
+def _append_call(cache, k, v, slots, q, positions, rope, interleaved, q_weight, k_weight, eps, out):
+    """The call's fp4q_append without its pointers, from checked tensors."""
+    dev, dim = cache.device, cache.head_dim
+    _ints("slots", slots, torch.int64, dev)
+    n = slots.shape[0]
+    ks = _rows("k", k, n, cache.heads, dim, dev)
+    vs = _rows("v", v, n, cache.heads, dim, dev)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _norm_weight(name, t, dim, dev)
+    call = fp4q_append(k_token_stride=ks[0], k_head_stride=ks[1], v_token_stride=vs[0], v_head_stride=vs[1], tokens=n,
+                       dtype=_dtype_code(k), interleaved=interleaved, eps=eps)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        heads = q.shape[1]
+        call.q_row_stride, call.q_head_stride = _rows("q", q, n, heads, dim, dev, (k.dtype,))[:2]
+        call.out_row_stride, call.out_head_stride = _rows("out", out, n, heads, dim, dev, (q.dtype,))[:2]
+        call.q_heads = heads
+    elif out is not None:
+        raise ValueError("out is given without q")
+    if rope is not None:
+        if rope.device != dev:
+            raise ValueError(f"rope is on {rope.device}, but the cache is on {dev}")
+        if rope.dtype != torch.float32 or rope.dim() != 2 or (rope.numel() > 0 and rope.stride(1) != 1):
+            raise ValueError("rope must be float32 [positions, rope_dim], the last dimension contiguous")
+        if rope.shape[1] % 16 or not 0 < rope.shape[1] <= dim:
+            raise ValueError(f"rope_dim is {rope.shape[1]}; expected a multiple of 16 up to head_dim, {dim}")
+        if positions is None:
+            raise ValueError("rope needs positions")
+        _ints("positions", positions, torch.int64, dev)
+        if positions.shape[0] != n:
+            raise ValueError(f"positions has {positions.shape[0]} entries; expected {n}")
+        call.rope_rows, call.rope_dim = rope.shape
+        # torch gives a single row any stride
+        call.rope_stride = rope.stride(0) if rope.shape[0] > 1 else rope.shape[1]
+    return call
 
 
 def kv_append(cache, k, v, slots, q=None, positions=None, rope=None, interleaved=False, q_weight=None,
@@ -686,49 +724,40 @@ def kv_append(cache, k, v, slots, q=None, positions=None, rope=None, interleaved
     if not _here(dev, stream):
         with _on(dev, stream):
             return kv_append(cache, k, v, slots, q, positions, rope, interleaved, q_weight, k_weight, eps, out)
-    _ints("slots", slots, torch.int64, dev)
-    n, dim = slots.shape[0], cache.head_dim
-    ks = _rows("k", k, n, cache.heads, dim, dev)
-    vs = _rows("v", v, n, cache.heads, dim, dev)
-    if k.dtype != v.dtype:
-        raise ValueError("k and v must have the same dtype")
-    call = fp4q_append(k=k.data_ptr(), k_token_stride=ks[0], k_head_stride=ks[1], v=v.data_ptr(),
-                       v_token_stride=vs[0], v_head_stride=vs[1], slots=slots.data_ptr(), tokens=n,
-                       dtype=_dtype_code(k), interleaved=bool(interleaved), eps=eps,
-                       q_weight=_norm_weight("q_weight", q_weight, dim, dev),
-                       k_weight=_norm_weight("k_weight", k_weight, dim, dev))
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    if q is not None and out is None:
+        if not isinstance(q, torch.Tensor):
             raise TypeError("q must be a torch tensor [tokens, q_heads, head_dim]")
-        heads = q.shape[1]
-        qs = _rows("q", q, n, heads, dim, dev, (k.dtype,))
-        if out is None:
-            out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
-        os = _rows("out", out, n, heads, dim, dev, (q.dtype,))
-        call.q, call.q_row_stride, call.q_head_stride, call.q_heads = q.data_ptr(), qs[0], qs[1], heads
-        call.q_out, call.out_row_stride, call.out_head_stride = out.data_ptr(), os[0], os[1]
-    elif out is not None:
-        raise ValueError("out is given without q")
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if type(interleaved) is not bool:
+        interleaved = bool(interleaved)
+    if type(eps) is not float:
+        eps = float(eps)
+    tensors = (k, v, slots, q, out, positions, rope, q_weight, k_weight)
+    for t in tensors:
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError("k, v, slots, q, positions, rope and the weights must be torch tensors")
+    # calls that differ in addresses alone share their checks
+    key = (*map(_same, tensors), interleaved, eps)
+    known = cache._appends.get(key)
+    if known is None:
+        if len(cache._appends) >= 64:
+            cache._appends.clear()
+        known = cache._appends[key] = bytes(_append_call(cache, k, v, slots, q, positions, rope, interleaved, q_weight,
+                                                         k_weight, eps, out))
+    call = fp4q_append.from_buffer_copy(known)
+    call.k, call.v, call.slots = k.data_ptr(), v.data_ptr(), slots.data_ptr()
+    if q is not None:
+        call.q, call.q_out = q.data_ptr(), out.data_ptr()
     if rope is not None:
-        if not isinstance(rope, torch.Tensor):
-            raise TypeError("rope must be a torch tensor")
-        if rope.device != dev:
-            raise ValueError(f"rope is on {rope.device}, but the cache is on {dev}")
-        if rope.dtype != torch.float32 or rope.dim() != 2 or (rope.numel() > 0 and rope.stride(1) != 1):
-            raise ValueError("rope must be float32 [positions, rope_dim], the last dimension contiguous")
-        if rope.shape[1] % 16 or not 0 < rope.shape[1] <= dim:
-            raise ValueError(f"rope_dim is {rope.shape[1]}; expected a multiple of 16 up to head_dim, {dim}")
-        if positions is None:
-            raise ValueError("rope needs positions")
-        _ints("positions", positions, torch.int64, dev)
-        if positions.shape[0] != n:
-            raise ValueError(f"positions has {positions.shape[0]} entries; expected {n}")
-        call.rope, call.rope_rows, call.rope_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
-        # torch gives a single row any stride
-        call.rope_stride = rope.stride(0) if rope.shape[0] > 1 else rope.shape[1]
-        call.positions = positions.data_ptr()
-    _check("fp4q_kv_append", _lib_handle().fp4q_kv_append(cache._spec, cache._struct, C.byref(call),
-                                                          _current_stream(dev.index)))
+        call.rope, call.positions = rope.data_ptr(), positions.data_ptr()
+    if q_weight is not None:
+        call.q_weight = q_weight.data_ptr()
+    if k_weight is not None:
+        call.k_weight = k_weight.data_ptr()
+    st = _lib_handle().fp4q_kv_append(cache._spec, cache._struct, C.byref(call), _current_stream(dev.index))
+    if st:
+        cache._appends.pop(key, None)
+        _check("fp4q_kv_append", st)
     return out
 
 
@@ -946,6 +975,7 @@ class QuantizedWeight:
         self.struct = fp4q_weight(*ptr, rows, cols)
         self._spec, self._struct = C.byref(self.spec), C.byref(self.struct)
         self._needs = {}  # workspace bytes by (number of weights, tokens, dtype)
+        self._calls = {}  # checked argument shapes
 
 
 def _token_rows(name, t, cols, device, dtype=None):
@@ -991,31 +1021,44 @@ def gated_workspace_bytes(gate, up, tokens, dtype=torch.bfloat16):
     return _product_need((gate, up), operator.index(tokens), FP4Q_BF16 if dtype == torch.bfloat16 else FP4Q_F32)
 
 
-def _product(fn, weights, extra, x, out, workspace):
+def _product_call(weights, x, out):
+    """(tokens, x's and out's row strides, dtype code, workspace bytes) of checked arguments."""
     w = weights[0]
-    dev = w.device
-    if isinstance(x, torch.Tensor) and x.dim() != 2:
-        if x.dim() < 1 or not x.is_contiguous() or (out is not None and not out.is_contiguous()):
-            raise ValueError("x (and out) of other than 2 dimensions must be contiguous")
-        if out is not None and tuple(out.shape) != (*x.shape[:-1], w.rows):
-            raise ValueError(f"out has shape {tuple(out.shape)}; expected {(*x.shape[:-1], w.rows)}")
-        lead = x.shape[:-1]
-        tokens = 1
-        for n in lead:
-            tokens *= n
-        y = _product(fn, weights, extra, x.reshape(tokens, x.shape[-1]),
-                     None if out is None else out.view(tokens, w.rows), workspace)
-        return y.view(*lead, w.rows)
-    tokens, xs = _token_rows("x", x, w.cols, dev)
-    if out is None:
-        out = torch.empty((tokens, w.rows), dtype=x.dtype, device=dev)
-        ys = w.rows
-    else:
-        rows, ys = _token_rows("out", out, w.rows, dev, x.dtype)
+    tokens, xs = _token_rows("x", x, w.cols, w.device)
+    ys = w.rows
+    if out is not None:
+        rows, ys = _token_rows("out", out, w.rows, w.device, x.dtype)
         if rows != tokens:
             raise ValueError(f"out has {rows} rows; expected {tokens}")
     code = FP4Q_BF16 if x.dtype == torch.bfloat16 else FP4Q_F32
-    need = _product_need(weights, tokens, code)
+    return tokens, xs, ys, code, _product_need(weights, tokens, code)
+
+
+def _product(fn, weights, extra, x, out, workspace):
+    w = weights[0]
+    dev = w.device
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch tensor")
+    shape = x.shape
+    if len(shape) != 2:
+        if not shape or not x.is_contiguous() or (out is not None and not out.is_contiguous()):
+            raise ValueError("x (and out) of other than 2 dimensions must be contiguous")
+        if out is not None and tuple(out.shape) != (*shape[:-1], w.rows):
+            raise ValueError(f"out has shape {tuple(out.shape)}; expected {(*shape[:-1], w.rows)}")
+        tokens = math.prod(shape[:-1])
+        y = _product(fn, weights, extra, x.reshape(tokens, shape[-1]),
+                     None if out is None else out.view(tokens, w.rows), workspace)
+        return y.view(*shape[:-1], w.rows)
+    # calls that differ in addresses alone share their checks
+    key = (shape, x.stride(), x.dtype, x.device, _same(out), len(weights))
+    known = w._calls.get(key)
+    if known is None:
+        if len(w._calls) >= 64:
+            w._calls.clear()
+        known = w._calls[key] = _product_call(weights, x, out)
+    tokens, xs, ys, code, need = known
+    if out is None:
+        out = torch.empty((tokens, w.rows), dtype=x.dtype, device=dev)
     space = None
     if need:
         if workspace is None:
@@ -1023,9 +1066,14 @@ def _product(fn, weights, extra, x, out, workspace):
         else:
             _check_tensor("workspace", workspace, _U8, need, dev, require_cuda=False)
         space = workspace.data_ptr()
-    st = getattr(_lib_handle(), fn)(w._spec, *[u._struct for u in weights], *extra, x.data_ptr(), code, tokens, xs,
-                                    out.data_ptr(), ys, space, need, _current_stream(dev.index))
+    if extra:
+        st = _lib_handle().fp4q_gated(w._spec, w._struct, weights[1]._struct, *extra, x.data_ptr(), code, tokens, xs,
+                                      out.data_ptr(), ys, space, need, _current_stream(dev.index))
+    else:
+        st = _lib_handle().fp4q_matmul(w._spec, w._struct, x.data_ptr(), code, tokens, xs, out.data_ptr(), ys, space, need,
+                                       _current_stream(dev.index))
     if st:
+        w._calls.pop(key, None)
         _check(fn, st)
     return out
 

@@ -6,7 +6,9 @@
 
 namespace fp4q {
 
-constexpr size_t kFewLds = 64 * 1024; // of x, in a workgroup of few rows
+// LDS of x in a workgroup of few rows, beside the 54 KiB (two weights 108) of codes on their way,
+// of a compute unit's 160
+constexpr size_t few_lds(int weights) { return weights == 2 ? 48 * 1024 : 68 * 1024; }
 constexpr int kFewRows = 16;          // rows of x that the kernel for few takes
 constexpr int kConvertRows = 4;       // of these, rows that its workgroups convert themselves
 constexpr int kFewWaves = 1536;       // waves that it is given at least, where the long axis can be shared
@@ -41,14 +43,14 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
         const int64_t tiles = (a.n + 15) / 16;
         int kw = tiles * 2 >= kFewWaves ? 2 : (tiles * 4 >= kFewWaves ? 4 : 8);
         const size_t row = (size_t)p.parts * a.m;
-        while (kw > 2 && row * (kw * kFewStep * 2 + 16) > kFewLds) // a chunk is a step of each of them
+        while (kw > 2 && row * (kw * kFewStep * 2 + 16) > few_lds(a.weights)) // a chunk is a step of each of them
             kw /= 2;
         p.waves_k = kw;
         p.rows = 16 * (8 / kw);
         p.tokens = 16;
         const int steps = (int)((a.k + kFewStep - 1) / kFewStep);
         p.chunk_steps = (steps + kw - 1) / kw * kw;
-        while (p.chunk_steps > kw && row * (p.chunk_steps * kFewStep * 2 + 16) > kFewLds)
+        while (p.chunk_steps > kw && row * (p.chunk_steps * kFewStep * 2 + 16) > few_lds(a.weights))
             p.chunk_steps = (p.chunk_steps / 2 + kw - 1) / kw * kw;
         const size_t x = row * (p.chunk_steps * kFewStep * 2 + 16), red = (size_t)8 * a.weights * 1024;
         p.lds = x > red ? x : red;

@@ -16,7 +16,7 @@ IDS = [f"{f}{'-rotated' if r else ''}-{str(d)[6:]}" for f, r, d in FORMS]
 # tokens, rows, cols (in units of 32): every form of the kernels, sizes at their tiles' ends, one less and one more
 SIZES = [(1, 1, 1), (1, 16, 1), (1, 4096, 4), (2, 17, 3), (3, 33, 129), (4, 100, 32), (5, 31, 40), (8, 256, 17), (16, 32, 64),
          (17, 65, 9), (31, 64, 33), (32, 129, 8), (33, 63, 24), (48, 260, 68), (64, 128, 16), (65, 64, 5), (100, 127, 36),
-         (128, 256, 8), (130, 300, 44), (255, 257, 12), (300, 515, 20), (513, 129, 67)]
+         (16, 20, 500), (4, 33, 640), (128, 256, 8), (130, 300, 44), (255, 257, 12), (300, 515, 20), (513, 129, 67)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=str)
@@ -57,7 +57,8 @@ def gated64(w0, w1, x, act):
 
 
 @pytest.mark.parametrize("act", [B.FP4Q_ACT_SILU, B.FP4Q_ACT_GELU, B.FP4Q_ACT_GELU_TANH])
-@pytest.mark.parametrize("size", [(1, 16, 4), (3, 31, 9), (16, 100, 36), (33, 65, 12), (70, 130, 8), (300, 257, 17)], ids=str)
+@pytest.mark.parametrize("size", [(1, 16, 4), (3, 31, 9), (4, 20, 300), (16, 100, 36), (13, 40, 512), (33, 65, 12),
+                                  (70, 130, 8), (300, 257, 17)], ids=str)
 @pytest.mark.parametrize("form", FORMS, ids=IDS)
 def test_gated(form, size, act):
     fmt, rotate, dtype = form

@@ -23,12 +23,13 @@ namespace {
 constexpr int kThreads = 256;
 
 // 1 / sqrt(d), rounded to binary32, for d > 0 in binary64: one step of third order on
-// the hardware's estimate (off by at most 2^-22 or so) leaves 2^-52
+// the hardware's estimate (off by at most 2^-22 or so) leaves 2^-52; infinity gives 0
 __device__ __forceinline__ float inverse_root(double d)
 {
     const double y = __builtin_amdgcn_rsq(d);
     const double e = __builtin_fma(-(d * y), y, 1.0);
-    return (float)__builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y);
+    const double r = __builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y);
+    return d == __builtin_huge_val() ? 0.0f : (float)r;
 }
 
 // the E values from value e0 on of a row, widened

@@ -207,3 +207,16 @@ def test_tables():
     assert np.allclose(B.rope_frequencies(64, factor=8.0).cpu().numpy(), f / 8, rtol=1e-12)
     custom = B.rope_table(10, 64, frequencies=g).cpu().numpy()
     assert np.abs(custom[:, :32] - np.cos(np.arange(10)[:, None] * g)).max() < 1e-7
+
+
+@pytest.mark.parametrize("rule", ["absmax", "sweep"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_of_a_row_with_infinities(dtype, rule):
+    """1 / infinity is 0: the row's finite values become zeros, the infinite ones NaN; a NaN is the whole row's."""
+    c = Case(20, rule=rule, dtype=dtype, turn=0)
+    c.q[1, 2, 40], c.q[3, 0, 0], c.q[3, 0, 127], c.q[5, 4, 9] = float("inf"), float("inf"), -float("inf"), float("nan")
+    want, sides, good = c.expected()
+    assert (want[1, 2] == 0).sum() == 127 and torch.isnan(want[5, 4]).all()
+    cache = c.cache()
+    assert same(c.call(cache), want)
+    c.check_cache(cache, sides, good)

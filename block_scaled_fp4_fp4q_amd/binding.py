@@ -959,9 +959,9 @@ class QuantizedWeight:
         self.spec = make_spec(format, rotate=rotate)
         if rotate not in (0, self.spec.block):
             raise ValueError(f"rotate is {rotate}; expected 0 or the block, {self.spec.block}")
-        if rows < 0 or cols < 0 or cols % self.spec.block or cols > 1 << 24 or rows > 1 << 36:
+        if rows < 0 or cols < 0 or cols % self.spec.block or cols > 1 << 22 or rows > 1 << 36:
             raise ValueError(f"a weight of [{rows}, {cols}] is not supported: cols must be a multiple of "
-                             f"{self.spec.block}, at most 2^24")
+                             f"{self.spec.block}, at most 2^22")
         if not isinstance(codes, torch.Tensor):
             raise TypeError("codes must be a torch tensor")
         self.rows, self.cols, self.device = rows, cols, codes.device

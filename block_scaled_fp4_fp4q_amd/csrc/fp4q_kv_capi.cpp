@@ -332,6 +332,10 @@ fp4q_status fp4q_kv_append(const fp4q_spec* spec, const fp4q_kv_cache* cache, co
     if (c->tokens != 0 && c->q_heads != 0 &&
         !rows_apart<2>({c->tokens, c->q_heads}, {c->out_row_stride, c->out_head_stride}, cache->head_dim))
         return FP4Q_E_SHAPE;
+    // in place a row is overwritten by its own result alone
+    if (c->q_heads != 0 && c->q == c->q_out &&
+        ((c->tokens > 1 && c->q_row_stride != c->out_row_stride) || (c->q_heads > 1 && c->q_head_stride != c->out_head_stride)))
+        return FP4Q_E_SHAPE;
     if (c->tokens == 0)
         return FP4Q_OK;
     a.rule = spec->scale_rule;

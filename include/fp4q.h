@@ -458,7 +458,7 @@ fp4q_status fp4q_attend(const fp4q_spec* spec, const fp4q_kv_cache* cache,
  * global scale (read at each call; may be NULL for MXFP4).  spec of the calls
  * below: format (others: FP4Q_E_UNSUPPORTED), block, and rotate = 0, or = block
  * for a weight that was quantized with it; the other members are ignored.
- * cols is at most 2^24.  codes 8-byte aligned (16 for MXFP4), scales of any
+ * cols is at most 2^22.  codes 8-byte aligned (16 for MXFP4), scales of any
  * alignment. */
 typedef struct {
     const uint8_t* codes;
@@ -472,13 +472,15 @@ typedef enum { FP4Q_ACT_SILU = 0, FP4Q_ACT_GELU = 1, FP4Q_ACT_GELU_TANH = 2 } fp
 /* y [tokens, rows] = x [tokens, cols] W^T, W the dequantized weight (un-rotated,
  * where it is stored rotated: x is rotated instead).
  *   x        dtype FP4Q_F32 or FP4Q_BF16, 16-byte aligned, row stride in
- *            elements, a multiple of 16 bytes.
+ *            elements, a multiple of 16 bytes and at most 2^22 elements.
  *   y        of the same dtype, row stride in elements, at least `rows`.
  *   workspace  fp4q_matmul_workspace_bytes() bytes, 256-byte aligned (NULL where
  *            that is 0).
- * Weights enter the products exactly; bf16 x does, binary32 x in 24 bits, rotated
- * bf16 x in 16 bits (rotated in binary32).  Sums are binary32, in an order
- * that the sizes alone decide, and the global scale is a factor of the sum.
+ * Weights enter the products exactly, and so does bf16 x.  Rotated bf16 x (rotated in
+ * binary32) and binary32 x enter them in 16 and 24 bits; with NVFP4 and more than 4
+ * tokens in 11 and 22, of which a value loses what lies below 2^-39 of its row's
+ * largest, and else what lies below 2^-134.  Sums are binary32, in an order that the sizes alone decide, and the
+ * global scale is a factor of the sum.
  * Precondition beside those above: sum_k |x_k w_k| / S (MXFP4: S = 1) is below
  * 2^127.  A row of x with values that are not finite gives what it gives in
  * its own row of y alone. */

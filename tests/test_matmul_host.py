@@ -168,6 +168,13 @@ def test_appends(L, status, change):
     assert append(L, a=call(**change)) == status
 
 
+def test_appends_in_place_take_one_layout(L):
+    """q_out may be q where each row is overwritten by its own result alone."""
+    for change in (dict(out_row_stride=2048), dict(q_row_stride=2048), dict(out_row_stride=128, out_head_stride=512)):
+        assert append(L, a=call(q_out=P[6], **change)) == SHAPE
+    assert append(L, a=call(q_out=P[6], tokens=0, out_row_stride=2048)) == 0
+
+
 def test_appends_to_caches_that_cannot_be_written(L):
     for change in (dict(code_token=0), dict(scale_head=64), dict(v_codes=P[0])):
         assert append(L, c=cache(**change)) == SHAPE
@@ -195,7 +202,7 @@ def host_weight(n=8, k=64, **kw):
 def test_binding_refuses_weights(L):
     c, s, g = torch.zeros(256, dtype=torch.uint8), torch.zeros(32, dtype=torch.uint8), torch.ones(1)
     for bad in (dict(codes=c[:255]), dict(scales=s[:31]), dict(global_scale=None), dict(codes=c.float()), dict(rows=-1),
-                dict(cols=60), dict(format=B.FP4Q_IF4), dict(rotate=32), dict(scales=s[::2])):
+                dict(cols=60), dict(cols=(1 << 22) + 16), dict(format=B.FP4Q_IF4), dict(rotate=32), dict(scales=s[::2])):
         a = dict(codes=c, scales=s, global_scale=g, rows=8, cols=64, require_cuda=False)
         a.update(bad)
         with pytest.raises(ValueError):

@@ -15,7 +15,9 @@
 // largest value to [2^14, 2^15) (what falls below f16's range is under 2^-38 of that
 // value): rotated bf16 in one part, 11 bits, 8 times finer than the rounding of a bf16
 // result; binary32 in two, 22 bits.  With MXFP4, whose weights f16 does not hold, they
-// are bf16: rotated bf16 in two, 16 bits, binary32 in three, which hold its 24 bits.
+// are bf16: rotated bf16 in two, 16 bits, binary32 in three, which hold its 24 bits (down to
+// bf16's last bit, 2^-133).  At most four rows are cut into these by the workgroups
+// themselves, with NVFP4 too.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,7 +57,7 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
 // ---- weights -------------------------------------------------------------------
 
 // Two codes of a word times their block's scale s.  The product has six bits: f16 holds it,
-// and cutting it from binary32 to bf16 loses nothing.  (A step of two codes costs about
+// and cutting it from binary32 to bf16 loses nothing.  (Two codes cost about
 // 16 cycles of a SIMD as bf16, 11 as f16, 7 for a power of two.)
 template <Kind KIND, int SEL>
 __device__ __forceinline__ uint32_t expand_pair(uint32_t w, float s)
@@ -234,7 +236,7 @@ __device__ __forceinline__ void load_x(const MatmulArgs& a, int64_t row, int64_t
 }
 
 // The bf16 parts of x, for MXFP4: [part][m][k] in the workspace, a block of values a
-// thread.  Moves x once: bound by HBM.
+// thread.  Moves x once; 37 rows of 4064: 5 us, a launch's latency.
 template <int PARTS>
 __global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
 {
@@ -262,7 +264,8 @@ __global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
 // The f16 parts of x, for NVFP4: [part][m][k] in the workspace, and behind them each row's
 // exponent (what its values were multiplied by is 2^exponent).  A workgroup has a row:
 // its largest finite value first, then the parts; blocks that a thread does not hold
-// itself it reads again, from cache.
+// itself it reads again, from cache.  Moves x once; 509 rows of 4096: 5 us, a launch's
+// latency.
 template <int PARTS>
 __global__ __launch_bounds__(256) void matmul_halves(const MatmulArgs a, const MatmulPlan p)
 {
@@ -397,6 +400,12 @@ __device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulP
 // with the row, so that 16 rows' meet all banks).  kStages steps are held or on their way.
 // x comes from LDS too, where the whole workgroup put it (CONV: rotated and cut into bf16
 // parts on the way; else as it is, or as matmul_parts and matmul_halves left it).
+//   Bound by latency for small weights (one token, 4096 x 4096, NVFP4: 4.7 us in a graph) and by the vector ALU's expansion and the conversion of x in every
+// workgroup for wide ones: 14336 x 4096, NVFP4, one token 9.8 us, 3.4 TB/s of weights, MXFP4 7.5;
+// 16 tokens, whose x of 128 KiB each workgroup takes to its LDS, 14.9.  Scale bytes come four
+// at a time where every row allows it (two weights of 14336 x 4096, before other steps: 24 us; a
+// byte at a time 30).  Waves that begin at different steps, to spread the rows' lines over the memory's channels,
+// were slower (10.1 -> 13.4 us).
 constexpr int kStages = 3;
 
 template <Kind KIND, int NW, int PARTS, bool CONV, int RW, int KW, bool ONE>
@@ -618,8 +627,17 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 //   Row 8 q + 4 h + e of a product's 32 rows of W is column 16 h + 4 q + e of y, so that a
 // lane ends with 16 neighbouring columns.
 //   While the products of eight values run, the weights of the next eight are expanded; the
-// last ones' are those of the next step.  D steps' x and codes are held or on their way, each
-// in a buffer and registers of its own.
+// last ones' are those of the next step.  Two steps' x and codes are held or on their way, each
+// in a buffer and registers of its own.  (Loads three steps ahead changed nothing.)
+//   Two parts of x (BOTH) are rows of one step, each with its own sums, joined at the end: W is
+// read and expanded once for both.  Else a part is a step of its own.
+//   Bound by several units at once.  8192 rows, 14336 x 4096, NVFP4 bf16, TM = 4: 831 us, 1157
+// TFLOP/s; of a SIMD's cycles the matrix cores are busy in 56 of 100 and the vector ALU, which
+// expands, in 43, LDS gives x to a CU at 64 bytes a clock and each 16 bytes of a lane feed
+// two products, and the clock is at 1.87 GHz under the power that this takes.  MXFP4, whose
+// codes take one instruction a pair, 774 to 823 us.  Products of 128 weight rows a wave would
+// halve the reads of x and spill registers (1240 us); 16x16x32 products spill too.  A step of a
+// workgroup costs its CU 0.95, 1.15, 1.9 us with TM = 1, 2, 4.
 constexpr int WN = 4; // waves of a workgroup
 constexpr int TN = 2; // products of 32 weight rows in a wave
 
@@ -635,11 +653,12 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
     n = __builtin_amdgcn_readfirstlane(in / high);
 }
 
-template <Kind KIND, int NW, int TM, bool ONE>
+template <Kind KIND, int NW, int TM, int BOTH, bool ONE>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
     constexpr int B = KIND == kMxBf16 ? 32 : 16;
-    constexpr int BM = 32 * TM;
+    constexpr int XM = TM / BOTH;    // products of 32 rows of x
+    constexpr int BM = 32 * XM;
     constexpr int D = 2;             // steps held
     constexpr int WC = 32 * TN / NW; // columns of y of a wave
     constexpr int BN = WC * WN;
@@ -647,7 +666,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     constexpr bool MX = KIND == kMxBf16;
     constexpr bool STAGED = TM <= 2;     // codes through LDS
     constexpr int NS = Wide<KIND, ONE>::NS;
-    __shared__ u32x4 xbuf[D][BM * U];
+    __shared__ u32x4 xbuf[D][32 * TM * U];
     __shared__ u32x4 cbuf[STAGED ? WN : 1][D][STAGED ? 128 * TN : 1];
     __shared__ uint32_t sbuf[STAGED && ONE ? WN : 1][D][STAGED && ONE ? 64 * TN : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -669,7 +688,8 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     const int steps = (cols + kStepK - 1) / kStepK;
     const int s0 = (int)blockIdx.z * p.split_steps;
     const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
-    const int turns = (s1 - s0) * p.parts; // a step for each part of x, the small ones first
+    const int parts = BOTH == 2 ? 1 : p.parts;
+    const int turns = (s1 - s0) * parts; // a step for each part of x, the small ones first
     // Offsets are a lane's own (in a vector register) and a uniform part that never passes
     // the buffer's end, where the check against it would wrap: rows of a tile that do not
     // exist are replaced by others, whose results are not stored.
@@ -680,7 +700,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     const int x_row = (int)(p.prepared ? a.k : a.x_row) * 2; // bytes
     const char* x = static_cast<const char*>(p.prepared ? a.workspace : a.x) + m0 * x_row;
     const int64_t plane = a.m * a.k * 2;
-    constexpr int LOADS = BM / (4 * WN); // of a wave: four rows each
+    constexpr int LOADS = 32 * TM / (4 * WN); // of a wave: four rows each
     const int quad = lane >> 4;          // row of the four
     constexpr int KINDS = LOADS < 4 ? LOADS : 4; // the exchange of units repeats every four loads
     int x_unit[KINDS];
@@ -688,16 +708,18 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     for (int i = 0; i < KINDS; ++i)
         x_unit[i] = (lane & 15) ^ ((4 * (wave * LOADS + i) + quad) & 15);
     const uint32_t x_place = lds_place(xbuf), c_place = lds_place(cbuf), s_place = lds_place(sbuf);
-    auto load_x_tile = [&](int step, int part, bool real, int to) {
+    const int second = BOTH == 2 ? wave / (WN / 2) : 0; // half of the waves load each part
+    auto load_x_tile = [&](int step, int turn_part, bool real, int to) {
+        const int part = BOTH == 2 ? second : turn_part;
         const u32x4 src = words_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
         const bool whole = (step + 1) * kStepK <= cols;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int row = (wave * LOADS + i) * 4;
+            const int row = (wave * LOADS + i) * 4 - second * BM;
             int at = (quad * x_row + x_unit[i % KINDS] * 16) | (real ? 0 : kPast);
             if (!whole) // values past the row's end are zeros
                 at |= step * kStepK + x_unit[i % KINDS] * 8 < cols ? 0 : kPast;
-            load_to_lds<16>(src, x_place + (to * BM * U + (wave * LOADS + i) * 64) * 16, at,
+            load_to_lds<16>(src, x_place + (to * 32 * TM * U + (wave * LOADS + i) * 64) * 16, at,
                             (row < rows ? row : 0) * x_row + step * (kStepK * 2));
         }
     };
@@ -807,7 +829,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     };
     // Loads of a step, whose number never changes: past the last step they are made past
     // their buffers' ends.
-    int next_step = s0, next_part = p.parts - 1, next_turn = 0;
+    int next_step = s0, next_part = parts - 1, next_turn = 0;
     auto load_turn = [&](int to) {
         const bool real = next_turn < turns;
         asm volatile("" ::: "memory"); // the loads of two steps keep their order
@@ -816,17 +838,13 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         asm volatile("" ::: "memory");
         ++next_turn;
         if (next_part == 0) {
-            next_part = p.parts;
+            next_part = parts;
             next_step += next_turn < turns ? 1 : 0;
         }
         --next_part;
     };
-    constexpr int PER = LOADS + TN * (2 + NS); // loads of a step
-    static_assert((D - 2) * PER < 64, "what the counter of loads holds");
     if (turns > 0) {
-#pragma unroll
-        for (int d = 0; d < D - 1; ++d)
-            load_turn(d);
+        load_turn(0);
         if constexpr (STAGED)
             take_half(0, 0, ring[0]);
         expand_pairs(ring[0], 0, 0, 4 * TN);
@@ -836,16 +854,12 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         for (int d = 0; d < D; ++d) {
             if (base + d >= turns)
                 break;
-            // of this wave's loads only those of the D - 2 later steps are on their way still;
-            // after the barrier that holds for every wave, and the buffer of the step before
-            // this one is free: its reads have all been used by products (__syncthreads would
-            // wait for the later steps too)
-            constexpr int STAY = (D - 2) * PER;
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0x0F70 | (STAY & 15) | ((STAY >> 4) << 14)); // vmcnt alone
+            // this wave's loads have arrived; after the barrier that holds for every wave, and the
+            // buffer of the step before this one is free: its reads have all been used by products
+            all_loads_over();
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            load_turn((d + D - 1) % D);
+            load_turn((d + 1) % D);
             auto read_x = [&](int i) { // the i-th of the step's reads
                 const int row = 32 * (i % TM) + n;
                 return xbuf[d][row * U + ((8 * h + i / TM) ^ (n & 15))];
@@ -876,13 +890,20 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
                 }
         }
     all_loads_over();
+    if constexpr (BOTH == 2) {
+#pragma unroll
+        for (int i = 0; i < XM; ++i)
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                acc[i][t] = acc[XM + i][t] + acc[i][t];
+    }
 
     // a lane's results: of row m of y 16 neighbouring columns for each tile
     constexpr int TC = TN / NW; // tiles of a weight
     if (p.splits > 1) { // partial sums as they lie in the registers: four a lane, the lanes' in order
-        f32x4* to = partials_of(a, p) + ((size_t)blockIdx.z * all + id) * (WN * TM * TN * 4 * 64) + (size_t)wave * (TM * TN * 4 * 64) + lane;
+        f32x4* to = partials_of(a, p) + ((size_t)blockIdx.z * all + id) * (WN * XM * TN * 4 * 64) + (size_t)wave * (XM * TN * 4 * 64) + lane;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
+        for (int i = 0; i < XM; ++i) {
             if (32 * i + n >= rows)
                 break;
 #pragma unroll
@@ -896,7 +917,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
         return;
     }
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    for (int i = 0; i < XM; ++i) {
         const int64_t m = m0 + 32 * i + n;
         if (m >= a.m)
             continue;
@@ -925,18 +946,19 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 
 // The sums of all splits, in order, and the results: a workgroup for the partial sums of 32 rows
 // of x and 32 of each weight, a wave for a quarter of the columns, whose lanes have what
-// the lanes that left them had.
-template <Kind KIND, int NW, int TM>
+// the lanes that left them had: all reads are of whole lines, in the order they were written.
+// 2 to 16 splits of up to 509 x 4096 results: 4 to 7 us.
+template <Kind KIND, int NW, int XM>
 __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const MatmulPlan p)
 {
-    constexpr int TC = TN / NW, WC = 32 * TC, BM = 32 * TM, BN = WC * WN;
+    constexpr int TC = TN / NW, WC = 32 * TC, BM = 32 * XM, BN = WC * WN;
     const uint32_t tiles_m = (uint32_t)((a.m + BM - 1) / BM), tiles_n = (uint32_t)((a.n + BN - 1) / BN), all = tiles_m * tiles_n;
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, n = lane & 31, h = lane >> 5;
     uint32_t rest = blockIdx.x;
     const uint32_t t = rest % TC;
     rest /= TC;
-    const uint32_t i = rest % TM;
-    rest /= TM;
+    const uint32_t i = rest % XM;
+    rest /= XM;
     const uint32_t wave = rest % WN, id = rest / WN;
     uint32_t row, col;
     tile_of(id, tiles_m, tiles_n, row, col);
@@ -946,10 +968,10 @@ __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const Mat
     f32x4 sum[NW];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const f32x4* from = partials_of(a, p) + (size_t)id * (WN * TM * TN * 256) + wave * (TM * TN * 256) + ((i * TN + w * TC + t) * 4 + q) * 64 + lane;
+        const f32x4* from = partials_of(a, p) + (size_t)id * (WN * XM * TN * 256) + wave * (XM * TN * 256) + ((i * TN + w * TC + t) * 4 + q) * 64 + lane;
         sum[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < p.splits; ++s)
-            sum[w] += from[(size_t)s * all * (WN * TM * TN * 256)];
+            sum[w] += from[(size_t)s * all * (WN * XM * TN * 256)];
     }
     store4(a, m, c, finish4<KIND, NW>(a, p, m, sum));
 }
@@ -984,28 +1006,37 @@ void few_form(const MatmulArgs& a, const MatmulPlan& p)
     }
 }
 
-template <Kind KIND, int NW, int TM>
+template <Kind KIND, int NW, int XM, int BOTH>
 void many_tiles(const MatmulArgs& a, const MatmulPlan& p)
 {
     const uint32_t tiles = (uint32_t)((a.n + p.rows - 1) / p.rows * ((a.m + p.tokens - 1) / p.tokens));
     const dim3 grid(tiles, 1, (uint32_t)p.splits);
     if (scales_together(a))
-        matmul_many<KIND, NW, TM, true><<<grid, 64 * WN, 0, a.stream>>>(a, p);
+        matmul_many<KIND, NW, XM * BOTH, BOTH, true><<<grid, 64 * WN, 0, a.stream>>>(a, p);
     else
-        matmul_many<KIND, NW, TM, false><<<grid, 64 * WN, 0, a.stream>>>(a, p);
+        matmul_many<KIND, NW, XM * BOTH, BOTH, false><<<grid, 64 * WN, 0, a.stream>>>(a, p);
     if (p.splits > 1)
-        matmul_join<KIND, NW, TM><<<tiles * (WN * TM * TN / NW), 256, 0, a.stream>>>(a, p);
+        matmul_join<KIND, NW, XM><<<tiles * (WN * XM * TN / NW), 256, 0, a.stream>>>(a, p);
 }
 
 template <Kind KIND, int NW>
 void many_form(const MatmulArgs& a, const MatmulPlan& p)
 {
+    if constexpr (KIND != kNvBf16) { // whose x has one part
+        if (p.both) {
+            if (p.tokens == 32)
+                many_tiles<KIND, NW, 1, 2>(a, p);
+            else
+                many_tiles<KIND, NW, 2, 2>(a, p);
+            return;
+        }
+    }
     if (p.tokens == 32)
-        many_tiles<KIND, NW, 1>(a, p);
+        many_tiles<KIND, NW, 1, 1>(a, p);
     else if (p.tokens == 64)
-        many_tiles<KIND, NW, 2>(a, p);
+        many_tiles<KIND, NW, 2, 1>(a, p);
     else
-        many_tiles<KIND, NW, 4>(a, p);
+        many_tiles<KIND, NW, 4, 1>(a, p);
 }
 
 } // namespace

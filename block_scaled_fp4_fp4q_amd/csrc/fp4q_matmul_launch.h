@@ -42,6 +42,7 @@ struct MatmulPlan {
     int tokens;      // rows of x of a workgroup
     int waves_k;     // few: waves that share the long axis
     int chunk_steps; // few: steps whose x is held in LDS at once
+    bool both;       // many: two parts of x in each step (else a step for each part)
     int splits;      // many: workgroups that share a tile's long axis
     int split_steps; // many: steps of each
     size_t lds;      // few

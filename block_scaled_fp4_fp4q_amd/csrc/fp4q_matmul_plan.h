@@ -59,7 +59,9 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
         return p;
     }
     // Tiles of 32, 64 or 128 rows of x by 256 rows of weights, and splits of the long axis: what
-    // is least of a cost in us.  A compute unit works through its tiles' steps one
+    // is least of a cost in us.  Two parts of x are rows of the same step where a tile of twice
+    // the rows holds them (32 binary32 rows, 14336 x 4096, NVFP4, 22 us so and 26 a step for each
+    // part; 64 rotated ones, MXFP4, 30 and 32).  A compute unit works through its tiles' steps one
     // after the other whether one or two workgroups are there; a launch costs 6, joining 3
     // and the partial sums' way to memory and back (4 TB/s).  As measured against
     // it: 48 rows, 4096 x 14336, MXFP4, 64-row tiles in 1, 4, 8, 16, 32 splits 114, 37, 25, 21,
@@ -74,17 +76,20 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
         if (tiles_n > 0x7FFFFF / tiles_m)
             continue;
         const int64_t tiles = tiles_n * tiles_m;
-        const double turn = tokens == 32 ? 0.95 : (tokens == 64 ? 1.15 : 1.9);
+        const bool both = p.parts == 2 && tokens <= 64;
+        const int wide = both ? 2 * tokens : tokens; // rows of x, or of its parts, in a step
+        const double turn = (both ? 1 : p.parts) * (wide == 32 ? 0.95 : (wide == 64 ? 1.15 : 1.9));
         // more splits than fill the chip four times, or than give each two steps, cost more
         for (int64_t c = 1; c == 1 || (c <= steps / 2 && tiles * c <= 4 * kCus); ++c) {
             const int64_t each = (steps + c - 1) / c, splits = each == 0 ? 1 : (steps + each - 1) / each;
             const double mb = (double)tiles * splits * tokens * 256 * 4e-6;
-            const double us = 6.0 + (double)((tiles * splits + kCus - 1) / kCus) * each * p.parts * turn +
+            const double us = 6.0 + (double)((tiles * splits + kCus - 1) / kCus) * each * turn +
                               (splits > 1 ? 3.0 + mb * 2 / 4 : 0.0);
             if (best_tiles == 0 || us < best) {
                 best = us;
                 best_tiles = tiles;
                 p.tokens = tokens;
+                p.both = both;
                 p.splits = (int)splits;
                 p.split_steps = (int)each;
             }

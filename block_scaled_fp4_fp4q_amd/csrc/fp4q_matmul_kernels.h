@@ -451,7 +451,7 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     }
     const int s_row = MX ? (lane >> 1) & 15 : lane >> 2, s_dword = MX ? lane & 1 : lane & 3;
     uint32_t bytes[kStages][NW][NS];
-    const uint32_t c_place = lds_place(cbuf), s_place = lds_place(sbuf);
+    const uint32_t c_place = lds_place(cbuf), s_place = lds_place(sbuf), x_place = (uint32_t)(uintptr_t)(lds_void*)lds;
     auto load = [&](int step, int to) {
         asm volatile("" ::: "memory"); // the loads of two steps keep their order
         const int k = step * kFewStep;
@@ -507,17 +507,20 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
                 }
             }
         } else {
-            const int per = p.chunk_steps * U; // units of a row
-            const uint16_t* x = static_cast<const uint16_t*>(p.prepared ? a.workspace : a.x);
-            const int64_t row_of = p.prepared ? a.k : a.x_row;
-            for (int u = threadIdx.x; u < PARTS * mt * per; u += T) {
-                const int row = u / per, b = u - row * per; // rows of all parts in turn
-                const int k = from * kFewStep + b * 8;
-                u32x4 v = u32x4{0u, 0u, 0u, 0u};
-                if (k < cols)
-                    v = *reinterpret_cast<const u32x4*>(x + row * row_of + k);
-                lds[row * stride + b] = v;
+            // 64 units of a row a load, rows of all parts in turn
+            const int per = p.chunk_steps * U / 64, row_of = (int)(p.prepared ? a.k : a.x_row) * 2;
+            const u32x4 x = words_of(p.prepared ? a.workspace : a.x, (int64_t)(PARTS * mt - 1) * row_of + cols * 2);
+            int row = 0, c = wave;
+            for (;;) {
+                for (; c >= per; c -= per)
+                    ++row;
+                if (row >= PARTS * mt)
+                    break;
+                const int k = from * kFewStep + c * 512 + lane * 8;
+                load_to_lds<16>(x, x_place + (row * stride + c * 64) * 16, k * 2 | (k < cols ? 0 : kPast), row * row_of);
+                c += RW * KW;
             }
+            all_loads_over();
         }
     };
 

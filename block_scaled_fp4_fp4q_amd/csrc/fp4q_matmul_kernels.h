@@ -16,7 +16,7 @@
 // value): rotated bf16 in one part, 11 bits, 8 times finer than the rounding of a bf16
 // result; binary32 in two, 22 bits.  With MXFP4, whose weights f16 does not hold, they
 // are bf16: rotated bf16 in two, 16 bits, binary32 in three, which hold its 24 bits (down to
-// bf16's last bit, 2^-133).  At most four rows are cut into these by the workgroups
+// bf16's last bit, 2^-133).  The fewest rows are cut into these by the workgroups
 // themselves, with NVFP4 too.
 #pragma once
 

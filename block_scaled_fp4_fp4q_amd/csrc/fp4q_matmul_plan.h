@@ -10,7 +10,6 @@ namespace fp4q {
 // of a compute unit's 160
 constexpr size_t few_lds(int weights) { return weights == 2 ? 48 * 1024 : 68 * 1024; }
 constexpr int kFewRows = 16;          // rows of x that the kernel for few takes
-constexpr int kConvertRows = 4;       // of these, rows that its workgroups convert themselves
 constexpr int kFewWaves = 1536;       // waves that it is given at least, where the long axis can be shared
 
 inline size_t whole256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -20,11 +19,13 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
     MatmulPlan p{};
     p.splits = 1;
     p.many = a.m > kFewRows;
-    // x of bf16, not rotated, enters as it is.  Else the workgroups convert few rows on the way (a
-    // launch less: one rotated row, 14336 x 4096, takes 11.8 us so and 12.8 prepared), and
-    // more are prepared by a launch of their own (16 such rows: 34.7 and 18.1 us).
+    // x of bf16, not rotated, enters as it is.  Else the workgroups convert the fewest rows on the
+    // way, a launch less, and more are prepared by a launch of their own.  Rotated bf16, so and
+    // prepared, in us: NVFP4, 4096 x 4096, 1, 2, 4 rows 6.0 and 7.1, 6.2 and 7.2, 7.9 and 7.6; 14336 x
+    // 4096 12.4 and 11.5, 12.1 and 11.4, 13.8 and 11.7; 4096 x 14336 13.2 and 14.5, 16.6 and 15.2,
+    // 23.9 and 16.1; MXFP4, 14336 x 4096, 1, 4 rows 11.1 and 13.0, 11.5 and 13.5.
     const bool exact = a.bf16 && !a.rotate;
-    p.prepared = !exact && a.m > kConvertRows;
+    p.prepared = !exact && a.m > (a.mx ? 4 : 2);
     if (exact)
         p.parts = 1;
     else if (a.mx || !p.prepared)

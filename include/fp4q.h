@@ -477,7 +477,7 @@ typedef enum { FP4Q_ACT_SILU = 0, FP4Q_ACT_GELU = 1, FP4Q_ACT_GELU_TANH = 2 } fp
  *   workspace  fp4q_matmul_workspace_bytes() bytes, 256-byte aligned (NULL where
  *            that is 0).
  * Weights enter the products exactly, and so does bf16 x.  Rotated bf16 x (rotated in
- * binary32) and binary32 x enter them in 16 and 24 bits; with NVFP4 and more than 4
+ * binary32) and binary32 x enter them in 16 and 24 bits; with NVFP4 and more than 2
  * tokens in 11 and 22, of which a value loses what lies below 2^-39 of its row's
  * largest, and else what lies below 2^-134.  Sums are binary32, in an order that the sizes alone decide, and the
  * global scale is a factor of the sum.

@@ -129,7 +129,7 @@ def test_workspace_grows_as_the_parts_and_partial_sums(L, fmt, dtype):
                 rows = -(-tokens // tile) * tile
                 most = parts * tokens * k * 2 + tokens * 4 + 1024 + max(4 * 256 * tile, rows * 4) * 256 * 4 * 4
                 assert 0 <= got <= most
-                if tokens <= 4 or (exact and tokens <= 16):
+                if tokens <= 2 or (exact and tokens <= 16):
                     assert got == 0
 
 

@@ -52,3 +52,20 @@ def test_many_rows_of_the_weight(tokens):
     w.values, w.k = np.stack(rows), k
     y, tol = product64(w, x.cpu())
     close(got[:, at], y, rounded(y, tol, BF16))
+
+
+@pytest.mark.parametrize("tokens,dtype,rotate", [(1, BF16, False), (16, BF16, True), (20, torch.float32, False), (130, BF16, False),
+                                                 (130, BF16, True)])
+def test_the_longest_rows(tokens, dtype, rotate):
+    """2^22 columns, the most that there can be, of a weight whose scales differ along the row."""
+    n, k = 20, 1 << 22
+    rng = np.random.default_rng(4)
+    w = Made(rng, "nvfp4", n, 16, rotate, S=0.01)
+    w.codes, w.scales = rng.integers(0, 256, n * k // 2, dtype=np.uint8), rng.integers(40, 90, n * k // 16, dtype=np.uint8)
+    from oracle import ref
+    w.values, w.k = np.asarray(ref.dequantize(w.codes, w.scales, 0.01, n, k), np.float64).reshape(n, k), k
+    x = torch.randn(tokens, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).to(dtype)
+    got = B.matmul(w.handle(), x)
+    at = sorted({0, tokens // 2, tokens - 1})
+    y, tol = product64(w, x[at].cpu())
+    close(got[at], y, rounded(y, tol, dtype))

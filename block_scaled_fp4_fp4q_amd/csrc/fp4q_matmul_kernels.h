@@ -631,7 +631,8 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 // lane ends with 16 neighbouring columns.
 //   While the products of eight values run, the weights of the next eight are expanded; the
 // last ones' are those of the next step.  Two steps' x and codes are held or on their way, each
-// in a buffer and registers of its own.  (Loads three steps ahead changed nothing.)
+// in a buffer and registers of its own.  (Loads three steps ahead changed
+// nothing at any size, nor did x read from LDS four products ahead with TM = 1, 2.)
 //   Two parts of x (BOTH) are rows of one step, each with its own sums, joined at the end: W is
 // read and expanded once for both.  Else a part is a step of its own.
 //   Bound by several units at once.  8192 rows, 14336 x 4096, NVFP4 bf16, TM = 4: 831 us, 1157

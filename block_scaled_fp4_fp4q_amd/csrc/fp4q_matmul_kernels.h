@@ -390,7 +390,7 @@ __device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulP
 
 // ---- few rows of x ------------------------------------------------------------------
 //
-// A workgroup of RW x KW waves takes 16 RW rows of the weight (of each of two) and up to 16
+// A workgroup of RW x KW waves takes 16 RW rows of the weight (of each of two) and up to 16 XT
 // rows of x; RW waves share the rows, KW the long axis, 256 values a step.  W is the
 // first operand of 16x16x32 products: lane n + 16 g has the 32 bytes of row n that hold
 // values 64 g .. 64 g + 63 of a step and gives them to eight products, eight at a
@@ -408,7 +408,7 @@ __device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulP
 // were slower (10.1 -> 13.4 us).
 constexpr int kStages = 3;
 
-template <Kind KIND, int NW, int PARTS, bool CONV, int RW, int KW, bool ONE>
+template <Kind KIND, int NW, int PARTS, bool CONV, int XT, int RW, int KW, bool ONE>
 __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, const MatmulPlan p)
 {
     constexpr int B = KIND == kMxBf16 ? 32 : 16;
@@ -524,12 +524,14 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
         }
     };
 
-    f32x4 acc[NW];
+    f32x4 acc[NW][XT];
 #pragma unroll
-    for (int i = 0; i < NW; ++i)
-        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // this lane's row of x; lanes past the last repeat it
-    const int x_at = (r < mt ? r : mt - 1) * stride + 8 * g;
+    for (int i = 0; i < NW * XT; ++i)
+        acc[i / XT][i % XT] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    int x_at[XT]; // this lane's rows of x; lanes past the last repeat it
+#pragma unroll
+    for (int i = 0; i < XT; ++i)
+        x_at[i] = (16 * i + r < mt ? 16 * i + r : mt - 1) * stride + 8 * g;
 
     const int turns = p.chunk_steps / KW; // of this wave in a chunk
     const int all = (steps + KW - 1) / KW; // the same for every wave of the workgroup
@@ -547,7 +549,7 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
                 __syncthreads();
                 in_chunk = 0;
             }
-            const u32x4* x = lds + (in_chunk * KW + kw) * U + x_at;
+            const u32x4* x = lds + (in_chunk * KW + kw) * U;
             load(kw + KW * (i + kStages - 1), (d + kStages - 1) % kStages);
             // this step's loads have arrived; those of the later ones may still be on their way
             constexpr int STAY = (kStages - 1) * PER;
@@ -572,16 +574,20 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                u32x4 xv[PARTS];
+                u32x4 xv[XT][PARTS];
 #pragma unroll
-                for (int q = 0; q < PARTS; ++q)
-                    xv[q] = x[q * mt * stride + j];
+                for (int i = 0; i < XT; ++i)
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q)
+                        xv[i][q] = x[x_at[i] + q * mt * stride + j];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     const u32x4 wv = expand<KIND>(t[w].c[j >> 2][j & 3], factor_of<KIND>(word[w], j));
 #pragma unroll
                     for (int q = PARTS - 1; q >= 0; --q) // small parts first
-                        acc[w] = mfma16<KIND>(wv, xv[q], acc[w]);
+#pragma unroll
+                        for (int i = 0; i < XT; ++i)
+                            acc[w][i] = mfma16<KIND>(wv, xv[i][q], acc[w][i]);
                 }
             }
             asm volatile("" ::: "memory"); // the next load into this stage comes after these reads
@@ -595,11 +601,13 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
     f32x4* red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
     for (int w = 0; w < NW; ++w)
-        red[(wave * NW + w) * 64 + lane] = acc[w];
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+            red[((wave * NW + w) * XT + i) * 64 + lane] = acc[w][i];
     __syncthreads();
-    for (int u = threadIdx.x; u < RW * 64; u += T) {
-        const int l = u & 63, part = u >> 6;
-        const int64_t n = n0 + part * 16 + 4 * (l >> 4), m = l & 15;
+    for (int u = threadIdx.x; u < RW * XT * 64; u += T) {
+        const int l = u & 63, tile = (u >> 6) % XT, part = (u >> 6) / XT;
+        const int64_t n = n0 + part * 16 + 4 * (l >> 4), m = 16 * tile + (l & 15);
         if (n >= a.n || m >= a.m)
             continue;
         f32x4 sum[NW];
@@ -608,7 +616,7 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
             sum[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < KW; ++k)
-                sum[w] += red[((k * RW + part) * NW + w) * 64 + l];
+                sum[w] += red[(((k * RW + part) * NW + w) * XT + tile) * 64 + l];
         }
         store4(a, m, n, finish4<KIND, NW>(a, p, m, sum));
     }
@@ -991,7 +999,7 @@ inline bool scales_together(const MatmulArgs& a)
     return places % 4 == 0;
 }
 
-template <Kind KIND, int NW, int PARTS, bool CONV>
+template <Kind KIND, int NW, int PARTS, bool CONV, int XT = 1>
 void few_form(const MatmulArgs& a, const MatmulPlan& p)
 {
     const dim3 grid((uint32_t)((a.n + p.rows - 1) / p.rows));
@@ -999,9 +1007,9 @@ void few_form(const MatmulArgs& a, const MatmulPlan& p)
     switch (p.waves_k) {
 #define FP4Q_FEW(RW, KW)                                                                             \
     if (one)                                                                                         \
-        matmul_few<KIND, NW, PARTS, CONV, RW, KW, true><<<grid, 512, p.lds, a.stream>>>(a, p);       \
+        matmul_few<KIND, NW, PARTS, CONV, XT, RW, KW, true><<<grid, 512, p.lds, a.stream>>>(a, p);       \
     else                                                                                             \
-        matmul_few<KIND, NW, PARTS, CONV, RW, KW, false><<<grid, 512, p.lds, a.stream>>>(a, p);      \
+        matmul_few<KIND, NW, PARTS, CONV, XT, RW, KW, false><<<grid, 512, p.lds, a.stream>>>(a, p);      \
     break;
     case 2: FP4Q_FEW(4, 2)
     case 4: FP4Q_FEW(2, 4)

@@ -20,7 +20,12 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
         many_form<kMxBf16, NW>(a, p);
     } else {
         switch (p.parts) {
-        case 1: few_form<kMxBf16, NW, 1, false>(a, p); break;
+        case 1:
+            if (p.tokens == 32)
+                few_form<kMxBf16, NW, 1, false, 2>(a, p);
+            else
+                few_form<kMxBf16, NW, 1, false>(a, p);
+            break;
         case 2:
             if (p.prepared)
                 few_form<kMxBf16, NW, 2, false>(a, p);

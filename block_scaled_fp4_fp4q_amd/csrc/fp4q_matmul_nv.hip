@@ -21,13 +21,20 @@ hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
         else
             many_form<kNvBf16, NW>(a, p);
     } else if (p.prepared) {
-        if (p.parts == 1)
+        if (p.parts == 1 && p.tokens == 32)
+            few_form<kNvF16, NW, 1, false, 2>(a, p);
+        else if (p.parts == 1)
             few_form<kNvF16, NW, 1, false>(a, p);
         else
             few_form<kNvF16, NW, 2, false>(a, p);
     } else {
         switch (p.parts) {
-        case 1: few_form<kNvBf16, NW, 1, false>(a, p); break;
+        case 1:
+            if (p.tokens == 32)
+                few_form<kNvBf16, NW, 1, false, 2>(a, p);
+            else
+                few_form<kNvBf16, NW, 1, false>(a, p);
+            break;
         case 2: few_form<kNvBf16, NW, 2, true>(a, p); break;
         default: few_form<kNvBf16, NW, 3, true>(a, p); break;
         }

@@ -9,16 +9,39 @@ namespace fp4q {
 // LDS of x in a workgroup of few rows, beside the 54 KiB (two weights 108) of codes on their way,
 // of a compute unit's 160
 constexpr size_t few_lds(int weights) { return weights == 2 ? 48 * 1024 : 68 * 1024; }
-constexpr int kFewRows = 16;          // rows of x that the kernel for few takes
+constexpr int kFewRows = 16;          // rows of x that the kernel for few takes in one tile
 constexpr int kFewWaves = 1536;       // waves that it is given at least, where the long axis can be shared
 
 inline size_t whole256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Waves of a workgroup of few rows that share the long axis: as few as give the chip kFewWaves
+// waves (one token, 4096 x 4096: 2, 4 or 8 of them take 8.7, 6.0 and 4.7 us; 14336 x 4096
+// 10.0, 10.1 and 11.5), and as few as let a chunk of x, a step of each of them, fit.
+inline int few_waves_k(const MatmulArgs& a, int parts)
+{
+    const int64_t tiles = (a.n + 15) / 16;
+    int kw = tiles * 2 >= kFewWaves ? 2 : (tiles * 4 >= kFewWaves ? 4 : 8);
+    while (kw > 2 && (size_t)parts * a.m * (kw * kFewStep * 2 + 16) > few_lds(a.weights))
+        kw /= 2;
+    return kw;
+}
+
+// Whether the kernel for few rows takes them.  Up to 16 always.  Up to 32, in two tiles of 16, where
+// x, that every workgroup passes through its LDS, is small and one round of workgroups has
+// all weight rows; one part of x.  In us, so and by the kernel for many: NVFP4, 14336 x 4096, 17 and
+// 32 rows 13.9 and 17.0, 15.9 and 17.5; 4096 x 4096 9.3 and 13.0, 11.5 and 14.3; two weights of
+// 14336 x 4096 21.0 and 26.1, 27.4 and 26.7 (MXFP4 16.6 and 23.5, 23.0 and 24.3).  Outside:
+// 4096 x 14336 26.8 and 18.8, 34.4 and 19.4; 65536 x 4096 51.9 and 50.4, 60.9 and 51.0.
+inline bool takes_few(const MatmulArgs& a, int parts)
+{
+    return a.m <= kFewRows || (parts == 1 && a.m <= 2 * kFewRows && a.m * a.k <= 1 << 17 &&
+                               a.n <= (int64_t)kCus * 16 * (8 / few_waves_k(a, parts)));
+}
 
 inline MatmulPlan plan_of(const MatmulArgs& a)
 {
     MatmulPlan p{};
     p.splits = 1;
-    p.many = a.m > kFewRows;
     // x of bf16, not rotated, enters as it is.  Else the workgroups convert the fewest rows on the
     // way, a launch less, and more are prepared by a launch of their own.  Rotated bf16, so and
     // prepared, in us: NVFP4, 4096 x 4096, 1, 2, 4 rows 6.0 and 7.1, 6.2 and 7.2, 7.9 and 7.6; 14336 x
@@ -32,28 +55,23 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
         p.parts = a.bf16 ? 2 : 3; // in bf16
     else
         p.parts = a.bf16 ? 1 : 2; // in f16
+    p.many = !takes_few(a, p.parts);
     size_t at = p.prepared ? whole256((size_t)p.parts * a.m * a.k * 2) : 0;
     p.exponents = at;
     if (p.prepared && !a.mx)
         at = whole256(at + (size_t)a.m * 4);
     p.partials = at;
     if (!p.many) {
-        // Waves of a workgroup that share the long axis: as few as give the chip kFewWaves
-        // waves (one token, 4096 x 4096: 2, 4 or 8 of them take 8.7, 6.0 and 4.7 us; 14336 x 4096
-        // 10.0, 10.1 and 11.5).
-        const int64_t tiles = (a.n + 15) / 16;
-        int kw = tiles * 2 >= kFewWaves ? 2 : (tiles * 4 >= kFewWaves ? 4 : 8);
+        const int kw = few_waves_k(a, p.parts);
         const size_t row = (size_t)p.parts * a.m;
-        while (kw > 2 && row * (kw * kFewStep * 2 + 16) > few_lds(a.weights)) // a chunk is a step of each of them
-            kw /= 2;
         p.waves_k = kw;
         p.rows = 16 * (8 / kw);
-        p.tokens = 16;
+        p.tokens = a.m > kFewRows ? 32 : 16;
         const int steps = (int)((a.k + kFewStep - 1) / kFewStep);
         p.chunk_steps = (steps + kw - 1) / kw * kw;
         while (p.chunk_steps > kw && row * (p.chunk_steps * kFewStep * 2 + 16) > few_lds(a.weights))
             p.chunk_steps = (p.chunk_steps / 2 + kw - 1) / kw * kw;
-        const size_t x = row * (p.chunk_steps * kFewStep * 2 + 16), red = (size_t)8 * a.weights * 1024;
+        const size_t x = row * (p.chunk_steps * kFewStep * 2 + 16), red = (size_t)8 * a.weights * (p.tokens / 16) * 1024;
         p.lds = x > red ? x : red;
         p.workspace = at;
         p.refused = (a.n + p.rows - 1) / p.rows > 0x7FFFFF;

@@ -57,7 +57,7 @@ def gated64(w0, w1, x, act):
 
 
 @pytest.mark.parametrize("act", [B.FP4Q_ACT_SILU, B.FP4Q_ACT_GELU, B.FP4Q_ACT_GELU_TANH])
-@pytest.mark.parametrize("size", [(1, 16, 4), (3, 31, 9), (4, 20, 300), (16, 100, 36), (13, 40, 512), (33, 65, 12),
+@pytest.mark.parametrize("size", [(1, 16, 4), (3, 31, 9), (4, 20, 300), (16, 100, 36), (13, 40, 512), (20, 100, 36), (32, 257, 17), (33, 65, 12),
                                   (70, 130, 8), (300, 257, 17)], ids=str)
 @pytest.mark.parametrize("form", FORMS, ids=IDS)
 def test_gated(form, size, act):
@@ -113,7 +113,7 @@ def test_shapes_of_x():
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rotate", [False, True])
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
-@pytest.mark.parametrize("m", [3, 40, 300])
+@pytest.mark.parametrize("m", [3, 24, 40, 300])
 def test_values_that_are_not_finite_stay_in_their_row(m, fmt, rotate, dtype):
     rng = np.random.default_rng(m)
     w, x = Made(rng, fmt, 50, 160, rotate), rows_of_x(rng, m, 160, dtype)

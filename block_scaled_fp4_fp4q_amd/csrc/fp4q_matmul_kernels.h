@@ -5,19 +5,16 @@
 //
 // and, of two weights, act(x W0^T) * (x W1^T).  A code times its E4M3 scale has
 // at most six significant bits and lies in [2^-10, 2688], and a code times 2^e has two:
-// dequantized weights enter the matrix cores exactly, NVFP4 as bf16 or as f16,
-// MXFP4 as bf16, and so does x of bf16; the global scale is one binary32 factor of the sum.
+// dequantized weights enter the matrix cores exactly as bf16, and so does x of bf16; the
+// global scale is one binary32 factor of the sum.
 // A weight that is stored rotated is never rotated back: x W^T = (x H)(W H)^T with H
 // the orthonormal block Hadamard, so x is rotated, in binary32.
 //
-// Parts.  Where x is not exact in bf16 it is given as a sum of 16-bit parts, one matrix product
-// each.  With NVFP4 they are f16, after a power of two per row that brings its
-// largest value to [2^14, 2^15) (what falls below f16's range is under 2^-38 of that
-// value): rotated bf16 in one part, 11 bits, 8 times finer than the rounding of a bf16
-// result; binary32 in two, 22 bits.  With MXFP4, whose weights f16 does not hold, they
-// are bf16: rotated bf16 in two, 16 bits, binary32 in three, which hold its 24 bits (down to
-// bf16's last bit, 2^-133).  The fewest rows are cut into these by the workgroups
-// themselves, with NVFP4 too.
+// Parts.  Where x is not exact in bf16 (binary32, or rotated) it is given as a sum of three
+// bf16 parts, one matrix product each, which hold its 24 bits (down to bf16's last bit, 2^-133),
+// in every form and for any number of rows.  Fewer lose results: two parts, 16 bits, or f16
+// parts under a power of two for each row (one, 11 bits; two, 22, and what lies 2^-39 below the row's
+// largest value, which a weight of zero may meet) differ where sums cancel.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,44 +26,30 @@ namespace fp4q {
 namespace {
 
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// what the weights are, and enter the products as
-enum Kind { kNvBf16, kNvF16, kMxBf16 };
+enum Kind { kNv, kMx }; // the weights' format
 
-template <Kind KIND>
 __device__ __forceinline__ f32x4 mfma16(u32x4 x, u32x4 y, f32x4 c)
 {
-    if constexpr (KIND == kNvF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
 }
 
-template <Kind KIND>
 __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c)
 {
-    if constexpr (KIND == kNvF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b16x8, x), __builtin_bit_cast(b16x8, y), c, 0, 0, 0);
 }
 
 // ---- weights -------------------------------------------------------------------
 
-// Two codes of a word times their block's scale s.  The product has six bits: f16 holds it,
-// and cutting it from binary32 to bf16 loses nothing.  (Two codes cost about
-// 16 cycles of a SIMD as bf16, 11 as f16, 7 for a power of two.)
+// Two codes of a word times their block's scale s.  The product has six bits: cutting it
+// from binary32 to bf16 loses nothing.  (Two codes cost about 16 cycles of a SIMD, 7 for a
+// power of two.)
 template <Kind KIND, int SEL>
 __device__ __forceinline__ uint32_t expand_pair(uint32_t w, float s)
 {
-    if constexpr (KIND == kMxBf16) {
+    if constexpr (KIND == kMx) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, SEL));
-    } else if constexpr (KIND == kNvF16) {
-        const f16x2 v = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL));
-        return __builtin_bit_cast(uint32_t, v * __builtin_bit_cast(f16x2, s));
     } else {
         float a, b;
         fp4_unpack2<SEL>(w, a, b);
@@ -86,7 +69,7 @@ __device__ __forceinline__ u32x4 expand(uint32_t w, float s)
 // them before.
 template <Kind KIND, bool ONE>
 struct Wide {
-    static constexpr int NS = ONE ? 1 : (KIND == kMxBf16 ? 2 : 4);
+    static constexpr int NS = ONE ? 1 : (KIND == kMx ? 2 : 4);
     u32x4 c[2];
     uint32_t s[NS];
 };
@@ -96,25 +79,19 @@ __device__ __forceinline__ uint32_t scale_word(const Wide<KIND, ONE>& w)
 {
     if constexpr (ONE)
         return w.s[0];
-    else if constexpr (KIND == kMxBf16)
+    else if constexpr (KIND == kMx)
         return w.s[0] | (w.s[1] << 8);
     else
         return w.s[0] | (w.s[1] << 8) | (w.s[2] << 16) | (w.s[3] << 24);
 }
 
-// The factor of values 8 j .. 8 j + 7 of 64: the value of their E4M3 byte in binary32 or
-// twice in f16, or the power of two of their E8M0 byte, whose exponent alone the conversions
-// apply (255 stands for NaN).
+// The factor of values 8 j .. 8 j + 7 of 64: the value of their E4M3 byte, or the power of
+// two of their E8M0 byte, whose exponent alone the conversions apply (255 stands for NaN).
 template <Kind KIND>
 __device__ __forceinline__ float factor_of(uint32_t word, int j)
 {
-    if constexpr (KIND == kMxBf16) {
+    if constexpr (KIND == kMx) {
         return __uint_as_float((j < 4 ? word & 0xFFu : word >> 8) << 23);
-    } else if constexpr (KIND == kNvF16) {
-        const f16x2 t = __builtin_bit_cast(f16x2, j < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false)
-                                                        : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true));
-        const _Float16 one = t[(j >> 1) & 1];
-        return __builtin_bit_cast(float, f16x2{one, one});
     } else {
         const auto t = j < 4 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, false)
                              : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, 1.0f, true);
@@ -177,14 +154,14 @@ template <Kind KIND, bool ONE>
 __device__ __forceinline__ Wide<KIND, ONE> load_wide(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, int c_at, int s_at,
                                                      int c_to, int s_to, int k, int cols)
 {
-    constexpr int B = KIND == kMxBf16 ? 32 : 16;
+    constexpr int B = KIND == kMx ? 32 : 16;
     Wide<KIND, ONE> t;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
         t.c[c] = __builtin_amdgcn_raw_buffer_load_b128(codes, (c_at + 16 * c) | (k < cols - 32 * c ? 0 : kPast), c_to, 0);
     if constexpr (ONE) {
         const int past = k < cols ? 0 : kPast;
-        t.s[0] = KIND == kMxBf16 ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales, s_at | past, s_to, 0)
+        t.s[0] = KIND == kMx ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales, s_at | past, s_to, 0)
                                  : __builtin_amdgcn_raw_buffer_load_b32(scales, s_at | past, s_to, 0);
     } else {
 #pragma unroll
@@ -196,30 +173,19 @@ __device__ __forceinline__ Wide<KIND, ONE> load_wide(__amdgpu_buffer_rsrc_t code
 
 // ---- activations ------------------------------------------------------------------
 
-// x as a sum of PARTS bf16 values, their bits in the upper halves of h: cut, the
-// remainder cut again, and for the last part rounded to nearest even (with three
-// parts it is exact).  A value that is not finite is its first part alone.
-template <int PARTS>
+constexpr int kParts = 3; // of x that is not exact in bf16
+
+// x as a sum of three bf16 values, their bits in the upper halves of h: cut, the remainder
+// cut again, and the last part rounded to nearest even (exact but for what lies below
+// 2^-133).  A value that is not finite is its first part alone.
 __device__ __forceinline__ void parts_of(float x, uint32_t* h)
 {
     const bool finite = __builtin_fabsf(x) < __builtin_huge_valf();
     h[0] = finite ? __float_as_uint(x) & 0xFFFF0000u : f32_to_bf16(x) << 16;
     float rest = finite ? x - __uint_as_float(h[0]) : 0.0f;
-    if constexpr (PARTS == 3) {
-        h[1] = __float_as_uint(rest) & 0xFFFF0000u;
-        rest -= __uint_as_float(h[1]);
-    }
-    h[PARTS - 1] = f32_to_bf16(rest) << 16;
-}
-
-// the same in f16, of values below 2^15, in the lower halves
-template <int PARTS>
-__device__ __forceinline__ void halves_of(float x, uint32_t* h)
-{
-    const _Float16 first = (_Float16)x;
-    h[0] = __builtin_bit_cast(uint16_t, first);
-    if constexpr (PARTS == 2)
-        h[1] = __builtin_bit_cast(uint16_t, (_Float16)(__builtin_fabsf(x) < __builtin_huge_valf() ? x - (float)first : 0.0f));
+    h[1] = __float_as_uint(rest) & 0xFFFF0000u;
+    rest -= __uint_as_float(h[1]);
+    h[2] = f32_to_bf16(rest) << 16;
 }
 
 // the B values of a block of x, widened and rotated
@@ -235,12 +201,24 @@ __device__ __forceinline__ void load_x(const MatmulArgs& a, int64_t row, int64_t
         fwht<B>(v);
 }
 
-// The bf16 parts of x, for MXFP4: [part][m][k] in the workspace, a block of values a
-// thread.  Moves x once; 37 rows of 4064: 5 us, a launch's latency.
-template <int PARTS>
+// eight values in parts, as they lie in memory
+__device__ __forceinline__ void parts_of8(const float* v, u32x4* to)
+{
+    uint32_t h[8][kParts];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        parts_of(v[j], h[j]);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+        to[q] = u32x4{h[0][q] >> 16 | h[1][q], h[2][q] >> 16 | h[3][q], h[4][q] >> 16 | h[5][q], h[6][q] >> 16 | h[7][q]};
+}
+
+// The parts of x: [part][m][k] in the workspace, a block of values a thread.  Moves x once;
+// 37 rows of 4064: 5 us, a launch's latency.
+template <Kind KIND>
 __global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
 {
-    constexpr int B = 32;
+    constexpr int B = KIND == kMx ? 32 : 16;
     const int64_t blocks = a.k / B, all = a.m * blocks, plane = a.m * a.k;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
         const int64_t row = u / blocks, b = u - row * blocks;
@@ -249,63 +227,11 @@ __global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
         uint16_t* to = static_cast<uint16_t*>(a.workspace) + u * B;
 #pragma unroll
         for (int i = 0; i < B / 8; ++i) {
-            uint32_t h[8][PARTS];
+            u32x4 part[kParts];
+            parts_of8(v + 8 * i, part);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                parts_of<PARTS>(v[8 * i + j], h[j]);
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q)
-                *reinterpret_cast<u32x4*>(to + q * plane + 8 * i) =
-                    u32x4{h[0][q] >> 16 | h[1][q], h[2][q] >> 16 | h[3][q], h[4][q] >> 16 | h[5][q], h[6][q] >> 16 | h[7][q]};
-        }
-    }
-}
-
-// The f16 parts of x, for NVFP4: [part][m][k] in the workspace, and behind them each row's
-// exponent (what its values were multiplied by is 2^exponent).  A workgroup has a row:
-// its largest finite value first, then the parts; blocks that a thread does not hold
-// itself it reads again, from cache.  Moves x once; 509 rows of 4096: 5 us, a launch's
-// latency.
-template <int PARTS>
-__global__ __launch_bounds__(256) void matmul_halves(const MatmulArgs a, const MatmulPlan p)
-{
-    constexpr int B = 16;
-    __shared__ float most[4];
-    const int64_t row = (int64_t)blockIdx.y * 65536 + blockIdx.x;
-    if (row >= a.m)
-        return;
-    const int blocks = (int)(a.k / B);
-    float v[B], top = 0.0f;
-    for (int b = threadIdx.x; b < blocks; b += 256) {
-        load_x<B>(a, row, (int64_t)b * B, v);
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const float x = __builtin_fabsf(v[i]);
-            top = x < __builtin_huge_valf() ? __builtin_fmaxf(top, x) : top;
-        }
-    }
-    top = wave_max(top);
-    if ((threadIdx.x & 63) == 0)
-        most[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = __builtin_fmaxf(__builtin_fmaxf(most[0], most[1]), __builtin_fmaxf(most[2], most[3]));
-    const int up = top > 0.0f ? 141 - (int)(__float_as_uint(top) >> 23) : 0; // to [2^14, 2^15)
-    if (threadIdx.x == 0)
-        reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + p.exponents)[row] = up;
-    for (int b = threadIdx.x; b < blocks; b += 256) {
-        if (blocks > 256)
-            load_x<B>(a, row, (int64_t)b * B, v);
-        uint16_t* to = static_cast<uint16_t*>(a.workspace) + row * a.k + (int64_t)b * B;
-#pragma unroll
-        for (int i = 0; i < B / 8; ++i) {
-            uint32_t h[8][PARTS];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                halves_of<PARTS>(__builtin_ldexpf(v[8 * i + j], up), h[j]);
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q)
-                *reinterpret_cast<u32x4*>(to + q * a.m * a.k + 8 * i) =
-                    u32x4{h[0][q] | h[1][q] << 16, h[2][q] | h[3][q] << 16, h[4][q] | h[5][q] << 16, h[6][q] | h[7][q] << 16};
+            for (int q = 0; q < kParts; ++q)
+                *reinterpret_cast<u32x4*>(to + q * plane + 8 * i) = part[q];
         }
     }
 }
@@ -344,19 +270,11 @@ __device__ __forceinline__ void store4(const MatmulArgs& a, int64_t m, int64_t n
         }
 }
 
-// y's values from the sums of one weight, or of two, of row m
+// y's values from the sums of one weight, or of two
 template <Kind KIND, int NW>
-__device__ __forceinline__ f32x4 finish4(const MatmulArgs& a, const MatmulPlan& p, int64_t m, f32x4* sum)
+__device__ __forceinline__ f32x4 finish4(const MatmulArgs& a, f32x4* sum)
 {
-    if constexpr (KIND == kNvF16) {
-        const int up = reinterpret_cast<const int32_t*>(static_cast<const char*>(a.workspace) + p.exponents)[m];
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sum[w][i] = __builtin_ldexpf(sum[w][i], -up);
-    }
-    if constexpr (KIND != kMxBf16) {
+    if constexpr (KIND != kMx) {
 #pragma unroll
         for (int w = 0; w < NW; ++w)
             sum[w] *= *a.global[w];
@@ -399,7 +317,7 @@ __device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulP
 // and read from there (each wave its own: no barrier; 16-byte units are exchanged by an XOR
 // with the row, so that 16 rows' meet all banks).  kStages steps are held or on their way.
 // x comes from LDS too, where the whole workgroup put it (CONV: rotated and cut into bf16
-// parts on the way; else as it is, or as matmul_parts and matmul_halves left it).
+// parts on the way; else as it is, or as matmul_parts left it).
 //   Bound by latency for small weights (one token, 4096 x 4096, NVFP4: 4.7 us in a graph) and by the vector ALU's expansion and the conversion of x in every
 // workgroup for wide ones: 14336 x 4096, NVFP4, one token 9.8 us, 3.4 TB/s of weights, MXFP4 7.5;
 // 16 tokens, whose x of 128 KiB each workgroup takes to its LDS, 14.9.  Scale bytes come four
@@ -411,11 +329,11 @@ constexpr int kStages = 3;
 template <Kind KIND, int NW, int PARTS, bool CONV, int XT, int RW, int KW, bool ONE>
 __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, const MatmulPlan p)
 {
-    constexpr int B = KIND == kMxBf16 ? 32 : 16;
+    constexpr int B = KIND == kMx ? 32 : 16;
     constexpr int T = 64 * RW * KW;
     constexpr int U = kFewStep / 8; // 16-byte units of x in a step
     constexpr int NS = Wide<KIND, ONE>::NS;
-    constexpr bool MX = KIND == kMxBf16;
+    constexpr bool MX = KIND == kMx;
     extern __shared__ u32x4 lds[];
     __shared__ u32x4 cbuf[RW * KW][kStages][NW][16 * 8]; // by wave
     __shared__ uint32_t sbuf[RW * KW][kStages][NW][ONE ? 64 : 1];
@@ -496,14 +414,11 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
                 }
 #pragma unroll
                 for (int i = 0; i < B / 8; ++i) {
-                    uint32_t h[8][PARTS];
+                    u32x4 part[kParts];
+                    parts_of8(v + 8 * i, part);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        parts_of<PARTS>(v[8 * i + j], h[j]);
-#pragma unroll
-                    for (int q = 0; q < PARTS; ++q)
-                        to[q * mt * stride + i] =
-                            u32x4{h[0][q] >> 16 | h[1][q], h[2][q] >> 16 | h[3][q], h[4][q] >> 16 | h[5][q], h[6][q] >> 16 | h[7][q]};
+                    for (int q = 0; q < kParts; ++q)
+                        to[q * mt * stride + i] = part[q];
                 }
             }
         } else {
@@ -587,7 +502,7 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
                     for (int q = PARTS - 1; q >= 0; --q) // small parts first
 #pragma unroll
                         for (int i = 0; i < XT; ++i)
-                            acc[w][i] = mfma16<KIND>(wv, xv[i][q], acc[w][i]);
+                            acc[w][i] = mfma16(wv, xv[i][q], acc[w][i]);
                 }
             }
             asm volatile("" ::: "memory"); // the next load into this stage comes after these reads
@@ -618,7 +533,7 @@ __global__ __launch_bounds__(64 * RW * KW) void matmul_few(const MatmulArgs a, c
             for (int k = 0; k < KW; ++k)
                 sum[w] += red[(((k * RW + part) * NW + w) * XT + tile) * 64 + l];
         }
-        store4(a, m, n, finish4<KIND, NW>(a, p, m, sum));
+        store4(a, m, n, finish4<KIND, NW>(a, sum));
     }
 }
 
@@ -641,8 +556,8 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 // last ones' are those of the next step.  Two steps' x and codes are held or on their way, each
 // in a buffer and registers of its own.  (Loads three steps ahead changed
 // nothing at any size, nor did x read from LDS four products ahead with TM = 1, 2.)
-//   Two parts of x (BOTH) are rows of one step, each with its own sums, joined at the end: W is
-// read and expanded once for both.  Else a part is a step of its own.
+//   The parts of x are rows of one step (PARTS = 3), so that W is read and expanded once for
+// them, where a tile has 32 rows; else a part is a step of its own.
 //   Bound by several units at once.  8192 rows, 14336 x 4096, NVFP4 bf16, TM = 4: 831 us, 1157
 // TFLOP/s; of a SIMD's cycles the matrix cores are busy in 56 of 100 and the vector ALU, which
 // expands, in 43, LDS gives x to a CU at 64 bytes a clock and each 16 bytes of a lane feed
@@ -665,17 +580,17 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
     n = __builtin_amdgcn_readfirstlane(in / high);
 }
 
-template <Kind KIND, int NW, int TM, int BOTH, bool ONE>
+template <Kind KIND, int NW, int XM, int PARTS, bool ONE>
 __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, const MatmulPlan p)
 {
-    constexpr int B = KIND == kMxBf16 ? 32 : 16;
-    constexpr int XM = TM / BOTH;    // products of 32 rows of x
+    constexpr int B = KIND == kMx ? 32 : 16;
+    constexpr int TM = XM * PARTS;   // products of 32 rows of x or of its parts in a step
     constexpr int BM = 32 * XM;
     constexpr int D = 2;             // steps held
     constexpr int WC = 32 * TN / NW; // columns of y of a wave
     constexpr int BN = WC * WN;
     constexpr int U = kStepK / 8;    // 16-byte units of a row of x
-    constexpr bool MX = KIND == kMxBf16;
+    constexpr bool MX = KIND == kMx;
     constexpr bool STAGED = TM <= 2;     // codes through LDS
     constexpr int NS = Wide<KIND, ONE>::NS;
     __shared__ u32x4 xbuf[D][32 * TM * U];
@@ -700,7 +615,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     const int steps = (cols + kStepK - 1) / kStepK;
     const int s0 = (int)blockIdx.z * p.split_steps;
     const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
-    const int parts = BOTH == 2 ? 1 : p.parts;
+    const int parts = PARTS == 1 ? p.parts : 1;
     const int turns = (s1 - s0) * parts; // a step for each part of x, the small ones first
     // Offsets are a lane's own (in a vector register) and a uniform part that never passes
     // the buffer's end, where the check against it would wrap: rows of a tile that do not
@@ -720,14 +635,12 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     for (int i = 0; i < KINDS; ++i)
         x_unit[i] = (lane & 15) ^ ((4 * (wave * LOADS + i) + quad) & 15);
     const uint32_t x_place = lds_place(xbuf), c_place = lds_place(cbuf), s_place = lds_place(sbuf);
-    const int second = BOTH == 2 ? wave / (WN / 2) : 0; // half of the waves load each part
     auto load_x_tile = [&](int step, int turn_part, bool real, int to) {
-        const int part = BOTH == 2 ? second : turn_part;
-        const u32x4 src = words_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
         const bool whole = (step + 1) * kStepK <= cols;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int row = (wave * LOADS + i) * 4 - second * BM;
+            const int place = (wave * LOADS + i) * 4, part = PARTS == 1 ? turn_part : place / BM, row = place - (PARTS == 1 ? 0 : part * BM);
+            const u32x4 src = words_of(x + part * plane, (int64_t)(rows - 1) * x_row + cols * 2);
             int at = (quad * x_row + x_unit[i % KINDS] * 16) | (real ? 0 : kPast);
             if (!whole) // values past the row's end are zeros
                 at |= step * kStepK + x_unit[i % KINDS] * 8 < cols ? 0 : kPast;
@@ -807,9 +720,9 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
     };
     static_assert(LOADS < 16, "what take_half waits for");
 
-    f32x16 acc[TM][TN];
+    f32x16 acc[XM][TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < XM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -873,7 +786,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
             asm volatile("" ::: "memory");
             load_turn((d + 1) % D);
             auto read_x = [&](int i) { // the i-th of the step's reads
-                const int row = 32 * (i % TM) + n;
+                const int row = 32 * (TM - 1 - i % TM) + n; // small parts first
                 return xbuf[d][row * U + ((8 * h + i / TM) ^ (n & 15))];
             };
             u32x4 xv[kReadAhead];
@@ -896,19 +809,14 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
                     for (int t = 0; t < TN; ++t) {
                         // the order of these is kept: a product, and what is expanded while it runs
                         __builtin_amdgcn_sched_barrier(0);
-                        acc[i][t] = mfma32<KIND>(wv[j & 1][t], mine, acc[i][t]);
-                        expand_pairs(ring[j < 7 ? d : (d + 1) % D], (j + 1) & 7, (TN * i + t) * (4 / TM), 4 / TM);
+                        f32x16& sum = acc[(TM - 1 - i) % XM][t];
+                        sum = mfma32(wv[j & 1][t], mine, sum);
+                        const int at = (TN * i + t) * 4 / TM, end = (TN * i + t + 1) * 4 / TM;
+                        expand_pairs(ring[j < 7 ? d : (d + 1) % D], (j + 1) & 7, at, end - at);
                     }
                 }
         }
     all_loads_over();
-    if constexpr (BOTH == 2) {
-#pragma unroll
-        for (int i = 0; i < XM; ++i)
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
-                acc[i][t] = acc[XM + i][t] + acc[i][t];
-    }
 
     // a lane's results: of row m of y 16 neighbouring columns for each tile
     constexpr int TC = TN / NW; // tiles of a weight
@@ -949,7 +857,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             sum[w][e] = acc[i][w * TC + t][4 * (q + o) + e];
-                    y[o] = finish4<KIND, NW>(a, p, m, sum);
+                    y[o] = finish4<KIND, NW>(a, sum);
                 }
                 store8(a, m, col, y[0], y[1]);
             }
@@ -985,7 +893,7 @@ __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const Mat
         for (int s = 0; s < p.splits; ++s)
             sum[w] += from[(size_t)s * all * (WN * XM * TN * 256)];
     }
-    store4(a, m, c, finish4<KIND, NW>(a, p, m, sum));
+    store4(a, m, c, finish4<KIND, NW>(a, sum));
 }
 
 // ---- launch -------------------------------------------------------------------------------
@@ -1018,37 +926,47 @@ void few_form(const MatmulArgs& a, const MatmulPlan& p)
     }
 }
 
-template <Kind KIND, int NW, int XM, int BOTH>
+template <Kind KIND, int NW, int XM, int PARTS>
 void many_tiles(const MatmulArgs& a, const MatmulPlan& p)
 {
     const uint32_t tiles = (uint32_t)((a.n + p.rows - 1) / p.rows * ((a.m + p.tokens - 1) / p.tokens));
     const dim3 grid(tiles, 1, (uint32_t)p.splits);
     if (scales_together(a))
-        matmul_many<KIND, NW, XM * BOTH, BOTH, true><<<grid, 64 * WN, 0, a.stream>>>(a, p);
+        matmul_many<KIND, NW, XM, PARTS, true><<<grid, 64 * WN, 0, a.stream>>>(a, p);
     else
-        matmul_many<KIND, NW, XM * BOTH, BOTH, false><<<grid, 64 * WN, 0, a.stream>>>(a, p);
+        matmul_many<KIND, NW, XM, PARTS, false><<<grid, 64 * WN, 0, a.stream>>>(a, p);
     if (p.splits > 1)
         matmul_join<KIND, NW, XM><<<tiles * (WN * XM * TN / NW), 256, 0, a.stream>>>(a, p);
 }
 
 template <Kind KIND, int NW>
-void many_form(const MatmulArgs& a, const MatmulPlan& p)
+hipError_t launch_weights(const MatmulArgs& a, const MatmulPlan& p)
 {
-    if constexpr (KIND != kNvBf16) { // whose x has one part
-        if (p.both) {
-            if (p.tokens == 32)
-                many_tiles<KIND, NW, 1, 2>(a, p);
-            else
-                many_tiles<KIND, NW, 2, 2>(a, p);
-            return;
-        }
+    if (p.prepared) {
+        const int64_t all = (a.m * (a.k / (KIND == kMx ? 32 : 16)) + 255) / 256;
+        const dim3 cover((uint32_t)(all < 1 ? 1 : (all < 65536 ? all : 65536)));
+        matmul_parts<KIND><<<cover, 256, 0, a.stream>>>(a);
     }
-    if (p.tokens == 32)
-        many_tiles<KIND, NW, 1, 1>(a, p);
-    else if (p.tokens == 64)
+    if (!p.many) {
+        if (p.parts == 1 && p.tokens == 32)
+            few_form<KIND, NW, 1, false, 2>(a, p);
+        else if (p.parts == 1)
+            few_form<KIND, NW, 1, false>(a, p);
+        else if (p.prepared)
+            few_form<KIND, NW, kParts, false>(a, p);
+        else
+            few_form<KIND, NW, kParts, true>(a, p);
+    } else if (p.tokens == 32) {
+        if (p.parts == 1)
+            many_tiles<KIND, NW, 1, 1>(a, p);
+        else
+            many_tiles<KIND, NW, 1, kParts>(a, p);
+    } else if (p.tokens == 64) {
         many_tiles<KIND, NW, 2, 1>(a, p);
-    else
+    } else {
         many_tiles<KIND, NW, 4, 1>(a, p);
+    }
+    return hipGetLastError();
 }
 
 } // namespace

@@ -35,18 +35,16 @@ constexpr int kCus = 256;
 // How one call is cut into workgroups, from its sizes and types alone.
 struct MatmulPlan {
     bool many;       // the kernel for many rows of x (else the one for few)
-    bool prepared;   // x is taken from the workspace, in 16-bit parts
+    bool prepared;   // x is taken from the workspace, in parts
     bool refused;    // more workgroups than a launch holds
-    int parts;       // 16-bit parts of x
+    int parts;       // bf16 parts of x: 1 or 3
     int rows;        // weight rows of a workgroup
     int tokens;      // rows of x of a workgroup
     int waves_k;     // few: waves that share the long axis
     int chunk_steps; // few: steps whose x is held in LDS at once
-    bool both;       // many: two parts of x in each step (else a step for each part)
     int splits;      // many: workgroups that share a tile's long axis
     int split_steps; // many: steps of each
     size_t lds;      // few
-    size_t exponents; // where the rows' exponents begin in the workspace (NVFP4, prepared)
     size_t partials;  // where the partial sums begin
     size_t workspace; // bytes
 };

@@ -476,11 +476,9 @@ typedef enum { FP4Q_ACT_SILU = 0, FP4Q_ACT_GELU = 1, FP4Q_ACT_GELU_TANH = 2 } fp
  *   y        of the same dtype, row stride in elements, at least `rows`.
  *   workspace  fp4q_matmul_workspace_bytes() bytes, 256-byte aligned (NULL where
  *            that is 0).
- * Weights enter the products exactly, and so does bf16 x.  Rotated bf16 x (rotated in
- * binary32) and binary32 x enter them in 16 and 24 bits; with NVFP4 and more than 2
- * tokens in 11 and 22, of which a value loses what lies below 2^-39 of its row's
- * largest, and else what lies below 2^-134.  Sums are binary32, in an order that the sizes alone decide, and the
- * global scale is a factor of the sum.
+ * Weights enter the products exactly, and so does x: rotated x (rotated in binary32) and
+ * binary32 x in all their 24 bits, but for what lies below 2^-134.  Sums are binary32, in an
+ * order that the sizes alone decide, and the global scale is a factor of the sum.
  * Precondition beside those above: sum_k |x_k w_k| / S (MXFP4: S = 1) is below
  * 2^127.  A row of x with values that are not finite gives what it gives in
  * its own row of y alone. */

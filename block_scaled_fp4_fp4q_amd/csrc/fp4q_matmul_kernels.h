@@ -242,8 +242,8 @@ __device__ __forceinline__ float activation(int act, float g)
 {
     if (act == kActSilu)
         return g / (1.0f + expf(-g));
-    if (act == kActGelu)
-        return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    if (act == kActGelu) // g Phi(g); 1 + erf(g / sqrt 2) would cancel below zero, all digits at -5.5
+        return 0.5f * g * erfcf(-g * 0.70710678118654752f);
     // 0.5 g (1 + tanh z) = g / (1 + exp(-2 z))
     const float z = 0.79788456080286536f * (g + 0.044715f * g * g * g);
     return g / (1.0f + expf(-2.0f * z));

@@ -921,7 +921,10 @@ void few_form(const MatmulArgs& a, const MatmulPlan& p)
     break;
     case 2: FP4Q_FEW(4, 2)
     case 4: FP4Q_FEW(2, 4)
-    default: FP4Q_FEW(1, 8)
+    default:
+        if constexpr (XT == 1) { // eight steps of more than 16 rows do not fit
+            FP4Q_FEW(1, 8)
+        }
 #undef FP4Q_FEW
     }
 }

@@ -16,11 +16,17 @@ inline size_t whole256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Waves of a workgroup of few rows that share the long axis: as few as give the chip kFewWaves
 // waves (one token, 4096 x 4096: 2, 4 or 8 of them take 8.7, 6.0 and 4.7 us; 14336 x 4096
-// 10.0, 10.1 and 11.5), and as few as let a chunk of x, a step of each of them, fit.
-inline int few_waves_k(const MatmulArgs& a, int parts)
+// 10.0, 10.1 and 11.5),
+inline int few_waves_wanted(const MatmulArgs& a)
 {
     const int64_t tiles = (a.n + 15) / 16;
-    int kw = tiles * 2 >= kFewWaves ? 2 : (tiles * 4 >= kFewWaves ? 4 : 8);
+    return tiles * 2 >= kFewWaves ? 2 : (tiles * 4 >= kFewWaves ? 4 : 8);
+}
+
+// and as few as let a chunk of x, a step of each of them, fit
+inline int few_waves_k(const MatmulArgs& a, int parts)
+{
+    int kw = few_waves_wanted(a);
     while (kw > 2 && (size_t)parts * a.m * (kw * kFewStep * 2 + 16) > few_lds(a.weights))
         kw /= 2;
     return kw;
@@ -38,11 +44,14 @@ inline int few_chunk(const MatmulArgs& a, int parts, int kw)
 
 // Whether the kernel for few rows takes them.
 // One part of x: up to 16 always.  Up to 32, in two tiles of 16, where x, that every workgroup
-// passes through its LDS, is small and one round of workgroups has all weight rows.  In us, so and
-// by the kernel for many: NVFP4, 14336 x 4096, 17 and 32 rows 13.9 and 17.0, 15.9 and 17.5;
-// 4096 x 4096 9.3 and 13.0, 11.5 and 14.3; two weights of 14336 x 4096 21.0 and 26.1, 27.4 and
-// 26.7 (MXFP4 16.6 and 23.5, 23.0 and 24.3).  Outside: 4096 x 14336 26.8 and 18.8, 34.4 and 19.4;
-// 65536 x 4096 51.9 and 50.4, 60.9 and 51.0.
+// passes through its LDS, is small, one round of workgroups has all weight rows, and there are at
+// most four chunks (MXFP4, whose products are shorter: eight, by the waves wanted).  In us, so and by
+// the kernel for many: NVFP4, 14336 x 4096, 17 and 32 rows 13.5 and 16.5, 15.9 and 17.2; 4096 x 4096 9.3
+// and 12.6, 11.6 and 14.0; two weights of 14336 x 4096, 17, 20, 24, 32 rows, 4, 4, 8, 8 chunks, 20.9 and
+// 25.8, 21.5 and 25.9, 25.5 and 26.0, 27.3 and 26.5 (MXFP4 16.7 and 23.6, 17.2 and 23.8, 21.0 and 24.1,
+// 22.9 and 24.5); of 4096 x 4096, 20 and 24 rows, 4 and 8 chunks, 14.7 and 17.4, 23.8 and 17.9 (MXFP4,
+// by fewer waves than wanted, 12.3 and 16.3, 19.5 and 16.8).  Outside: 4096 x 14336 26.8 and 18.8, 34.4
+// and 19.4; 65536 x 4096 51.9 and 50.4, 60.9 and 51.0.
 // Three parts: up to 16 in less than eight chunks of x (two weights, of which the kernel for many
 // makes half-wide tiles: sixteen), each of which is waited for.  NVFP4, so and by the kernel for many: 14336 x
 // 4096, 8 and 16 rows, 4 and 8 chunks, 19.3 and 25.3, 27.6 and 25.8; 4096 x 4096, 4, 8 and 12 rows, 2,
@@ -51,10 +60,12 @@ inline int few_chunk(const MatmulArgs& a, int parts, int kw)
 inline bool takes_few(const MatmulArgs& a, int parts)
 {
     const int kw = few_waves_k(a, parts);
-    if (parts == 1)
-        return a.m <= kFewRows || (a.m <= 2 * kFewRows && a.m * a.k <= 1 << 17 && a.n <= (int64_t)kCus * 16 * (8 / kw));
     const int64_t steps = (a.k + kFewStep - 1) / kFewStep;
-    return a.m <= 2 || (a.m <= kFewRows && (steps == 0 || steps <= (8 * a.weights - 1) * (int64_t)few_chunk(a, parts, kw)));
+    auto within = [&](int64_t chunks) { return steps == 0 || steps <= chunks * few_chunk(a, parts, kw); };
+    if (parts == 1)
+        return a.m <= kFewRows || (a.m <= 2 * kFewRows && a.m * a.k <= 1 << 17 && a.n <= (int64_t)kCus * 16 * (8 / kw) &&
+                                   (within(4) || (a.mx && kw == few_waves_wanted(a) && within(8))));
+    return a.m <= 2 || (a.m <= kFewRows && within(8 * a.weights - 1));
 }
 
 inline MatmulPlan plan_of(const MatmulArgs& a)

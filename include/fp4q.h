@@ -479,6 +479,9 @@ typedef enum { FP4Q_ACT_SILU = 0, FP4Q_ACT_GELU = 1, FP4Q_ACT_GELU_TANH = 2 } fp
  * Weights enter the products exactly, and so does x: rotated x (rotated in binary32) and
  * binary32 x in all their 24 bits, but for what lies below 2^-134.  Sums are binary32, in an
  * order that the sizes alone decide, and the global scale is a factor of the sum.
+ * A product of more workgroups than a launch holds is refused (FP4Q_E_SHAPE; its
+ * workspace query gives 0, as that of any refused call): none is while ceil(rows / 64) *
+ * ceil(tokens / 32) is below 2^23.
  * Precondition beside those above: sum_k |x_k w_k| / S (MXFP4: S = 1) is below
  * 2^127.  A row of x with values that are not finite gives what it gives in
  * its own row of y alone. */

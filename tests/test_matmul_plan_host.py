@@ -1,4 +1,6 @@
 """How the products' calls are cut into workgroups, asked of the plan itself on the host (no GPU needed)."""
+import ctypes as C
+import os
 import shutil
 
 import pytest
@@ -25,3 +27,29 @@ MEASURED = [(2, 0, 0, 1, 4096, 4096, 20, "few"), (2, 0, 0, 1, 4096, 4096, 24, "m
 @pytest.mark.parametrize("case", MEASURED, ids=str)
 def test_the_faster_kernel_is_taken(exe, case):
     assert plans(exe, [case[:7]])[0].kernel == case[7]
+
+
+def test_no_call_within_the_stated_limit_is_refused(exe):
+    """ceil(rows / 64) * ceil(tokens / 32) below 2^23, at its ends; beyond it some are, and ask for no workspace."""
+    forms = [(w, mx, rotate, bf16) for w in (1, 2) for mx in (0, 1) for rotate in (0, 1) for bf16 in (0, 1)]
+    most = (1 << 23) - 1
+    sizes = [(64 * most, 32, t) for t in (1, 2, 3, 16, 17, 32)] + [(64 * (most // 2), 4096, t) for t in (33, 64)]
+    sizes += [(64, 32, 32 * most), (1, 1 << 22, 32 * most), (64 * 2896, 64, 32 * 2896), (64 * 65, 32, 32 * (most // 65))]
+    assert not any(p.refused for p in plans(exe, [(*f, *s) for f in forms for s in sizes]))
+    beyond = plans(exe, [(*f, 1 << 36, 32, t) for f in forms for t in (1, 20, 500)])
+    assert all(p.refused for p in beyond)
+
+
+def test_refused_calls_say_so():
+    """Through the C ABI: the call's status, and no workspace asked for."""
+    from block_scaled_fp4_fp4q_amd import binding as B
+    if not os.path.exists(B.LIB_PATH):
+        pytest.skip("libfp4q.so not built")
+    L, s = B.lib(), B.make_spec(B.FP4Q_NVFP4)
+    w = B.fp4q_weight(1 << 20, 1 << 21, 1 << 22, 1 << 36, 32)
+    for tokens in (1, 20, 500):
+        assert L.fp4q_matmul_workspace_bytes(C.byref(s), C.byref(w), tokens, B.FP4Q_F32) == 0
+        assert L.fp4q_gated_workspace_bytes(C.byref(s), C.byref(w), tokens, B.FP4Q_F32) == 0
+        assert L.fp4q_matmul(C.byref(s), C.byref(w), 1 << 23, B.FP4Q_F32, tokens, 32, 1 << 24, 1 << 36, None, 0, None) == -3
+        assert L.fp4q_gated(C.byref(s), C.byref(w), C.byref(w), 0, 1 << 23, B.FP4Q_F32, tokens, 32, 1 << 24, 1 << 36, None, 0,
+                            None) == -3

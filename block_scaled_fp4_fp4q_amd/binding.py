@@ -719,7 +719,8 @@ def kv_append(cache, k, v, slots, q=None, positions=None, rope=None, interleaved
     positions    int64 [tokens], rows of the table; one out of range gives NaN in
                  q and is not written.
     interleaved  pairs are neighbours (2i, 2i + 1), not halves (i, i + rope_dim / 2).
-    out          like q, of any strides without expanded dimensions; may be q."""
+    out          like q, of any strides without expanded dimensions; may be q, and
+                 shares no element with q, k or v otherwise."""
     dev = cache.device
     if not _here(dev, stream):
         with _on(dev, stream):
@@ -1082,7 +1083,7 @@ def matmul(weight, x, out=None, workspace=None, stream=None):
     """x W^T for x float32 or bfloat16 [tokens, cols] (the last dimension
     contiguous; more or fewer leading dimensions if all are), W the values of
     the quantized weight [rows, cols]: [tokens, rows] of x's dtype.  out may
-    have any row stride.  Runs on torch's current stream of the weight's
+    have any row stride; it shares no element with x.  Runs on torch's current stream of the weight's
     device, or on `stream`, one of that device.  A given workspace (uint8,
     matmul_workspace_bytes) must not be shared by calls that may run at the
     same time."""

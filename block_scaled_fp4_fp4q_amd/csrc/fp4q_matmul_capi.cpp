@@ -19,6 +19,28 @@ constexpr int64_t kMostRows = (int64_t)1 << 36; // and a weight within 63 bits
 constexpr int64_t kMostStride = (int64_t)1 << 46;
 constexpr int64_t kMostRowStride = (int64_t)1 << 22; // of x
 
+// Whether a row of x and one of y share a byte: `rows` of each, strides and widths in bytes.
+bool share(uintptr_t x, int64_t x_step, int64_t x_wide, uintptr_t y, int64_t y_step, int64_t y_wide, int64_t rows)
+{
+    const int64_t apart = (int64_t)(y - x); // of the first rows
+    if (apart >= (rows - 1) * x_step + x_wide || -apart >= (rows - 1) * y_step + y_wide)
+        return false;
+    if (x_step == y_step && x_step >= x_wide && x_step >= y_wide) { // as two columns of one array
+        const int64_t at = ((apart % x_step) + x_step) % x_step;
+        return at < x_wide || at + y_wide > x_step;
+    }
+    for (int64_t i = 0; i < rows; ++i) {
+        const int64_t at = apart + i * y_step; // of y's row, from x's first one
+        if (at + y_wide <= 0)
+            continue;
+        int64_t row = x_step == 0 ? 0 : (at + y_wide - 1) / x_step; // the last one that begins before its end
+        row = row < rows ? row : rows - 1;
+        if (row * x_step + x_wide > at)
+            return true;
+    }
+    return false;
+}
+
 fp4q_status check_weight(const fp4q_spec* s, const fp4q_weight* w)
 {
     if (!s)
@@ -94,6 +116,9 @@ fp4q_status run(const fp4q_spec* spec, const fp4q_weight* const* w, int weights,
         return FP4Q_E_ALIGN;
     if (a.n == 0 || a.m == 0)
         return FP4Q_OK;
+    const int64_t size = a.bf16 ? 2 : 4;
+    if (a.k != 0 && share((uintptr_t)x, x_stride * size, a.k * size, (uintptr_t)y, y_stride * size, a.n * size, a.m))
+        return FP4Q_E_SHAPE; // x would be overwritten while it is read
     for (int i = 0; i < weights; ++i) {
         a.codes[i] = w[i]->codes;
         a.scales[i] = w[i]->scales;

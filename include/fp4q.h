@@ -331,8 +331,9 @@ fp4q_status fp4q_kv_write(const fp4q_spec* spec, const fp4q_kv_cache* cache, con
  * Members of the call:
  *   q, q_out [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim] of
  *            `dtype`, strides and alignment as for fp4q_kv_write; the rows of q_out
- *            share no element.  q_out may be q, with the same strides.  q_heads 0:
- *            no q (its members are ignored).
+ *            share no element.  q_out may be q, with the same strides; else its
+ *            rows share no element with those of q, k and v.  q_heads 0: no q (its
+ *            members are ignored).
  *   q_weight, k_weight  fp32 [head_dim], 16-byte aligned; NULL: no norm of these
  *            rows.  eps is positive where one is given.
  *   rope     fp32 [rope_rows, rope_dim], row stride in elements (a multiple of
@@ -473,7 +474,8 @@ typedef enum { FP4Q_ACT_SILU = 0, FP4Q_ACT_GELU = 1, FP4Q_ACT_GELU_TANH = 2 } fp
  * where it is stored rotated: x is rotated instead).
  *   x        dtype FP4Q_F32 or FP4Q_BF16, 16-byte aligned, row stride in
  *            elements, a multiple of 16 bytes and at most 2^22 elements.
- *   y        of the same dtype, row stride in elements, at least `rows`.
+ *   y        of the same dtype, row stride in elements, at least `rows`; its rows share
+ *            no element with those of x (FP4Q_E_SHAPE), nor memory with the others.
  *   workspace  fp4q_matmul_workspace_bytes() bytes, 256-byte aligned (NULL where
  *            that is 0).
  * Weights enter the products exactly, and so does x: rotated x (rotated in binary32) and

@@ -1012,14 +1012,27 @@ def _product_need(weights, tokens, code):
     return need
 
 
+def _same_weights(gate, up):
+    if (gate.rows, gate.cols, gate.spec.format, gate.spec.rotate, gate.device) != \
+            (up.rows, up.cols, up.spec.format, up.spec.rotate, up.device):
+        raise ValueError("gate and up must have the same sizes, format, rotation and device")
+
+
+def _type_code(dtype):
+    if dtype not in _X:
+        raise ValueError(f"dtype is {dtype}; expected {' or '.join(map(str, _X))}")
+    return FP4Q_BF16 if dtype == torch.bfloat16 else FP4Q_F32
+
+
 def matmul_workspace_bytes(weight, tokens, dtype=torch.bfloat16):
     """Bytes that `matmul` needs as its workspace for x [tokens, cols] of `dtype`."""
-    return _product_need((weight,), operator.index(tokens), FP4Q_BF16 if dtype == torch.bfloat16 else FP4Q_F32)
+    return _product_need((weight,), operator.index(tokens), _type_code(dtype))
 
 
 def gated_workspace_bytes(gate, up, tokens, dtype=torch.bfloat16):
     """Bytes that `gated` needs as its workspace for x [tokens, cols] of `dtype`."""
-    return _product_need((gate, up), operator.index(tokens), FP4Q_BF16 if dtype == torch.bfloat16 else FP4Q_F32)
+    _same_weights(gate, up)
+    return _product_need((gate, up), operator.index(tokens), _type_code(dtype))
 
 
 def _product_call(weights, x, out):
@@ -1097,9 +1110,7 @@ def gated(gate, up, x, activation=FP4Q_ACT_SILU, out=None, workspace=None, strea
     """act(x Wgate^T) * (x Wup^T), the first half of a gated feed-forward block,
     for two weights of the same sizes, format and rotation; `activation` is
     FP4Q_ACT_SILU, FP4Q_ACT_GELU or FP4Q_ACT_GELU_TANH.  Else as `matmul`."""
-    if (gate.rows, gate.cols, gate.spec.format, gate.spec.rotate, gate.device) != \
-            (up.rows, up.cols, up.spec.format, up.spec.rotate, up.device):
-        raise ValueError("gate and up must have the same sizes, format, rotation and device")
+    _same_weights(gate, up)
     if not _here(gate.device, stream):
         with _on(gate.device, stream, "weight"):
             return gated(gate, up, x, activation, out, workspace)

@@ -5,6 +5,7 @@ import shutil
 
 import pytest
 
+from matmul_forms import ONE_PART, THREE_PARTS, form
 from matmul_plans import compiled, plans
 
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
@@ -53,3 +54,19 @@ def test_refused_calls_say_so():
         assert L.fp4q_matmul(C.byref(s), C.byref(w), 1 << 23, B.FP4Q_F32, tokens, 32, 1 << 24, 1 << 36, None, 0, None) == -3
         assert L.fp4q_gated(C.byref(s), C.byref(w), C.byref(w), 0, 1 << 23, B.FP4Q_F32, tokens, 32, 1 << 24, 1 << 36, None, 0,
                             None) == -3
+
+
+def test_every_kernel_has_a_size_among_the_compared_ones(exe):
+    """The kernels that any of some 30,000 calls takes, and those of the sizes that are compared with 64 bits (matmul_forms)."""
+    rows = (1, 20, 100, 515, 1003, 2051, 4100, 6160, 8200, 12304, 16400, 33000, 70000, 200000)
+    cols = (32, 96, 256, 288, 512, 544, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 14336, 14368, 1 << 20)
+    tokens = (1, 2, 3, 4, 5, 8, 12, 16, 17, 20, 24, 32, 33, 48, 64, 65, 100, 128, 129, 200, 300, 512, 1000, 2000, 4096, 8192, 30000)
+
+    def taken(sizes):
+        return {form(c, p): c for c, p in zip(sizes, plans(exe, sizes)) if not p.refused}
+    some = taken([(w, mx, rotate, bf16, n, k, m) for w in (1, 2) for mx in (0, 1) for rotate, bf16 in ((0, 0), (0, 1), (1, 1))
+                  for n in rows for k in cols for m in tokens])
+    mine = taken([(w, mx, 0, bf16, *size) for w in (1, 2) for mx in (0, 1) for bf16, sizes in ((1, ONE_PART), (0, THREE_PARTS))
+                  for size in sizes])
+    assert not set(some) - set(mine), {f: some[f] for f in set(some) - set(mine)}
+    assert len(some) >= 160

@@ -638,9 +638,11 @@ def rope_table(length, rope_dim, base=10000.0, frequencies=None, factor=1.0, mag
 
 def rope_frequencies(rope_dim, base=10000.0, factor=1.0, original_length=None, fast=32.0, slow=1.0, device="cuda"):
     """Frequencies (binary64) for contexts `factor` times as long as the original
-    length: those that turn at least `fast` times over it stay, those that turn
-    at most `slow` times are divided by the factor, and those between are mixed
-    linearly in their index.  Without an original length all are divided."""
+    length, as YaRN has them (Peng et al., 2023, "NTK-by-parts", with its rounding
+    of the ramp's ends outwards): those that turn at least `fast` times over it stay,
+    those that turn at most `slow` times are divided by the factor, and those
+    between are mixed linearly in their index.  Without an original length all
+    are divided.  YaRN's factor of the logits is `magnitude` of rope_table."""
     f = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / rope_dim)
     if original_length is None:
         return f / factor

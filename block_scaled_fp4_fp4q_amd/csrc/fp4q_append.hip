@@ -194,7 +194,8 @@ __device__ __forceinline__ Share share_of(const AppendPlan& p)
 // The searching rules: a block a lane, whose 16 or 32 values stay in its registers.  Bound by
 // the vector ALU where many scales are tried (fp4q_kv.hip has the figures of the pick), by
 // latency for a decode step (64 tokens, 32 + 8 + 8 heads of 128 values, NVFP4, 11 scales,
-// rotated: 9.6 us).
+// rotated: 9.6 us).  8192 of those tokens, 92 us (AbsMax 54): q, whose rows are not searched, takes
+// a block a lane here too, which the other kernel has shown to be the slower layout.
 template <bool MX, int RULE, bool BF16, bool ROT>
 __global__ __launch_bounds__(kThreads) void kv_append_search(const KvAppendArgs a, const AppendPlan p)
 {

@@ -214,7 +214,7 @@ __device__ __forceinline__ void parts_of8(const float* v, u32x4* to)
 }
 
 // The parts of x: [part][m][k] in the workspace, a block of values a thread.  Moves x once;
-// 37 rows of 4064: 5 us, a launch's latency.
+// 37 rows of 4064: 5.6 us, a launch's latency; 509 of 4096: 9.
 template <Kind KIND>
 __global__ __launch_bounds__(256) void matmul_parts(const MatmulArgs a)
 {
@@ -318,12 +318,15 @@ __device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulP
 // with the row, so that 16 rows' meet all banks).  kStages steps are held or on their way.
 // x comes from LDS too, where the whole workgroup put it (CONV: rotated and cut into bf16
 // parts on the way; else as it is, or as matmul_parts left it).
-//   Bound by latency for small weights (one token, 4096 x 4096, NVFP4: 4.7 us in a graph) and by the vector ALU's expansion and the conversion of x in every
-// workgroup for wide ones: 14336 x 4096, NVFP4, one token 9.8 us, 3.4 TB/s of weights, MXFP4 7.5;
-// 16 tokens, whose x of 128 KiB each workgroup takes to its LDS, 14.9.  Scale bytes come four
-// at a time where every row allows it (two weights of 14336 x 4096, before other steps: 24 us; a
-// byte at a time 30).  Waves that begin at different steps, to spread the rows' lines over the memory's channels,
-// were slower (10.1 -> 13.4 us).
+//   Bound by latency for small weights (one token, 4096 x 4096, NVFP4: 4.5 us in a graph).  14336 x
+// 4096, NVFP4, in a graph: one token 10.5 us, 3.1 TB/s of weights (MXFP4 7.9); 16 tokens, whose x of
+// 128 KiB each workgroup takes to its LDS, 12.3; with weights that do not stay in the last-level
+// cache 11.7 and 12.6.  Of a compute unit's cycles there the vector ALU, which expands, is busy in 43
+// and 39 of 100, the matrix cores in 9 and 7, LDS in 14 and 19, and half of the waves' time is waiting (52 and 40
+// of 100): the two waves of a SIMD do not hide the loads behind the expansion.  Three parts of x: 8 tokens 19.5,
+// chunk after chunk waited for.  Scale bytes come four at a time where every row allows it (two
+// weights of 14336 x 4096, before other steps: 24 us; a byte at a time 30).  Waves that begin at
+// different steps, to spread the rows' lines over the memory's channels, were slower (10.1 -> 13.4 us).
 constexpr int kStages = 3;
 
 template <Kind KIND, int NW, int PARTS, bool CONV, int XT, int RW, int KW, bool ONE>
@@ -564,7 +567,13 @@ constexpr int kReadAhead = 2; // reads of x from LDS before their products
 // two products, and the clock is at 1.87 GHz under the power that this takes.  MXFP4, whose
 // codes take one instruction a pair, 774 to 823 us.  Products of 128 weight rows a wave would
 // halve the reads of x and spill registers (1240 us); 16x16x32 products spill too.  A step of a
-// workgroup costs its CU 0.95, 1.15, 1.9 us with TM = 1, 2, 4.
+// workgroup costs its CU 0.95, 1.15, 1.9 us with TM = 1, 2, 4.  Rotated x, in three parts: 2284 us, 1264
+// TFLOP/s of its products, the matrix cores busy in 74 of 100.
+//   Of few tiles, a wave a SIMD, none of these is near its rate, of 100 cycles: 64 rows, 14336 x 4096,
+// NVFP4, and 48 rows, 4096 x 14336, MXFP4 (XM = 2, 14 and 15 us beside the join): matrix cores 23 and
+// 23, vector ALU 32 and 15, LDS 8 and 8, waits 27 and 34, memory 3.6 and 3.9 TB/s with the partial
+// sums; 32 rows in three parts: 27, 26, 7 and 14.  A wave's products, expansion and waits follow
+// each other there.
 constexpr int WN = 4; // waves of a workgroup
 constexpr int TN = 2; // products of 32 weight rows in a wave
 
@@ -867,7 +876,7 @@ __global__ __launch_bounds__(64 * WN, 2) void matmul_many(const MatmulArgs a, co
 // The sums of all splits, in order, and the results: a workgroup for the partial sums of 32 rows
 // of x and 32 of each weight, a wave for a quarter of the columns, whose lanes have what
 // the lanes that left them had: all reads are of whole lines, in the order they were written.
-// 2 to 16 splits of up to 509 x 4096 results: 4 to 7 us.
+// 2 to 16 splits of up to 64 x 14336 results: 4 to 7 us.
 template <Kind KIND, int NW, int XM>
 __global__ __launch_bounds__(256) void matmul_join(const MatmulArgs a, const MatmulPlan p)
 {

@@ -100,7 +100,8 @@ inline MatmulPlan plan_of(const MatmulArgs& a)
     }
     // Tiles of 32, 64 or 128 rows of x by 256 rows of weights, and splits of the long axis: what
     // is least of a cost in us.  A compute unit works through its tiles' steps one after the other
-    // whether one or two workgroups are there; a launch costs 6, joining 3 and the partial sums'
+    // whether one or two workgroups are there (three parts in a tile of 32 take 2.1 us a step alone
+    // and 1.4 among several: 1.5 chose best); a launch costs 6, joining 3 and the partial sums'
     // way to memory and back (4 TB/s).  As measured against it: 48 rows, 4096 x 14336, MXFP4,
     // 64-row tiles in 1, 4, 8, 16, 32 splits 114, 37, 25, 21, 30 us; 8192 rows, 14336 x 4096, tiles of
     // 64 and 128 rows 1185 and 854.

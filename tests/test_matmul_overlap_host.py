@@ -32,7 +32,7 @@ OVER = [dict(y=X), dict(y=X + 4), dict(y=X - 4), dict(y=X + 40 * 1024 - 4), dict
         dict(y=X, xs=0), dict(y=X + 512, xs=0), dict(y=X - 39 * 4096 + 1000, xs=256, ys=1024),
         dict(y=X + 1024, xs=512, ys=1024 + 256), dict(y=X, n=8), dict(y=X + 800, n=8, ys=64, xs=512)]
 APART = [dict(y=X + 40 * 1024), dict(y=X - 40 * 1024), dict(y=X + 1024, xs=512, ys=512), dict(y=X - 1024, xs=512, ys=512),
-         dict(y=X + 3072, xs=512, ys=512), dict(y=X + 1024, xs=0), dict(y=X + 1024, xs=512, ys=1024),
+         dict(y=X + 5120, xs=512, ys=512), dict(y=X + 1024, xs=0), dict(y=X + 1024, xs=512, ys=1024),
          dict(y=X + 1024, n=8, xs=512, ys=512)]
 
 

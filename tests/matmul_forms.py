@@ -21,6 +21,7 @@ THREE_PARTS = [
     # many rows: tiles of 32 whose steps hold all parts, of 128 with a step for each
     (37, 256, 17), (301, 288, 33), (37, 768, 29), (37, 1056, 65), (12310, 256, 512), (6161, 288, 1001), (515, 256, 5000), (515, 288, 5000),
     (515, 2560, 3001), (515, 2592, 3001), (9001, 2560, 101), (9001, 2592, 101),
+    (2051, 256, 7001), (2051, 288, 7001), (515, 8192, 3001), (515, 8224, 3001), (301, 8192, 3001), (301, 8224, 3001),
 ]
 
 

@@ -22,6 +22,8 @@ MEASURED = [(2, 0, 0, 1, 4096, 4096, 20, "few"), (2, 0, 0, 1, 4096, 4096, 24, "m
             (2, 0, 0, 1, 14336, 4096, 20, "few"), (2, 0, 0, 1, 14336, 4096, 32, "many"), (2, 1, 0, 1, 14336, 4096, 32, "few"),
             (2, 0, 0, 1, 16384, 2048, 32, "few"), (1, 0, 0, 1, 14336, 4096, 32, "few"), (1, 0, 0, 1, 4096, 4096, 32, "few"),
             (1, 0, 0, 1, 4096, 14336, 17, "many"), (1, 0, 0, 0, 4096, 14336, 8, "many"), (1, 0, 0, 0, 4096, 14336, 4, "few"),
+            (1, 0, 1, 1, 28672, 8192, 6, "few"), (1, 0, 1, 1, 28672, 8192, 12, "many"), (1, 0, 1, 1, 8192, 8192, 6, "few"),
+            (2, 0, 1, 1, 1024, 4096, 12, "many"), (2, 1, 0, 0, 14336, 6144, 16, "few"), (1, 0, 1, 1, 1024, 4096, 6, "few"),
             (1, 0, 0, 0, 4096, 4096, 8, "few"), (1, 0, 0, 0, 4096, 4096, 16, "many"), (2, 0, 1, 1, 14336, 4096, 16, "few")]
 
 

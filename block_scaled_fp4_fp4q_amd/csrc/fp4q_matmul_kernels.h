@@ -322,11 +322,12 @@ __device__ __forceinline__ f32x4* partials_of(const MatmulArgs& a, const MatmulP
 // 4096, NVFP4, in a graph: one token 10.5 us, 3.1 TB/s of weights (MXFP4 7.9); 16 tokens, whose x of
 // 128 KiB each workgroup takes to its LDS, 12.3; with weights that do not stay in the last-level
 // cache 11.7 and 12.6.  Of a compute unit's cycles there the vector ALU, which expands, is busy in 43
-// and 39 of 100, the matrix cores in 9 and 7, LDS in 14 and 19, and half of the waves' time is waiting (52 and 40
-// of 100): the two waves of a SIMD do not hide the loads behind the expansion.  Three parts of x: 8 and 16 tokens 19.5 and 28.4,
-// chunk after chunk waited for.  Scale bytes come four at a time where every row allows it (two
-// weights of 14336 x 4096, before other steps: 24 us; a byte at a time 30).  Waves that begin at
-// different steps, to spread the rows' lines over the memory's channels, were slower (10.1 -> 13.4 us).
+// and 39 of 100, the matrix cores in 9 and 7, LDS in 14 and 19, and half of the waves' time is
+// waiting (52 and 40 of 100): the two waves of a SIMD do not hide the loads behind the expansion.
+// Three parts of x: 8 and 16 tokens 19.5 and 28.4, chunk after chunk waited for.  Scale bytes come
+// four at a time where every row allows it (two weights of 14336 x 4096, before other steps: 24 us;
+// a byte at a time 30).  Waves that begin at different steps, to spread the rows' lines over the
+// memory's channels, were slower (10.1 -> 13.4 us).
 constexpr int kStages = 3;
 
 template <Kind KIND, int NW, int PARTS, bool CONV, int XT, int RW, int KW, bool ONE>
